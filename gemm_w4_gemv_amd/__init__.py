@@ -547,3 +547,11 @@ def w4_repack_gptq(qweight, s_gn, z_gn, group: int = INT4_GROUP, stream=None):
     _check(lib.w4_repack_gptq(_dev(qweight, "qweight", _I32), _dev(s_gn, "s_gn", _F16), _dev(z_gn, "z_gn", _F16),
                               qw.data_ptr(), s.data_ptr(), z.data_ptr(), K, N, group, _stream(stream)), "w4_repack_gptq")
     return qw, s, z
+
+
+# The decode step's operators around the linears (include/w4_step.h); they
+# share the library handle and the error class above.
+from .step import *  # noqa: E402,F401,F403
+from .step import __all__ as _step_all  # noqa: E402
+
+__all__ += _step_all

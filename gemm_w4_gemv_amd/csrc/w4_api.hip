@@ -11,13 +11,14 @@
 #include "chain.hpp"
 #include "tune.hpp"
 #include "w4.h"
+#include "w4_check.hpp"
 #include "w4_internal.hpp"
 
 namespace {
-
 thread_local char g_last_error[256] = "no error";
+}  // namespace
 
-w4_status fail(w4_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace w4 {
 w4_status fail(w4_status st, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -25,21 +26,16 @@ w4_status fail(w4_status st, const char* fmt, ...) {
     va_end(ap);
     return st;
 }
+}  // namespace w4
 
-w4_status hip_fail(hipError_t err, const char* what) {
-    return fail(W4_ERR_HIP, "%s: %s (%d)", what, hipGetErrorString(err), (int)err);
-}
+namespace {
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-Range range(const void* p, size_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return {a, a + bytes};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
+using w4::aligned;
+using w4::fail;
+using w4::hip_fail;
+using w4::overlap;
+using w4::Range;
+using w4::range;
 
 // Shared checks of the INT4 weight operand and K.
 w4_status check_int4(const char* fn, const int32_t* qw, const void* s, const void* z, int K, int N,
