@@ -9,11 +9,10 @@
 //   outputs  O[d][r] = sum_t p s_t (q_td - 8) + sum_t p (m_t + 8 s_t)
 //
 // 128 + q is exact in BF16 and is one shift and one and-or per two codes.
-// In the outputs the 136 = 128 + 8 is taken off again by a second product
-// with a constant operand for each tile: left in until the end, the sums of
-// a long context would be 136 / 8 times larger than what they cancel to and
-// FP32 would lose it.  Those extra products are free: the vector unit, which
-// unpacks codes and makes the softmax, is the busier one.
+// In the outputs the 136 = 128 + 8 comes off as 136 times the sum of the
+// rounded weights, which one more product per group (with ones) keeps, every
+// few tiles: left in until the end, the sums of a long context would be
+// 136 / 8 times larger than what they cancel to and FP32 would lose it.
 //
 // Layout.  S = K Q^T puts a row's scores of tokens 4 g .. 4 g + 3 (g = lane / 16)
 // and 16 + 4 g .. in one lane (row = lane % 16), which is just the operand
@@ -22,17 +21,17 @@
 // its K words as 16 bytes of one token, and the values' layout (four tokens'
 // words of one place together) gives it its V words as 16 bytes too.
 //
-// A workgroup's four waves take a request's tiles in turn and join their
-// sums in LDS; a launch with few rows splits the tiles over workgroups too,
+// A workgroup's waves take a request's tiles in turn and join their sums in
+// LDS; a launch with few rows splits the tiles over workgroups too,
 // and a second kernel joins those.
+#include <type_traits>
+
 #include "kv4.hpp"
 #include "w4_device.hpp"
 
 namespace w4 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
 constexpr int kTile = 32;  // tokens
 
 struct AttnArgs {
@@ -77,6 +76,14 @@ __device__ __forceinline__ u32x4_t key_operand(uint32_t w, uint32_t bias) {
     return u32x4_t{p[0], p[1], p[2], p[3]};
 }
 
+// The tables are constant while a kernel runs: read through the constant
+// address space a uniform load is a scalar one.  As a vector load it would
+// queue behind the tiles in flight, and waiting for it would wait for them.
+typedef const __attribute__((address_space(4))) int32_t* table_ptr;
+__device__ __forceinline__ table_ptr as_table(const int32_t* p) {
+    return (table_ptr)(reinterpret_cast<uintptr_t>(p));
+}
+
 // A request's rows and tokens, as this workgroup sees them.
 struct Request {
     int first, rows, kv;
@@ -84,10 +91,10 @@ struct Request {
 __device__ __forceinline__ Request request_of(const AttnArgs& a, int b) {
     int q0 = b, q1 = b + 1;
     if (a.q_start) {
-        q0 = min(max(a.q_start[b], 0), a.T);
-        q1 = min(max(a.q_start[b + 1], 0), a.T);
+        q0 = min(max(as_table(a.q_start)[b], 0), a.T);
+        q1 = min(max(as_table(a.q_start)[b + 1], 0), a.T);
     }
-    return {q0, max(min(q1 - q0, 0x7FFFFFFF), 0), max(a.kv_lens[b], 0)};
+    return {q0, max(q1 - q0, 0), max(as_table(a.kv_lens)[b], 0)};
 }
 
 // The tiles that some of a run of rows (positions low .. high) see: those of
@@ -114,57 +121,115 @@ struct Frag {  // one tile's share of a lane
     u32x4_t km[2][kG], vm[2][kG];
 };
 
+// Where a tile lies: byte addresses, the same for all lanes (a lane adds a
+// 32-bit offset of its own).  With pages of 32 tokens or more (kWide) a tile
+// is in one page and its second half follows the first.
+template <bool kWide>
+struct Place {
+    static constexpr int kN = kWide ? 1 : 2;
+    uint64_t code[kN], meta[kN];
+};
+template <int D, bool kWide>
+__device__ __forceinline__ Place<kWide> place_of(const AttnArgs& a, int t0, int head, const int page[2]) {
+    Place<kWide> p;
+#pragma unroll
+    for (int h = 0; h < Place<kWide>::kN; ++h) {
+        const uint32_t off = (uint32_t)(t0 + 16 * h) & ((1u << a.c.shift) - 1);
+        const uint64_t ph = (uint64_t)(uint32_t)max(page[h], 0) * (uint32_t)a.c.heads + (uint32_t)head;
+        const uint64_t slot = (ph << a.c.shift) + off;
+        p.code[h] = slot * (D / 2);
+        p.meta[h] = (ph << a.c.shift) * (Frag<D>::kG * 4) + off * 4;
+    }
+    return p;
+}
+
+// One of a lane's loads: uniform base, the lane's offset, a constant.
+template <typename T>
+__device__ __forceinline__ T fetch(const uint32_t* base, uint64_t uniform, uint32_t lane_off) {
+    return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + uniform + lane_off);
+}
+
+// A lane's offsets within a tile.
+struct Offsets {
+    uint32_t k, v, meta;
+};
 template <int D>
-__device__ __forceinline__ void load_tile(const AttnArgs& a, Frag<D>& f, int t0, int head, const int page[2], int lane) {
-    constexpr int kG = Frag<D>::kG, kW = Frag<D>::kW, kWords = D / 8;
-    const int c = lane & 15, g = lane >> 4;
+__device__ __forceinline__ Offsets offsets_of(int lane) {
+    const uint32_t c = lane & 15, g = lane >> 4;
+    return {c * (D / 2) + (D == 64 ? 8 : 16) * g, g * (D * 2) + 16 * (D == 64 ? c >> 1 : c), 16 * g};
+}
+
+template <int D, bool kWide>
+__device__ __forceinline__ void load_keys(const AttnArgs& a, Frag<D>& f, const Place<kWide>& p, const Offsets& l) {
+    constexpr int kG = Frag<D>::kG, kW = Frag<D>::kW;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int bs = 1 << a.c.shift, off = (t0 + 16 * h) & (bs - 1);
-        const size_t ph = (size_t)page[h] * a.c.heads + head;
-        const uint32_t* kc = a.c.kc + (ph * bs + off) * kWords;
-        const uint32_t* vc = a.c.vc + (ph * bs + off) * kWords;  // (off / 4) * kWords * 4
-        const uint32_t* km = a.c.km + ph * kG * bs + off;
-        const uint32_t* vm = a.c.vm + ph * kG * bs + off;
+        const uint64_t code = kWide ? p.code[0] + h * 16 * (D / 2) : p.code[h % Place<kWide>::kN];
+        const uint64_t meta = kWide ? p.meta[0] + h * 64 : p.meta[h % Place<kWide>::kN];
 #pragma unroll
         for (int q = 0; q < kG; ++q) {
             if constexpr (kW == 4) {
-                const u32x4_t w = *reinterpret_cast<const u32x4_t*>(kc + c * kWords + q * 16 + 4 * g);
+                const u32x4_t w = fetch<u32x4_t>(a.c.kc, code + q * 64, l.k);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f.k[h][q][i] = w[i];
             } else {
-                const u32x2_t w = *reinterpret_cast<const u32x2_t*>(kc + c * kWords + 2 * g);
+                const u32x2_t w = fetch<u32x2_t>(a.c.kc, code, l.k);
                 f.k[h][q][0] = w.x;
                 f.k[h][q][1] = w.y;
             }
-            const int vw = D == 64 ? c >> 1 : q * 16 + c;
-            f.v[h][q] = *reinterpret_cast<const u32x4_t*>(vc + (g * kWords + vw) * 4);
-            f.km[h][q] = *reinterpret_cast<const u32x4_t*>(km + q * bs + 4 * g);
-            f.vm[h][q] = *reinterpret_cast<const u32x4_t*>(vm + q * bs + 4 * g);
+            f.km[h][q] = fetch<u32x4_t>(a.c.km, meta + (q ? (uint64_t)(4u * q << a.c.shift) : 0), l.meta);
         }
     }
 }
 
-// Pages of a tile's halves; -1 where the table has none for tokens that are seen.
-__device__ __forceinline__ void pages_of(const AttnArgs& a, const int32_t* table, int t0, int high, int page[2]) {
+template <int D, bool kWide>
+__device__ __forceinline__ void load_values(const AttnArgs& a, Frag<D>& f, const Place<kWide>& p, const Offsets& l) {
+    constexpr int kG = Frag<D>::kG;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int t = t0 + 16 * h, p = t >> a.c.shift;
-        int id = 0;
-        if (t <= high) {
-            id = p < a.width ? table[p] : -1;
-            if (id >= a.c.blocks) id = -1;
+        const uint64_t code = kWide ? p.code[0] + h * 16 * (D / 2) : p.code[h % Place<kWide>::kN];
+        const uint64_t meta = kWide ? p.meta[0] + h * 64 : p.meta[h % Place<kWide>::kN];
+#pragma unroll
+        for (int q = 0; q < kG; ++q) {
+            f.v[h][q] = fetch<u32x4_t>(a.c.vc, code + q * 256, l.v);
+            f.vm[h][q] = fetch<u32x4_t>(a.c.vm, meta + (q ? (uint64_t)(4u * q << a.c.shift) : 0), l.meta);
         }
-        page[h] = (int)sgpr((uint32_t)max(id, -1));
     }
 }
 
-template <int D, int kNB>
-__global__ __launch_bounds__(kThreads) void kv4_attn_kernel(AttnArgs a) {
+// The table's entries for a tile's halves, as they are (0 for none): nothing
+// waits for them here.
+struct Entries {
+    int e[2];
+};
+template <bool kWide>
+__device__ __forceinline__ Entries entries_of(const AttnArgs& a, table_ptr table, int t0) {
+    Entries x;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) x.e[h] = kWide && h ? x.e[0] : table[min((t0 + 16 * h) >> a.c.shift, a.width - 1)];
+    return x;
+}
+// Pages from entries; -1 where there is none for tokens that are seen.
+template <bool kWide>
+__device__ __forceinline__ void pages_of(const AttnArgs& a, const Entries& x, int t0, int high, int page[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (kWide && h) {
+            page[1] = page[0];
+            break;
+        }
+        const int t = t0 + 16 * h;
+        const bool sound = (t >> a.c.shift) < a.width && (unsigned)x.e[h] < (unsigned)a.c.blocks;
+        page[h] = t > high ? 0 : sound ? x.e[h] : -1;
+    }
+}
+
+template <int D, int kNB, int kWaves, bool kWide>
+__global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
     constexpr int kG = Frag<D>::kG, kW = Frag<D>::kW;
     constexpr int kJ = D == 64 ? 4 : 8;  // blocks of 16 d per group
     constexpr int kCols = 16 * kNB;
-    __shared__ float so[2][kCols][D + 4];
+    __shared__ float so[kWaves / 2][kCols][D + 4];
     __shared__ float sm[kWaves][kCols], sl[kWaves][kCols];
 
     const int lane = threadIdx.x & (kWave - 1), wave = (int)sgpr(threadIdx.x / kWave);
@@ -185,25 +250,53 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_kernel(AttnArgs a) {
     const int first_pos = req.kv - req.rows;
     const int low = first_pos + r0 / a.g, high = first_pos + (min(r0 + kCols, rows) - 1) / a.g;
     const Tiles tiles = tiles_of(a, low, high);
-    const int32_t* table = a.table + (size_t)b * a.width;
+    const table_ptr table = as_table(a.table + (size_t)b * a.width);
 
-    // this lane's rows, their queries as the score product's operand and sums
+    // this split's tiles, in turn over the waves
+    const int per = (tiles.count + a.splits - 1) / a.splits;
+    const int v1 = min(tiles.count, (split + 1) * per);
+    int v = split * per + wave;
+    const bool any = v < v1 && a.width > 0;
+    const auto clamped = [&](int x) { return x < v1 ? x : v1 - 1; };
+
+    // this lane's rows (past the last one: that one again, unseen) and their
+    // queries, on their way before the first tile
     int pos[kNB];
     u32x4_t xq[kNB][kG][kW];
+#pragma unroll
+    for (int n = 0; n < kNB; ++n) {
+        const int mine = r0 + 16 * n + c, r = min(mine, rows - 1);
+        pos[n] = mine < rows ? max(first_pos + r / a.g, -1) : -1;
+        const uint16_t* src = a.q + (int64_t)(req.first + r / a.g) * a.q_stride + (size_t)(head * a.g + r % a.g) * D;
+#pragma unroll
+        for (int q = 0; q < kG; ++q)
+#pragma unroll
+            for (int i = 0; i < kW; ++i)
+                xq[n][q][i] = *reinterpret_cast<const u32x4_t*>(src + q * W4_KV4_GROUP + (kW * g + i) * 8);
+    }
+    const Offsets offs = offsets_of<D>(lane);
+    Frag<D> f;
+    int page[2] = {-1, -1};
+    Entries next = {};
+    if (any) {
+        const Entries now = entries_of<kWide>(a, table, tiles.at(v) * kTile);
+        next = entries_of<kWide>(a, table, tiles.at(clamped(v + kWaves)) * kTile);
+        pages_of<kWide>(a, now, tiles.at(v) * kTile, high, page);
+        const Place<kWide> p = place_of<D, kWide>(a, tiles.at(v) * kTile, head, page);
+        load_keys<D, kWide>(a, f, p, offs);
+        load_values<D, kWide>(a, f, p, offs);
+    }
+    // the queries as the score product's operand, and their sums
+    f32x4_t xstart[kNB][kG];
     float xs[kNB][kG];
 #pragma unroll
     for (int n = 0; n < kNB; ++n) {
-        const int r = r0 + 16 * n + c;
-        const bool live = r < rows;
-        pos[n] = live ? max(first_pos + r / a.g, -1) : -1;
-        const uint16_t* src = a.q + (int64_t)(req.first + r / a.g) * a.q_stride + (size_t)(head * a.g + r % a.g) * D;
 #pragma unroll
         for (int q = 0; q < kG; ++q) {
             float sum = 0;
 #pragma unroll
             for (int i = 0; i < kW; ++i) {
-                u32x4_t w = {0, 0, 0, 0};
-                if (live) w = *reinterpret_cast<const u32x4_t*>(src + q * W4_KV4_GROUP + (kW * g + i) * 8);
+                const u32x4_t w = xq[n][q][i];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sum += bf16_to_f32(w[e] & 0xFFFFu) + __builtin_bit_cast(float, w[e] & 0xFFFF0000u);
                 uint32_t in[4] = {w.x, w.y, w.z, w.w}, pr[4];
@@ -211,40 +304,62 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_kernel(AttnArgs a) {
                 xq[n][q][i] = u32x4_t{pr[0], pr[1], pr[2], pr[3]};
             }
             xs[n][q] = row_sum(sum);
+            const float x0 = -128.0f * xs[n][q];
+            xstart[n][q] = f32x4_t{x0, x0, x0, x0};
         }
     }
 
-    f32x4_t o[kNB][kG][kJ];
+    f32x4_t o[kNB][kG][kJ], ones_sum[kNB][kG];  // of ones_sum only element 0 counts
     float extra[kNB][kG], m[kNB], l[kNB];
+    float means[kNB][kG], scales[kNB][kG];  // sums of p m and p s since the last settling
 #pragma unroll
     for (int n = 0; n < kNB; ++n) {
         m[n] = -INFINITY;
         l[n] = 0;
 #pragma unroll
         for (int q = 0; q < kG; ++q) {
-            extra[n][q] = 0;
+            extra[n][q] = means[n][q] = scales[n][q] = 0;
+            ones_sum[n][q] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < kJ; ++j) o[n][q][j] = f32x4_t{0, 0, 0, 0};
         }
     }
 
+    // The running maximum moves only when a score passes it by 2^8: weights up
+    // to 256 lose nothing, and a move costs a pass over the outputs.
+    const float slack = 8.0f / a.scale2;
     const uint32_t bias = vgpr_const(kInt4BiasPair);
-    const uint32_t c136 = 0xC308C308u;  // bf16 pair (-136, -136)
-    const u32x4_t minus = {c136, c136, c136, c136};
+    const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    // takes 136 times the weights' sum off the outputs; p (m + 8 s) so far
+    const auto settle = [&]() {
+#pragma unroll
+        for (int n = 0; n < kNB; ++n)
+#pragma unroll
+            for (int q = 0; q < kG; ++q) {
+                const float off = -136.0f * ones_sum[n][q][0];
+                ones_sum[n][q] = f32x4_t{0, 0, 0, 0};
+                extra[n][q] += fmaf(8.0f, scales[n][q], means[n][q]);
+                means[n][q] = scales[n][q] = 0;
+#pragma unroll
+                for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[n][q][j][r] += off;
+            }
+    };
     const uint32_t half_sel = (D == 64 && (c & 1)) ? 0x07060302u : 0x05040100u;
 
-    // this split's tiles, in turn over the waves
-    const int per = (tiles.count + a.splits - 1) / a.splits;
-    const int v1 = min(tiles.count, (split + 1) * per);
-    for (int v = split * per + wave; v < v1; v += kWaves) {
-        const int t0 = tiles.at(v) * kTile;
-        int page[2];
-        pages_of(a, table, t0, high, page);
-        Frag<D> f;
-        {
-            const int at[2] = {max(page[0], 0), max(page[1], 0)};
-            load_tile<D>(a, f, t0, head, at, lane);
-        }
+    // The next tile's keys are fetched when the scores are done with this
+    // one's, its values behind the outputs; page numbers a tile earlier.  The
+    // last tile fetches itself again: under a condition the compiler would
+    // load into other registers and wait for them to copy them over.
+    int t0 = tiles.at(clamped(v)) * kTile, t1 = tiles.at(clamped(v + kWaves)) * kTile;
+    if (!any) v = v1;
+    for (int done = 1; v < v1; v += kWaves, ++done) {
+        int coming[2];
+        pages_of<kWide>(a, next, t1, high, coming);
+        const Place<kWide> ahead = place_of<D, kWide>(a, t1, head, coming);
+        const int t2 = tiles.at(clamped(v + 2 * kWaves)) * kTile;
+        next = entries_of<kWide>(a, table, t2);
         // Whether every row sees every token of the tile.
         const bool whole = t0 + kTile - 1 <= low && (a.window == 0 || t0 > high - a.window || t0 + kTile <= a.sinks) &&
                            page[0] >= 0 && page[1] >= 0 && r0 + kCols <= rows;
@@ -260,8 +375,7 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_kernel(AttnArgs a) {
                 for (int i = 0; i < kW; ++i) kop[i] = key_operand(f.k[h][q][i], bias);
 #pragma unroll
                 for (int n = 0; n < kNB; ++n) {
-                    const float x0 = -128.0f * xs[n][q];
-                    f32x4_t acc = {x0, x0, x0, x0};
+                    f32x4_t acc = xstart[n][q];
 #pragma unroll
                     for (int i = 0; i < kW; ++i) acc = mfma(kop[i], xq[n][q][i], acc);
 #pragma unroll
@@ -272,6 +386,9 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_kernel(AttnArgs a) {
                 }
             }
         }
+        __builtin_amdgcn_sched_barrier(0);  // else loads above the last use of these registers land in others
+        load_keys<D, kWide>(a, f, ahead, offs);
+        __builtin_amdgcn_sched_barrier(0);
         uint32_t seen[kNB];  // bit 4 h + r
 #pragma unroll
         for (int n = 0; n < kNB; ++n) seen[n] = 0xFFu;
@@ -284,7 +401,8 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_kernel(AttnArgs a) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int t = t0 + 16 * h + 4 * g + r;
-                        const bool see = t <= pos[n] && (a.window == 0 || t > pos[n] - a.window || t < a.sinks);
+                        // no short cuts: branches would cost more than the comparisons
+                        const bool see = (t <= pos[n]) & ((a.window == 0) | (t > pos[n] - a.window) | (t < a.sinks));
                         if (see) seen[n] |= 1u << (4 * h + r);
                         s[n][h][r] = !see ? -INFINITY : page[h] < 0 ? NAN : s[n][h][r];
                     }
@@ -298,7 +416,7 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_kernel(AttnArgs a) {
             float top = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
                               fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
             top = row_max(top);
-            if (__any(top > m[n])) {
+            if (__any(top > m[n] + slack)) {
                 const float now = fmaxf(m[n], top);
                 const float keep = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[n] - now) * a.scale2);
                 m[n] = now;
@@ -306,6 +424,9 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_kernel(AttnArgs a) {
 #pragma unroll
                 for (int q = 0; q < kG; ++q) {
                     extra[n][q] *= keep;
+                    means[n][q] *= keep;
+                    scales[n][q] *= keep;
+                    ones_sum[n][q][0] *= keep;
 #pragma unroll
                     for (int j = 0; j < kJ; ++j)
 #pragma unroll
@@ -321,22 +442,31 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_kernel(AttnArgs a) {
                     p[h][r] = __builtin_amdgcn_exp2f(fmaf(s[n][h][r], a.scale2, -base));
                     l[n] += p[h][r];
                 }
+            // what a row does not see may hold anything, an infinity or a NaN too
+            const auto weigh = [&](auto masked) {
 #pragma unroll
-            for (int q = 0; q < kG; ++q) {
-                float ps[2][4];
+                for (int q = 0; q < kG; ++q) {
+                    float ps[2][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const uint32_t meta = f.vm[h][q][r];
-                        float sv = lo16(meta), mv = hi16(meta);
-                        // what a row does not see may hold anything, an infinity or a NaN too
-                        if (!whole && !(seen[n] >> (4 * h + r) & 1)) sv = mv = 0.0f;
-                        ps[h][r] = p[h][r] * sv;
-                        extra[n][q] = fmaf(p[h][r], fmaf(8.0f, sv, mv), extra[n][q]);
-                    }
-                pop[n][q] = u32x4_t{pack_bf16x2(ps[0][0], ps[0][1]), pack_bf16x2(ps[0][2], ps[0][3]),
-                                    pack_bf16x2(ps[1][0], ps[1][1]), pack_bf16x2(ps[1][2], ps[1][3])};
+                        for (int r = 0; r < 4; ++r) {
+                            uint32_t meta = f.vm[h][q][r];
+                            if constexpr (masked.value) meta = seen[n] >> (4 * h + r) & 1 ? meta : 0;
+                            ps[h][r] = p[h][r] * lo16(meta);
+                            means[n][q] = fmaf(p[h][r], hi16(meta), means[n][q]);
+                            scales[n][q] += ps[h][r];
+                        }
+                    // here, not put off behind the loads that reuse f.vm's registers
+                    asm volatile("" : "+v"(means[n][q]), "+v"(scales[n][q]));
+                    pop[n][q] = u32x4_t{pack_bf16x2(ps[0][0], ps[0][1]), pack_bf16x2(ps[0][2], ps[0][3]),
+                                        pack_bf16x2(ps[1][0], ps[1][1]), pack_bf16x2(ps[1][2], ps[1][3])};
+                }
+            };
+            if (whole) {
+                weigh(std::false_type{});
+            } else {
+                weigh(std::true_type{});
             }
         }
 
@@ -360,11 +490,24 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_kernel(AttnArgs a) {
                     for (int i = 0; i < 4; ++i) vop[i] = ((pr[i] >> (4 * j)) & 0x000F000Fu) | bias;
 #pragma unroll
                     for (int n = 0; n < kNB; ++n)
-                        o[n][q][4 * z + j] = mfma(minus, pop[n][q], mfma(vop, pop[n][q], o[n][q][4 * z + j]));
+                        o[n][q][4 * z + j] = mfma(vop, pop[n][q], o[n][q][4 * z + j]);
                 }
             }
+#pragma unroll
+            for (int n = 0; n < kNB; ++n) ones_sum[n][q] = mfma(ones, pop[n][q], ones_sum[n][q]);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        load_values<D, kWide>(a, f, ahead, offs);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            page[h] = coming[h];
+        }
+        t0 = t1;
+        t1 = t2;
+        if (done % 8 == 0) settle();
     }
+    settle();
 
     // each wave's own part, whole over its tokens
 #pragma unroll
@@ -379,7 +522,7 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_kernel(AttnArgs a) {
                 for (int r = 0; r < 4; ++r) o[n][q][j][r] += e;
         }
     }
-    // join the four waves: common maximum, then two rounds through LDS
+    // join the waves: common maximum, then pairwise through LDS
     if (lane < 16) {
 #pragma unroll
         for (int n = 0; n < kNB; ++n) {
@@ -391,7 +534,9 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_kernel(AttnArgs a) {
 #pragma unroll
     for (int n = 0; n < kNB; ++n) {
         const int col = 16 * n + c;
-        const float now = fmaxf(fmaxf(sm[0][col], sm[1][col]), fmaxf(sm[2][col], sm[3][col]));
+        float now = sm[0][col];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) now = fmaxf(now, sm[w][col]);
         const auto weight = [&](float x) { return x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((x - now) * a.scale2); };
         float sum = 0;
 #pragma unroll
@@ -432,14 +577,15 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_kernel(AttnArgs a) {
 #pragma unroll
                     for (int j = 0; j < kJ; ++j) o[n][q][j][r] += so[slot][16 * n + c][place(q, r) + j];
     };
-    if (wave & 1) put(wave >> 1);
-    __syncthreads();
-    if (!(wave & 1)) take(wave >> 1);
-    __syncthreads();
-    if (wave == 2) put(0);
-    __syncthreads();
+#pragma unroll
+    for (int step = 1; step < kWaves; step *= 2) {
+        const int pair = wave / (2 * step);
+        if (wave % (2 * step) == step) put(pair);
+        __syncthreads();
+        if (wave % (2 * step) == 0) take(pair);
+        if (2 * step < kWaves) __syncthreads();
+    }
     if (wave != 0) return;
-    take(0);
 
 #pragma unroll
     for (int n = 0; n < kNB; ++n) {
@@ -481,38 +627,74 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_kernel(AttnArgs a) {
     }
 }
 
-// Joins the splits of one row; a lane owns D / 64 values.
+// Joins the splits of one row, a workgroup a row: D / 4 lanes hold its values,
+// so 1024 / D splits are read at once.
+constexpr int kMaxSplits = 128;
+constexpr int kThreads = 256;
 template <int D>
 __global__ __launch_bounds__(kThreads) void kv4_attn_join_kernel(AttnArgs a) {
-    constexpr int kPer = D / kWave;
-    const int lane = threadIdx.x & (kWave - 1);
+    constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
+    __shared__ float weight[kMaxSplits];
+    __shared__ f32x4_t part[kThreads];
+    __shared__ float inv_sum;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int heads = a.g * a.c.heads;
-    const int64_t unit = (int64_t)blockIdx.x * kWaves + sgpr(threadIdx.x / kWave);
-    const int h = (int)(unit % heads);
-    const int i = (int)((unit / heads) % a.max_q), b = (int)(unit / heads / a.max_q);
-    if (b >= a.B) return;
+    const int h = (int)(blockIdx.x % heads);
+    const int i = (int)((blockIdx.x / heads) % a.max_q), b = (int)(blockIdx.x / heads / a.max_q);
     const Request req = request_of(a, b);
     if (i >= req.rows) return;
     const int t = req.first + i;
     const size_t at = ((size_t)t * heads + h) * a.splits;
-    float now = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) now = fmaxf(now, a.part_ml[2 * (at + s)]);
-    float sum = 0, v[kPer] = {};
-    for (int s = 0; s < a.splits; ++s) {
-        const float ms = a.part_ml[2 * (at + s)], ls = a.part_ml[2 * (at + s) + 1];
-        if (ls == 0.0f) continue;
-        const float w = ms == -INFINITY ? NAN : __builtin_amdgcn_exp2f((ms - now) * a.scale2);
-        sum += w * ls;
-        const float* src = a.part_o + (at + s) * D + lane * kPer;
+    if (tid < kWave) {
+        float ms[kMaxSplits / kWave], ls[kMaxSplits / kWave], now = -INFINITY, sum = 0;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) v[e] = fmaf(w, src[e], v[e]);
+        for (int u = 0; u < kMaxSplits / kWave; ++u) {
+            const int s = u * kWave + lane;
+            ms[u] = s < a.splits ? a.part_ml[2 * (at + s)] : -INFINITY;
+            ls[u] = s < a.splits ? a.part_ml[2 * (at + s) + 1] : 0.0f;
+            now = fmaxf(now, ms[u]);
+        }
+#pragma unroll
+        for (int x = 1; x < kWave; x <<= 1) now = fmaxf(now, __shfl_xor(now, x));
+#pragma unroll
+        for (int u = 0; u < kMaxSplits / kWave; ++u) {
+            // a split that saw nothing has l = 0 and counts for nothing; a NaN stays one
+            const float w = ls[u] == 0.0f ? 0.0f : ms[u] == -INFINITY ? NAN : __builtin_amdgcn_exp2f((ms[u] - now) * a.scale2);
+            weight[u * kWave + lane] = w;
+            sum += ls[u] == 0.0f ? 0.0f : w * ls[u];
+        }
+#pragma unroll
+        for (int x = 1; x < kWave; x <<= 1) sum += __shfl_xor(sum, x);
+        if (lane == 0) inv_sum = sum == 0.0f ? 0.0f : 1.0f / sum;
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t* dst = a.out + (int64_t)t * a.out_stride + (size_t)h * D + lane * kPer;
+    __syncthreads();
+    const int li = tid % kLanes;
+    f32x4_t v = {0, 0, 0, 0};
+#pragma unroll 8
+    for (int s = tid / kLanes; s < a.splits; s += kAtOnce) {
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part_o + (at + s) * D + 4 * li);
+        const float w = weight[s];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) dst[e] = f32_to_bf16(v[e] * inv);
+        for (int e = 0; e < 4; ++e) v[e] = fmaf(w, x[e], v[e]);
+    }
+    part[tid] = v;
+    __syncthreads();
+    if (tid >= kLanes) return;
+#pragma unroll
+    for (int s = 1; s < kAtOnce; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += part[s * kLanes + li][e];
+    const float inv = inv_sum;
+    *reinterpret_cast<u32x2_t*>(a.out + (int64_t)t * a.out_stride + (size_t)h * D + 4 * li) =
+        u32x2_t{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
 }
 
+#ifndef W4_ATTN_GROUPS
+#define W4_ATTN_GROUPS 512
+#endif
+#ifndef W4_ATTN_WAVES
+#define W4_ATTN_WAVES 4
+#endif
 constexpr int kNBDefault = 1;
 
 int row_tiles_of(const w4_attn_args& a, const w4_kv4_cache& c) {
@@ -527,20 +709,26 @@ int splits_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     int64_t tokens = a.max_kv;
     if (a.window > 0) tokens = tokens < (int64_t)a.window + a.sinks + a.max_q ? tokens : (int64_t)a.window + a.sinks + a.max_q;
     const int64_t tiles = (tokens + kTile - 1) / kTile;
-    int64_t want = (512 + groups - 1) / (groups > 0 ? groups : 1);
-    const int64_t most = tiles / (2 * kWaves);
+    int64_t want = (W4_ATTN_GROUPS + groups - 1) / (groups > 0 ? groups : 1);
+    const int64_t most = tiles / (2 * W4_ATTN_WAVES);
     want = want < most ? want : most;
-    return (int)(want < 1 ? 1 : want > 128 ? 128 : want);
+    return (int)(want < 1 ? 1 : want > kMaxSplits ? kMaxSplits : want);
 }
 
-template <int D>
+template <int D, bool kWide>
 hipError_t launch_d(AttnArgs& k, int64_t groups, hipStream_t stream) {
-    kv4_attn_kernel<D, kNBDefault><<<dim3((unsigned)groups), dim3(kThreads), 0, stream>>>(k);
+    constexpr int kWaves = W4_ATTN_WAVES;
+    kv4_attn_kernel<D, kNBDefault, kWaves, kWide><<<dim3((unsigned)groups), dim3(kWaves * kWave), 0, stream>>>(k);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || k.splits == 1) return err;
     const int64_t units = (int64_t)k.B * k.max_q * k.g * k.c.heads;
-    kv4_attn_join_kernel<D><<<dim3((unsigned)((units + kWaves - 1) / kWaves)), dim3(kThreads), 0, stream>>>(k);
+    kv4_attn_join_kernel<D><<<dim3((unsigned)units), dim3(kThreads), 0, stream>>>(k);
     return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_w(AttnArgs& k, int64_t groups, hipStream_t stream) {
+    return k.c.shift >= 5 ? launch_d<D, true>(k, groups, stream) : launch_d<D, false>(k, groups, stream);
 }
 
 }  // namespace
@@ -577,9 +765,9 @@ hipError_t launch_kv4_attn(const w4_attn_args& a, const w4_kv4_cache& c, void* w
     }
     const int64_t groups = (int64_t)a.B * c.kv_heads * k.row_tiles * k.splits;
     switch (c.head_dim) {
-        case 64: return launch_d<64>(k, groups, stream);
-        case 128: return launch_d<128>(k, groups, stream);
-        default: return launch_d<256>(k, groups, stream);
+        case 64: return launch_w<64>(k, groups, stream);
+        case 128: return launch_w<128>(k, groups, stream);
+        default: return launch_w<256>(k, groups, stream);
     }
 }
 
