@@ -66,68 +66,95 @@ for _name, (_res, _args) in SIGNATURES.items():
     _fn.restype, _fn.argtypes = _res, _args
 
 
-class _Call:
-    """Checks one call's tensors: on one GPU, of the given dtype and layout."""
+_bf16, _f16, _f32, _f64, _int32 = torch.bfloat16, torch.float16, torch.float32, torch.float64, torch.int32
 
-    def __init__(self, where: str):
-        self.where, self.device = where, None
-
-    def ptr(self, t, name, dtype, contiguous=True):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != dtype:
-            raise TypeError(f"{name}: dtype {t.dtype}, not {dtype}")
-        d = t.device
-        if d.type != "cuda":
-            raise ValueError(f"{name} must be a device tensor (got {d})")
-        if d != self.device:
-            if self.device is not None:
-                raise ValueError(f"{name} lies on {d}, other tensors of this call on {self.device}")
-            self.device = d
-        if contiguous and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
-
-    def maybe(self, t, name, dtype):
-        return None if t is None else self.ptr(t, name, dtype)
-
-    def heads(self, t, name, rows=None, heads=None, dim=None):
-        """[rows, heads, dim] BF16 whose heads lie together: (pointer, row stride)."""
-        if not isinstance(t, torch.Tensor) or t.dim() != 3:
-            raise ValueError(f"{name} must be a tensor [tokens, heads, head_dim]")
-        got = t.shape
-        if (rows is not None and got[0] != rows) or (heads is not None and got[1] != heads) or \
-                (dim is not None and got[2] != dim):
-            raise ValueError(f"{name} must be {[rows, heads, dim]}; got {list(got)}")
-        step, inner, unit = t.stride()
-        if (got[2] > 1 and unit != 1) or (got[1] > 1 and inner != got[2]):
-            raise ValueError(f"{name}: the heads of a row must lie together")
-        if got[0] <= 1:  # one row or none: whatever stride it has is not used
-            step = max(got[1] * got[2], 8)
-        return self.ptr(t, name, torch.bfloat16, contiguous=False), step
-
-    def run(self, fn, args, stream):
-        """fn(*args, stream) on the tensors' device."""
-        index = self.device.index
-        if index == torch.cuda.current_device():
-            self._run(fn, args, stream)
-        else:
-            with torch.cuda.device(index):
-                self._run(fn, args, stream)
-
-    def _run(self, fn, args, stream):
-        if stream is None:
-            stream = torch.cuda.current_stream().cuda_stream
-        elif isinstance(stream, torch.cuda.Stream):
-            if stream.device != self.device:
-                raise ValueError(f"{self.where}: stream of {stream.device}, tensors on {self.device}")
-            stream = stream.cuda_stream
-        _check(fn(*args, int(stream)), self.where)
+# The current stream's handle and the current device, without the Python
+# objects around them: a small call costs about as much as its launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _length(t, name, n):
-    if t.dim() != 1 or t.shape[0] != n:
+def _refuse(t, name, dtype, device):
+    """Raises what is wrong with a tensor that failed the quick test of ``_ptr``."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, not {dtype}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor (got {t.device})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} lies on {t.device}, other tensors of this call on cuda:{device}")
+
+
+def _device_of(t, name, dtype):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() < 0:
+        _refuse(t, name, dtype, None)
+    return t.get_device()
+
+
+def _ptr(t, name, dtype, device):
+    """Address of a contiguous tensor of ``dtype`` on GPU ``device``."""
+    try:
+        if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, device)
+
+
+def _vector(t, name, dtype, device, n):
+    """Address of a contiguous vector of n values."""
+    try:
+        if t.dtype is dtype and t.get_device() == device and t.shape == (n,) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if isinstance(t, torch.Tensor) and tuple(t.shape) != (n,):
         raise ValueError(f"{name} must be [{n}]; got {list(t.shape)}")
+    _refuse(t, name, dtype, device)
+
+
+def _heads(t, name, device, rows=None, heads=None, dim=None):
+    """[rows, heads, dim] BF16 whose heads lie together: (address, row stride)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a tensor [tokens, heads, head_dim]")
+    n, h, d = t.shape
+    if (rows is not None and n != rows) or (heads is not None and h != heads) or (dim is not None and d != dim):
+        raise ValueError(f"{name} must be {[rows, heads, dim]}; got {[n, h, d]}")
+    step, inner, unit = t.stride()
+    if (d > 1 and unit != 1) or (h > 1 and inner != d):
+        raise ValueError(f"{name}: the heads of a row must lie together")
+    if n <= 1:  # one row or none: whatever stride it has is not used
+        step = max(h * d, 8)
+    if t.dtype is not _bf16 or t.get_device() != device:
+        _refuse(t, name, _bf16, device)
+    return t.data_ptr(), step
+
+
+def _call(where, fn, args, stream, device):
+    """fn(*args, stream) on GPU ``device``."""
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return _call(where, fn, args, stream, device)
+    if stream is None:
+        stream = _raw_stream(device)
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != device:
+            raise ValueError(f"{where}: stream of {stream.device}, tensors on cuda:{device}")
+        stream = stream.cuda_stream
+    status = fn(*args, int(stream))
+    if status:
+        _check(status, where)
+
+
+def _cache_ref(cache, device):
+    if not isinstance(cache, Kv4Cache):
+        raise TypeError("cache must be a Kv4Cache")
+    if cache.device_index != device:
+        raise ValueError(f"the cache lies on cuda:{cache.device_index}, other tensors of this call on cuda:{device}")
+    return cache.ref
 
 
 class Kv4Cache:
@@ -146,14 +173,13 @@ class Kv4Cache:
                                ("k_meta", k_meta, (nb, h, groups, bs, 2)), ("v_meta", v_meta, (nb, h, groups, bs, 2))):
             if tuple(t.shape) != shape:
                 raise ValueError(f"{name} must be {shape}; got {tuple(t.shape)}")
-        call = _Call("Kv4Cache")
+        i = _device_of(k_codes, "k_codes", _int32)
         self.k_codes, self.k_meta, self.v_codes, self.v_meta = k_codes, k_meta, v_codes, v_meta
         self.num_blocks, self.kv_heads, self.block_size, self.head_dim = nb, h, bs, d
-        self.struct = _CacheStruct(call.ptr(k_codes, "k_codes", torch.int32), call.ptr(k_meta, "k_meta", torch.float16),
-                                   call.ptr(v_codes, "v_codes", torch.int32), call.ptr(v_meta, "v_meta", torch.float16),
-                                   nb, bs, h, d)
+        self.device_index = i
+        self.struct = _CacheStruct(_ptr(k_codes, "k_codes", _int32, i), _ptr(k_meta, "k_meta", _f16, i),
+                                   _ptr(v_codes, "v_codes", _int32, i), _ptr(v_meta, "v_meta", _f16, i), nb, bs, h, d)
         self.ref = ctypes.byref(self.struct)
-        self.device = call.device
 
     @classmethod
     def empty(cls, num_blocks: int, block_size: int, kv_heads: int, head_dim: int, device="cuda") -> "Kv4Cache":
@@ -166,15 +192,6 @@ class Kv4Cache:
                    torch.empty(num_blocks, kv_heads, groups, block_size, 2, **meta))
 
 
-def _with_cache(call, cache):
-    if not isinstance(cache, Kv4Cache):
-        raise TypeError("cache must be a Kv4Cache")
-    if call.device is not None and call.device != cache.device:
-        raise ValueError(f"the cache lies on {cache.device}, other tensors of this call on {call.device}")
-    call.device = cache.device
-    return cache.ref
-
-
 def w4_kv4_plan(cached, new_tokens, block_table, free_blocks, free_count, block_size: int, q_start, kv_lens,
                 positions, slots, counts, stream=None) -> None:
     """Block tables, slot map, positions and row ranges of a step from the requests' lengths.
@@ -183,21 +200,17 @@ def w4_kv4_plan(cached, new_tokens, block_table, free_blocks, free_count, block_
     pages' entries are written); ``free_blocks`` int32 [n], ``free_count`` int32 [1].
     Outputs: ``q_start`` [B + 1], ``kv_lens`` [B], ``positions`` and ``slots`` [rows] (-1
     behind the last request), ``counts`` [2] (pages left, pages short)."""
-    call, i32 = _Call("w4_kv4_plan"), torch.int32
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     B, width = block_table.shape
-    rows = positions.numel()
-    for name, t, n in (("cached", cached, B), ("new_tokens", new_tokens, B), ("q_start", q_start, B + 1),
-                       ("kv_lens", kv_lens, B), ("slots", slots, rows), ("positions", positions, rows),
-                       ("free_count", free_count, 1), ("counts", counts, 2), ("free_blocks", free_blocks, free_blocks.numel())):
-        _length(t, name, n)
-    args = (call.ptr(cached, "cached", i32), call.ptr(new_tokens, "new_tokens", i32),
-            call.ptr(block_table, "block_table", i32), call.ptr(free_blocks, "free_blocks", i32),
-            call.ptr(free_count, "free_count", i32), B, width, free_blocks.shape[0], int(block_size), rows,
-            call.ptr(q_start, "q_start", i32), call.ptr(kv_lens, "kv_lens", i32),
-            call.ptr(positions, "positions", i32), call.ptr(slots, "slots", i32), call.ptr(counts, "counts", i32))
-    call.run(lib.w4_kv4_plan, args, stream)
+    rows, pages, i, v = positions.numel(), free_blocks.numel(), _device_of(block_table, "block_table", _int32), _int32
+    args = (_vector(cached, "cached", v, i, B), _vector(new_tokens, "new_tokens", v, i, B),
+            _ptr(block_table, "block_table", v, i), _vector(free_blocks, "free_blocks", v, i, pages),
+            _vector(free_count, "free_count", v, i, 1), B, width, pages, block_size, rows,
+            _vector(q_start, "q_start", v, i, B + 1), _vector(kv_lens, "kv_lens", v, i, B),
+            _vector(positions, "positions", v, i, rows), _vector(slots, "slots", v, i, rows),
+            _vector(counts, "counts", v, i, 2))
+    _call("w4_kv4_plan", lib.w4_kv4_plan, args, stream, i)
 
 
 def w4_qk_norm_rope(q, k, positions=None, cos_sin=None, q_out=None, k_out=None, q_weight=None, k_weight=None,
@@ -209,55 +222,53 @@ def w4_qk_norm_rope(q, k, positions=None, cos_sin=None, q_out=None, k_out=None, 
     ``q`` [T, q_heads, head_dim] (None: keys only), ``k``, ``v`` [T, kv_heads, head_dim], BF16, rows at
     any stride; ``cos_sin`` float [max_pos, rot_dim] (cosines, then sines; None: no rotation).
     ``q_out`` and ``k_out`` may be ``q`` and ``k`` themselves; ``k_out`` may be None with a cache."""
-    call = _Call("w4_qk_norm_rope")
-    a = _QkArgs()
-    a.k, a.k_stride = call.heads(k, "k")
-    T, a.kv_heads, a.head_dim = k.shape
-    a.T = T
+    i = _device_of(k, "k", _bf16)
+    kp, ks = _heads(k, "k", i)
+    T, kv_heads, dim = k.shape
+    qp = qs = vp = vs = qop = qos = kop = kos = 0
+    q_heads = reach = rot = 0
+    qw = kw = cs = pos = sp = ref = None
     if q is not None:
-        a.q, a.q_stride = call.heads(q, "q", T, None, a.head_dim)
-        a.q_heads = q.shape[1]
+        qp, qs = _heads(q, "q", i, T, None, dim)
+        q_heads = q.shape[1]
         if q_out is None:
             raise ValueError("q_out must be given with q")
-        a.q_out, a.q_out_stride = call.heads(q_out, "q_out", T, a.q_heads, a.head_dim)
+        qop, qos = _heads(q_out, "q_out", i, T, q_heads, dim)
     if k_out is not None:
-        a.k_out, a.k_out_stride = call.heads(k_out, "k_out", T, a.kv_heads, a.head_dim)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _length(w, name, a.head_dim)
-            setattr(a, name, call.ptr(w, name, torch.bfloat16))
+        kop, kos = _heads(k_out, "k_out", i, T, kv_heads, dim)
+    if q_weight is not None:
+        qw = _vector(q_weight, "q_weight", _bf16, i, dim)
+    if k_weight is not None:
+        kw = _vector(k_weight, "k_weight", _bf16, i, dim)
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [max_pos, rot_dim]")
-        a.max_pos, a.rot_dim = cos_sin.shape
-        a.cos_sin = call.ptr(cos_sin, "cos_sin", torch.float32)
+        reach, rot = cos_sin.shape
+        cs = _ptr(cos_sin, "cos_sin", _f32, i)
     if positions is not None:
-        _length(positions, "positions", T)
-        a.positions = call.ptr(positions, "positions", torch.int32)
-    a.eps, a.weight_add, a.interleaved = eps, weight_add, bool(interleaved)
-    ref = None
+        pos = _vector(positions, "positions", _int32, i, T)
     if cache is not None:
         if v is None or slots is None:
             raise ValueError("v and slots must be given with a cache")
-        a.v, a.v_stride = call.heads(v, "v", T, a.kv_heads, a.head_dim)
-        _length(slots, "slots", T)
-        a.slots = call.ptr(slots, "slots", torch.int32)
-        ref = _with_cache(call, cache)
-    call.run(lib.w4_qk_norm_rope, (ctypes.byref(a), ref), stream)
+        vp, vs = _heads(v, "v", i, T, kv_heads, dim)
+        sp = _vector(slots, "slots", _int32, i, T)
+        ref = _cache_ref(cache, i)
+    a = _QkArgs(qp, kp, vp, qs, ks, vs, qw, kw, cs, pos, sp, qop, kop, qos, kos, T, q_heads, kv_heads, dim, rot, reach,
+                1 if interleaved else 0, eps, weight_add)
+    _call("w4_qk_norm_rope", lib.w4_qk_norm_rope, (ctypes.byref(a), ref), stream, i)
 
 
 def w4_kv4_read(cache, slots, k_out=None, v_out=None, stream=None) -> None:
     """The keys and values that ``slots`` of the cache stand for, in BF16 [n, kv_heads, head_dim]."""
-    call = _Call("w4_kv4_read")
-    ref = _with_cache(call, cache)
-    _length(slots, "slots", slots.numel())
-    n = slots.shape[0]
+    if not isinstance(cache, Kv4Cache):
+        raise TypeError("cache must be a Kv4Cache")
+    i, n = cache.device_index, slots.numel()
     outs = []
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None and tuple(t.shape) != (n, cache.kv_heads, cache.head_dim):
             raise ValueError(f"{name} must be {(n, cache.kv_heads, cache.head_dim)}; got {tuple(t.shape)}")
-        outs.append(call.maybe(t, name, torch.bfloat16))
-    call.run(lib.w4_kv4_read, (ref, call.ptr(slots, "slots", torch.int32), n, *outs), stream)
+        outs.append(None if t is None else _ptr(t, name, _bf16, i))
+    _call("w4_kv4_read", lib.w4_kv4_read, (cache.ref, _vector(slots, "slots", _int32, i, n), n, *outs), stream, i)
 
 
 def w4_kv4_attn_workspace_bytes(cache, T: int, B: int, q_heads: int, max_q: int, max_kv: int, window: int = 0,
@@ -276,29 +287,26 @@ def w4_kv4_attn(q, cache, block_table, kv_lens, out, q_start=None, max_q: int = 
     the last at position ``kv_lens[b] - 1``.  With ``window`` > 0 a row sees the last ``window`` tokens up
     to its own and the first ``sinks``.  ``max_kv`` (default: the block table's reach) and ``max_q`` size
     the split and the workspace (``w4_kv4_attn_workspace_bytes``).  ``scale``: 1 / sqrt(head_dim)."""
-    call = _Call("w4_kv4_attn")
-    ref = _with_cache(call, cache)
-    a = _AttnArgs()
-    d = cache.head_dim
-    a.q, a.q_stride = call.heads(q, "q", None, None, d)
-    a.T, a.q_heads, _ = q.shape
-    a.out, a.out_stride = call.heads(out, "out", a.T, a.q_heads, d)
+    if not isinstance(cache, Kv4Cache):
+        raise TypeError("cache must be a Kv4Cache")
+    i, d = cache.device_index, cache.head_dim
+    qp, qs = _heads(q, "q", i, None, None, d)
+    T, q_heads, _ = q.shape
+    op, os = _heads(out, "out", i, T, q_heads, d)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
-    a.B, a.max_blocks = block_table.shape
-    a.block_table = call.ptr(block_table, "block_table", torch.int32)
-    _length(kv_lens, "kv_lens", a.B)
-    a.kv_lens = call.ptr(kv_lens, "kv_lens", torch.int32)
-    if q_start is not None:
-        _length(q_start, "q_start", a.B + 1)
-        a.q_start = call.ptr(q_start, "q_start", torch.int32)
-    a.max_q, a.window, a.sinks = max_q, min(window, _INT_MAX), min(sinks, _INT_MAX)
-    a.max_kv = min(a.max_blocks * cache.block_size if max_kv is None else max_kv, _INT_MAX)
-    a.scale = 1.0 / math.sqrt(d) if scale is None else scale
+    B, width = block_table.shape
+    if max_kv is None:
+        max_kv = width * cache.block_size
+    a = _AttnArgs(qp, op, qs, os, _ptr(block_table, "block_table", _int32, i),
+                  _vector(kv_lens, "kv_lens", _int32, i, B),
+                  None if q_start is None else _vector(q_start, "q_start", _int32, i, B + 1), T, B, q_heads, width, max_q,
+                  min(max_kv, _INT_MAX), min(window, _INT_MAX), min(sinks, _INT_MAX),
+                  1.0 / math.sqrt(d) if scale is None else scale)
     pw, nbytes = None, 0
     if workspace is not None:
-        pw, nbytes = call.ptr(workspace, "workspace", workspace.dtype), workspace.numel() * workspace.element_size()
-    call.run(lib.w4_kv4_attn, (ctypes.byref(a), ref, pw, nbytes), stream)
+        pw, nbytes = _ptr(workspace, "workspace", workspace.dtype, i), workspace.numel() * workspace.element_size()
+    _call("w4_kv4_attn", lib.w4_kv4_attn, (ctypes.byref(a), cache.ref, pw, nbytes), stream, i)
     return out
 
 
@@ -312,23 +320,21 @@ def w4_sample(logits, uniform, tokens, temperature=None, top_k=None, top_p=None,
 
     ``temperature``, ``top_p``, ``min_p`` float32 [rows], ``top_k`` int32 [rows], each None for "off"
     (temperature 1).  ``tokens`` int32 [rows]; ``workspace`` as ``w4_sample_workspace_bytes``."""
-    call = _Call("w4_sample")
     if logits.dim() != 2:
         raise ValueError("logits must be [rows, vocab]")
     rows, vocab = logits.shape
     if vocab > 1 and logits.stride(1) != 1:
         raise ValueError("logits: the values of a row must lie together")
     stride = logits.stride(0) if rows > 1 else vocab
-    f32 = torch.float32
-    for name, t in (("uniform", uniform), ("tokens", tokens), ("temperature", temperature), ("top_k", top_k),
-                    ("top_p", top_p), ("min_p", min_p)):
-        if t is not None:
-            _length(t, name, rows)
-    args = [call.ptr(logits, "logits", torch.bfloat16, contiguous=False), stride,
-            call.ptr(uniform, "uniform", torch.float64), call.maybe(temperature, "temperature", f32),
-            call.maybe(top_k, "top_k", torch.int32), call.maybe(top_p, "top_p", f32), call.maybe(min_p, "min_p", f32),
-            call.ptr(tokens, "tokens", torch.int32), rows, vocab, None, 0]
+    i = _device_of(logits, "logits", _bf16)
+    pw, nbytes = None, 0
     if workspace is not None:
-        args[-2:] = (call.ptr(workspace, "workspace", workspace.dtype), workspace.numel() * workspace.element_size())
-    call.run(lib.w4_sample, args, stream)
+        pw, nbytes = _ptr(workspace, "workspace", workspace.dtype, i), workspace.numel() * workspace.element_size()
+    args = (logits.data_ptr(), stride, _vector(uniform, "uniform", _f64, i, rows),
+            None if temperature is None else _vector(temperature, "temperature", _f32, i, rows),
+            None if top_k is None else _vector(top_k, "top_k", _int32, i, rows),
+            None if top_p is None else _vector(top_p, "top_p", _f32, i, rows),
+            None if min_p is None else _vector(min_p, "min_p", _f32, i, rows),
+            _vector(tokens, "tokens", _int32, i, rows), rows, vocab, pw, nbytes)
+    _call("w4_sample", lib.w4_sample, args, stream, i)
     return tokens
