@@ -2,13 +2,18 @@
 // quantised into the 4-bit cache, in one pass; and the cache read back.
 //
 // Eight values a lane: a head is a run of D / 8 lanes, so a wave holds
-// 64 / (D / 8) heads of one token and walks over the token's heads with the
-// row of cosines and sines in registers (it is as large as two heads).  A
-// lane's eight 4-bit codes are one word of the cache.  The partner of a
-// rotated pair is either in the lane or in one lane of the same head, taken
-// as raw BF16 before its norm is applied (four exchanges instead of eight).
-// Memory bounds it for prompts; launch and latency for a decode step, where
-// the token's heads are spread over waves instead.
+// 64 / (D / 8) heads of one token and walks over the token's heads.  With
+// weights w, the rotated value is
+//   inv * (x_i (w_i c_i) -+ x_j (w_j s_i)),  inv = 1 / sqrt(mean(x^2) + eps),
+// and what stands in brackets is the token's, made once: two multiply-adds
+// and a product a value are left for each head.  The partner x_j is in the
+// lane or in one lane of the same head, taken as raw BF16 (four exchanges).  A
+// lane's eight 4-bit codes are one word of the cache.
+// Memory bounds it for prompts, as long as enough of it is asked for at once
+// (four heads' loads ahead); launch and latency for a decode step, where the
+// token's heads are spread over waves instead.
+#include <type_traits>
+
 #include "kv4.hpp"
 #include "w4_device.hpp"
 
@@ -25,23 +30,42 @@ __device__ __forceinline__ void unpack8(const u32x4_t& w, float v[8]) {
     }
 }
 
-// Reductions over the kLanes (8, 16 or 32) lanes of one head, in every lane.
-template <int kLanes, typename T>
-__device__ __forceinline__ T head_sum(T v) {
-#pragma unroll
-    for (int m = 1; m < kLanes; m <<= 1) v += __shfl_xor(v, m);
+// Exchanges inside a head's kLanes (8, 16 or 32) lanes, without LDS: across
+// lane bit 4 by a row swap, below it by DPP, from the highest bit down.
+template <int kOff, typename F>
+__device__ __forceinline__ float folded(float v, F f) {
+    if constexpr (kOff == 16) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, v);
+        const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        const uint32_t r0 = r[0], r1 = r[1];
+        return f(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
+    } else {
+        return f(v, dpp_partner<kOff>(v));
+    }
+}
+template <int kOff, typename F>
+__device__ __forceinline__ double folded(double v, F f) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)u, hi = (uint32_t)(u >> 32);
+    const auto join = [](uint32_t l, uint32_t h) { return __builtin_bit_cast(double, (uint64_t)h << 32 | l); };
+    if constexpr (kOff == 16) {
+        const auto a = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+        const auto b = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+        const uint32_t a0 = a[0], a1 = a[1], b0 = b[0], b1 = b[1];
+        return f(join(a0, b0), join(a1, b1));
+    } else {
+        return f(v, join(__builtin_bit_cast(uint32_t, dpp_partner<kOff>(__builtin_bit_cast(float, lo))),
+                         __builtin_bit_cast(uint32_t, dpp_partner<kOff>(__builtin_bit_cast(float, hi)))));
+    }
+}
+template <int kLanes, typename T, typename F>
+__device__ __forceinline__ T head_fold(T v, F f) {
+    if constexpr (kLanes > 1) return head_fold<kLanes / 2>(folded<kLanes / 2>(v, f), f);
     return v;
 }
-
-// One group's min, max and "holds a NaN or infinity" over its lanes.
-template <int kLanes>
-__device__ __forceinline__ void group_range(float& lo, float& hi, uint32_t& bad) {
-#pragma unroll
-    for (int m = 1; m < kLanes; m <<= 1) {
-        lo = fminf(lo, __shfl_xor(lo, m));
-        hi = fmaxf(hi, __shfl_xor(hi, m));
-        bad |= __shfl_xor(bad, m);
-    }
+template <int kLanes, typename T>
+__device__ __forceinline__ T head_sum(T v) {
+    return head_fold<kLanes>(v, [](T a, T b) { return a + b; });
 }
 
 __device__ __forceinline__ uint32_t f16_bits(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
@@ -53,189 +77,191 @@ __device__ __forceinline__ uint32_t quantise8(const u32x4_t& w, uint32_t& meta) 
     constexpr int kGroupLanes = (D < W4_KV4_GROUP ? D : W4_KV4_GROUP) / 8;
     float x[8];
     unpack8(w, x);
-    float lo = 3.0e38f, hi = -3.0e38f;
-    uint32_t bad = 0;
+    float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        bad |= !(fabsf(x[i]) <= 3.4e38f);
-        x[i] = fminf(fmaxf(x[i], -65504.0f), 65504.0f);
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
+        const float y = x[i] == x[i] ? x[i] : INFINITY;  // min and max pass a NaN over
+        lo = fminf(lo, y);
+        hi = fmaxf(hi, y);
     }
-    group_range<kGroupLanes>(lo, hi, bad);
+    lo = head_fold<kGroupLanes>(lo, [](float a, float b) { return fminf(a, b); });
+    hi = head_fold<kGroupLanes>(hi, [](float a, float b) { return fmaxf(a, b); });
+    const bool bad = !(lo > -INFINITY && hi < INFINITY);
+    lo = fminf(fmaxf(lo, -65504.0f), 65504.0f);
+    hi = fminf(fmaxf(hi, -65504.0f), 65504.0f);
     const float s = (float)(_Float16)((hi - lo) * (1.0f / 15.0f)), m = (float)(_Float16)lo;
     const float inv = s > 0.0f ? 1.0f / s : 0.0f;
     uint32_t word = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float t = fminf(fmaxf(rintf((x[i] - m) * inv), 0.0f), 15.0f);
+        // a value past +-65504 ends at 0 or 15 like that one
+        const float t = __builtin_amdgcn_fmed3f(rintf((x[i] - m) * inv), 0.0f, 15.0f);
         word |= (uint32_t)t << (4 * i);
     }
     meta = bad ? 0x00007E00u : f16_bits(s) | (f16_bits(m) << 16);
     return bad ? 0u : word;
 }
 
+// What a token's position and the weights make of a lane's eight values:
+// y = inv * (x * own + partner * other).
+template <typename T>
 struct Turn {
-    float c[8], s[8];  // of the lane's eight values (interleaved: four pairs)
+    T own[8], other[8];
 };
 
-// Norm and rotation of a lane's eight values, in T.
-template <typename T, int kLanes>
-__device__ __forceinline__ u32x4_t turned(const u32x4_t& w, const u32x4_t& gain, const u32x4_t& gain_partner,
-                                          bool norm, float weight_add, float eps, const Turn& turn, int role,
+// The eight values of a lane after norm and rotation.  ``partner`` is the lane
+// that holds the other values of its pairs, unless they are neighbours.
+template <int kLanes, bool kNeighbours, typename T>
+__device__ __forceinline__ u32x4_t turned(const u32x4_t& w, const Turn<T>& turn, bool norm, float eps, bool rotated,
                                           int partner, bool nan) {
-    // role: 0 not rotated, 1 first of a distant pair, 2 second of one, 3 neighbouring pairs
-    float x[8];
+    float x[8], z[8];
     unpack8(w, x);
-    T y[8], inv = 1;
+    if constexpr (kNeighbours) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = x[i ^ 1];
+    } else {
+        u32x4_t other;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) other[i] = __shfl(w[i], partner);
+        unpack8(other, z);
+    }
+    T inv = 1;
     if (norm) {
         T sum = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum += (T)x[i] * (T)x[i];
-        sum = head_sum<kLanes>(sum);
-        inv = (T)1 / sqrt(sum / (T)(8 * kLanes) + (T)eps);
-        float g[8];
-        unpack8(gain, g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = (T)x[i] * inv * ((T)g[i] + (T)weight_add);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i];
-    }
-    T r[8];
-    u32x4_t other;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) other[i] = __shfl(w[i], partner);
-    if (role == 1 || role == 2) {
-        float z[8], g[8];
-        unpack8(other, z);
-        if (norm) unpack8(gain_partner, g);
-        const T sign = role == 1 ? (T)-1 : (T)1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const T p = norm ? (T)z[i] * inv * ((T)g[i] + (T)weight_add) : (T)z[i];
-            r[i] = y[i] * (T)turn.c[i] + sign * p * (T)turn.s[i];
-        }
-    } else if (role == 3) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            r[2 * i] = y[2 * i] * (T)turn.c[i] - y[2 * i + 1] * (T)turn.s[i];
-            r[2 * i + 1] = y[2 * i + 1] * (T)turn.c[i] + y[2 * i] * (T)turn.s[i];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = y[i];
+        inv = (T)1 / sqrt(head_sum<kLanes>(sum) * (T)(1.0 / (8 * kLanes)) + (T)eps);
     }
     u32x4_t out;
+    T r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // an unrotated value takes no part of another, which may be an infinity
+        r[i] = ((T)x[i] * turn.own[i] + (T)(rotated ? z[i] : 0.0f) * turn.other[i]) * inv;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) out[i] = nan ? 0x7FC07FC0u : pack_bf16x2((float)r[2 * i], (float)r[2 * i + 1]);
     return out;
 }
 
 // The token's heads in runs of kHeads (the wave's width): q's, then k's, then
-// v's.  A wave takes runs ``part``, part + parts, ... of its token.
-template <int D, bool kCached>
+// v's.  A wave takes runs ``part``, part + parts, ... of its token, four loads
+// at a time.
+template <int D, bool kCached, bool kNeighbours>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(w4_qk_args a, Kv4 cache, int parts) {
     constexpr int kLanes = D / 8, kHeads = kWave / kLanes;
     constexpr int kGroups = D < W4_KV4_GROUP ? 1 : D / W4_KV4_GROUP;
     const int lane = threadIdx.x & (kWave - 1);
-    const int li = lane % kLanes, hi = lane / kLanes;
-    const int64_t unit = (int64_t)blockIdx.x * (kThreads / kWave) + sgpr(threadIdx.x / kWave);
-    const int t = (int)(unit / parts), part = (int)(unit % parts);
+    const int li = lane % kLanes, hi = lane / kLanes, e = 8 * li;
+    const uint32_t unit = blockIdx.x * (kThreads / kWave) + sgpr(threadIdx.x / kWave);
+    const int t = (int)(unit / (uint32_t)parts), part = (int)(unit % (uint32_t)parts);
     if (t >= a.T) return;
+    const int pos = a.positions ? (int)sgpr((uint32_t)a.positions[t]) : 0;
+    if (pos < 0) return;  // padding
 
-    bool nan = false;
-    int role = 0, partner = lane;
-    Turn turn = {};
-    if (a.rot_dim) {
-        const int pos = a.positions[t];
-        if (pos < 0) return;  // padding
-        nan = pos >= a.max_pos;
+    const bool nan = a.rot_dim && pos >= a.max_pos;
+    const int half = a.rot_dim / 2;
+    const bool rotated = e < a.rot_dim, first = e < half;
+    const int partner = kNeighbours || !rotated ? lane : first ? lane + half / 8 : lane - half / 8;
+    float c[8] = {1, 1, 1, 1, 1, 1, 1, 1}, s[8] = {};
+    if (rotated) {
         const float* row = a.cos_sin + (size_t)(nan ? 0 : pos) * a.rot_dim;
-        const int half = a.rot_dim / 2, e = 8 * li;
-        if (e < a.rot_dim) {
-            if (a.interleaved) {
-                role = 3;
+        const auto four = [](const float* p) { return *reinterpret_cast<const f32x4_t*>(p); };
+        // y_i = x_i c - x_j s for the first of a pair, x_j c + x_i s for the second
+        if constexpr (kNeighbours) {
+            const f32x4_t vc = four(row + e / 2), vs = four(row + half + e / 2);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    turn.c[i] = row[e / 2 + i];
-                    turn.s[i] = row[half + e / 2 + i];
-                }
-            } else {
-                role = e < half ? 1 : 2;
-                const int at = e < half ? e : e - half;
-                partner = role == 1 ? lane + half / 8 : lane - half / 8;
+            for (int i = 0; i < 8; ++i) {
+                c[i] = vc[i / 2];
+                s[i] = i % 2 ? vs[i / 2] : -vs[i / 2];
+            }
+        } else {
+            const float* at = row + (first ? e : e - half);
+            const f32x4_t vc[2] = {four(at), four(at + 4)}, vs[2] = {four(at + half), four(at + half + 4)};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    turn.c[i] = row[at + i];
-                    turn.s[i] = row[half + at + i];
-                }
+            for (int i = 0; i < 8; ++i) {
+                c[i] = vc[i / 4][i % 4];
+                s[i] = first ? -vs[i / 4][i % 4] : vs[i / 4][i % 4];
             }
         }
-    } else if (a.positions && a.positions[t] < 0) {
-        return;
     }
+    const auto turn_of = [&](const void* weight, auto& turn) {
+        typedef std::remove_reference_t<decltype(turn.own[0])> T;
+        const u32x4_t one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+        const u32x4_t* p = reinterpret_cast<const u32x4_t*>(weight);
+        const T add = weight ? (T)a.weight_add : (T)0;
+        float g[8], gp[8];
+        unpack8(weight ? p[li] : one, g);
+        unpack8(weight ? p[partner % kLanes] : one, gp);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            turn.own[i] = ((T)g[i] + add) * (T)c[i];
+            turn.other[i] = ((T)gp[kNeighbours ? i ^ 1 : i] + add) * (T)s[i];
+        }
+    };
+
     int64_t page = -1;
     int off = 0;
     if constexpr (kCached) {
-        const int slot = a.slots[t];
+        const int slot = (int)sgpr((uint32_t)a.slots[t]);
         if (slot >= 0 && (slot >> cache.shift) < cache.blocks) {
             page = slot >> cache.shift;
             off = slot & ((1 << cache.shift) - 1);
         }
     }
-
-    const int q_runs = (a.q_heads + kHeads - 1) / kHeads, k_runs = (a.kv_heads + kHeads - 1) / kHeads;
-    const int runs = q_runs + (kCached ? 2 : 1) * k_runs;
-    const int pli = (partner % kLanes);
-    const auto vec = [&](const void* p, int i) {
-        return reinterpret_cast<const u32x4_t*>(p)[i];
+    // Quantises a lane's values of head h into the cache.
+    const auto store = [&](const u32x4_t& y, int h, uint32_t* codes, uint32_t* metas, bool values) {
+        uint32_t meta;
+        const uint32_t word = quantise8<D>(y, meta);
+        if (h >= a.kv_heads || page < 0) return;
+        const size_t ph = (size_t)page * cache.heads + h, bs = (size_t)1 << cache.shift;
+        codes[values ? ((ph * (bs / 4) + off / 4) * kLanes + li) * 4 + off % 4 : (ph * bs + off) * kLanes + li] = word;
+        if (li % (kLanes / kGroups) == 0) metas[(ph * kGroups + li / (kLanes / kGroups)) * bs + off] = meta;
     };
-    const u32x4_t zero = {0, 0, 0, 0};
-    const bool qn = a.q_weight != nullptr, kn = a.k_weight != nullptr;
-    u32x4_t gq = zero, gqp = zero, gk = zero, gkp = zero;
-    if (qn) gq = vec(a.q_weight, li), gqp = vec(a.q_weight, pli);
-    if (kn) gk = vec(a.k_weight, li), gkp = vec(a.k_weight, pli);
-
-    for (int run = part; run < runs; run += parts) {
-        // wave-uniform: which input the run is of
-        const int kind = run < q_runs ? 0 : run < q_runs + k_runs ? 1 : 2;
-        const int heads = kind == 0 ? a.q_heads : a.kv_heads;
-        const int h = (run - (kind == 0 ? 0 : kind == 1 ? q_runs : q_runs + k_runs)) * kHeads + hi;
-        const bool live = h < heads;
-        const uint16_t* src = static_cast<const uint16_t*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v);
-        const int64_t stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
-        u32x4_t w = zero;
-        if (live) w = *reinterpret_cast<const u32x4_t*>(src + t * stride + (size_t)h * D + 8 * li);
-        if (kind == 0) {
-            const u32x4_t y = turned<float, kLanes>(w, gq, gqp, qn, a.weight_add, a.eps, turn, role, partner, nan);
-            if (live)
-                *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.q_out) + t * a.q_out_stride + (size_t)h * D +
-                                            8 * li) = y;
-            continue;
-        }
-        if (kind == 1) {
-            w = turned<double, kLanes>(w, gk, gkp, kn, a.weight_add, a.eps, turn, role, partner, nan);
-            if (live && a.k_out)
-                *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.k_out) + t * a.k_out_stride + (size_t)h * D +
-                                            8 * li) = w;
-        }
-        if constexpr (kCached) {
-            uint32_t meta;
-            const uint32_t word = quantise8<D>(w, meta);
-            if (live && page >= 0) {
-                const size_t ph = (size_t)page * cache.heads + h;
-                const size_t bs = (size_t)1 << cache.shift;
-                if (kind == 1) {
-                    cache.kc[(ph * bs + off) * kLanes + li] = word;
-                } else {
-                    cache.vc[((ph * (bs / 4) + off / 4) * kLanes + li) * 4 + off % 4] = word;
-                }
-                if (li % (kLanes / kGroups) == 0)
-                    (kind == 1 ? cache.km : cache.vm)[(ph * kGroups + li / (kLanes / kGroups)) * bs + off] = meta;
+    // Calls f(values, head) for this wave's runs of one input, from its run on.
+    const auto each = [&](const void* in, int64_t stride, int heads, int from, auto f) {
+        constexpr int kAhead = 4;
+        const uint16_t* src = static_cast<const uint16_t*>(in) + t * stride + e;
+        const int runs = (heads + kHeads - 1) / kHeads;
+        for (int r = from; r < runs; r += kAhead * parts) {
+            u32x4_t w[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int h = min((r + u * parts) * kHeads + hi, heads - 1);  // behind the last head: that one again
+                if (r + u * parts < runs) w[u] = *reinterpret_cast<const u32x4_t*>(src + (size_t)h * D);
             }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (r + u * parts < runs) f(w[u], (r + u * parts) * kHeads + hi);
         }
+        // where the next input's runs go on
+        return from < runs ? (parts - (runs - from) % parts) % parts : from - runs;
+    };
+
+    int at = part;
+    if (a.q_heads > 0) {
+        Turn<float> turn;
+        turn_of(a.q_weight, turn);
+        uint16_t* out = static_cast<uint16_t*>(a.q_out) + t * a.q_out_stride + e;
+        at = each(a.q, a.q_stride, a.q_heads, at, [&](const u32x4_t& w, int h) {
+            const u32x4_t y = turned<kLanes, kNeighbours>(w, turn, a.q_weight != nullptr, a.eps, rotated, partner, nan);
+            if (h < a.q_heads) *reinterpret_cast<u32x4_t*>(out + (size_t)h * D) = y;
+        });
     }
+    if (at < (a.kv_heads + kHeads - 1) / kHeads) {
+        Turn<double> turn;
+        turn_of(a.k_weight, turn);
+        at = each(a.k, a.k_stride, a.kv_heads, at, [&](const u32x4_t& w, int h) {
+            const u32x4_t y = turned<kLanes, kNeighbours>(w, turn, a.k_weight != nullptr, a.eps, rotated, partner, nan);
+            if (h < a.kv_heads && a.k_out)
+                *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.k_out) + t * a.k_out_stride + e + (size_t)h * D) = y;
+            if constexpr (kCached) store(y, h, cache.kc, cache.km, false);
+        });
+    } else {
+        at -= (a.kv_heads + kHeads - 1) / kHeads;
+    }
+    if constexpr (kCached)
+        each(a.v, a.v_stride, a.kv_heads, at, [&](const u32x4_t& w, int h) { store(w, h, cache.vc, cache.vm, true); });
 }
 
 template <int D>
@@ -276,10 +302,17 @@ hipError_t launch_d(const w4_qk_args& a, const w4_kv4_cache* c, hipStream_t stre
     parts = parts < 1 ? 1 : parts > runs ? runs : parts;
     const int64_t waves = (int64_t)a.T * parts, per = kThreads / kWave;
     const dim3 grid((unsigned)((waves + per - 1) / per)), block(kThreads);
+    const Kv4 cache = c ? kv4_of(*c) : Kv4{};
     if (c) {
-        qk_norm_rope_kernel<D, true><<<grid, block, 0, stream>>>(a, kv4_of(*c), parts);
+        if (a.interleaved) {
+            qk_norm_rope_kernel<D, true, true><<<grid, block, 0, stream>>>(a, cache, parts);
+        } else {
+            qk_norm_rope_kernel<D, true, false><<<grid, block, 0, stream>>>(a, cache, parts);
+        }
+    } else if (a.interleaved) {
+        qk_norm_rope_kernel<D, false, true><<<grid, block, 0, stream>>>(a, cache, parts);
     } else {
-        qk_norm_rope_kernel<D, false><<<grid, block, 0, stream>>>(a, Kv4{}, parts);
+        qk_norm_rope_kernel<D, false, false><<<grid, block, 0, stream>>>(a, cache, parts);
     }
     return hipGetLastError();
 }

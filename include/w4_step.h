@@ -214,7 +214,8 @@ W4_API w4_status w4_kv4_attn(const w4_attn_args* args, const w4_kv4_cache* cache
  * row of nothing but these gives -1; beside a +infinity everything less has
  * weight 0.
  *   logits       device bf16 [rows][vocab], rows row_stride elements apart, 2-byte aligned
- *   uniform      device double [rows] in [0, 1)
+ *   uniform      device double [rows] in [0, 1); less counts as 0, above 1 - 2^-40 as
+ *                that, so that no rounding of the sums draws a token without weight
  *   temperature  device float [rows] (not above 0: the largest logit), or NULL for 1
  *   top_k        device int32 [rows] (0 or less: all), or NULL
  *   top_p        device float [rows] (1 or more: all), or NULL

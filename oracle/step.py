@@ -220,6 +220,6 @@ def sample(bits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0) -> int:
         keep = max(1, n)
     if min_p > 0:
         keep = min(keep, max(1, int(np.sum(w >= float(np.float32(min_p))))))
-    goal = u * float(np.cumsum(w)[keep - 1])
+    goal = min(u, 1 - 2.0 ** -40) * float(np.cumsum(w)[keep - 1])  # never past the last token with a weight
     at = int(np.sum(np.cumsum(w) <= goal))
     return int(order[min(at, keep - 1)])
