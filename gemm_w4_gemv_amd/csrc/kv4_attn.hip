@@ -42,6 +42,7 @@ struct AttnArgs {
     Kv4 c;
     int T, B, g, width;  // g: query heads of a key/value head
     int max_q, row_tiles, splits;
+    bool in_turn;
     int window, sinks;
     float scale2;  // scale * log2(e)
     float* part_o;   // [T * q_heads][splits][D]
@@ -224,193 +225,122 @@ __device__ __forceinline__ void pages_of(const AttnArgs& a, const Entries& x, in
     }
 }
 
-template <int D, int kNB, int kWaves, bool kWide>
-__global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
-    constexpr int kG = Frag<D>::kG, kW = Frag<D>::kW;
-    constexpr int kJ = D == 64 ? 4 : 8;  // blocks of 16 d per group
-    constexpr int kCols = 16 * kNB;
-    __shared__ float so[kWaves / 2][kCols][D + 4];
-    __shared__ float sm[kWaves][kCols], sl[kWaves][kCols];
+// What a wave holds of its 16 * kNB rows: queries, running softmax and outputs.
+// A lane's rows are those of its column (lane % 16) of each block of 16; of
+// the tokens and of the outputs it has the share of its lane / 16.
+template <int D, int kNB>
+struct Rows {
+    static constexpr int kG = Frag<D>::kG, kW = Frag<D>::kW;
+    static constexpr int kJ = D == 64 ? 4 : 8;  // blocks of 16 d per group
 
-    const int lane = threadIdx.x & (kWave - 1), wave = (int)sgpr(threadIdx.x / kWave);
-    const int c = lane & 15, g = lane >> 4;
-    // key/value heads innermost: workgroups that share a head's pages meet on one XCD
-    int id = blockIdx.x;
-    const int head = id % a.c.heads;
-    id /= a.c.heads;
-    const int split = id % a.splits;
-    id /= a.splits;
-    const int row_tile = a.row_tiles - 1 - id % a.row_tiles;  // the longest first
-    const int b = id / a.row_tiles;
-
-    const Request req = request_of(a, b);
-    const int rows = min(req.rows, a.max_q) * a.g;  // < 2^31: checked on the host
-    const int r0 = row_tile * kCols;
-    if (r0 >= rows) return;
-    const int first_pos = req.kv - req.rows;
-    const int low = first_pos + r0 / a.g, high = first_pos + (min(r0 + kCols, rows) - 1) / a.g;
-    const Tiles tiles = tiles_of(a, low, high);
-    const table_ptr table = as_table(a.table + (size_t)b * a.width);
-
-    // this split's tiles, in turn over the waves
-    const int per = (tiles.count + a.splits - 1) / a.splits;
-    const int v1 = min(tiles.count, (split + 1) * per);
-    int v = split * per + wave;
-    const bool any = v < v1 && a.width > 0;
-    const auto clamped = [&](int x) { return x < v1 ? x : v1 - 1; };
-
-    // this lane's rows (past the last one: that one again, unseen) and their
-    // queries, on their way before the first tile
-    int pos[kNB];
+    int pos[kNB];  // -1: sees nothing
     u32x4_t xq[kNB][kG][kW];
-#pragma unroll
-    for (int n = 0; n < kNB; ++n) {
-        const int mine = r0 + 16 * n + c, r = min(mine, rows - 1);
-        pos[n] = mine < rows ? max(first_pos + r / a.g, -1) : -1;
-        const uint16_t* src = a.q + (int64_t)(req.first + r / a.g) * a.q_stride + (size_t)(head * a.g + r % a.g) * D;
-#pragma unroll
-        for (int q = 0; q < kG; ++q)
-#pragma unroll
-            for (int i = 0; i < kW; ++i)
-                xq[n][q][i] = *reinterpret_cast<const u32x4_t*>(src + q * W4_KV4_GROUP + (kW * g + i) * 8);
-    }
-    const Offsets offs = offsets_of<D>(lane);
-    Frag<D> f;
-    int page[2] = {-1, -1};
-    Entries next = {};
-    if (any) {
-        const Entries now = entries_of<kWide>(a, table, tiles.at(v) * kTile);
-        next = entries_of<kWide>(a, table, tiles.at(clamped(v + kWaves)) * kTile);
-        pages_of<kWide>(a, now, tiles.at(v) * kTile, high, page);
-        const Place<kWide> p = place_of<D, kWide>(a, tiles.at(v) * kTile, head, page);
-        load_keys<D, kWide>(a, f, p, offs);
-        load_values<D, kWide>(a, f, p, offs);
-    }
-    // the queries as the score product's operand, and their sums
-    f32x4_t xstart[kNB][kG];
-    float xs[kNB][kG];
-#pragma unroll
-    for (int n = 0; n < kNB; ++n) {
-#pragma unroll
-        for (int q = 0; q < kG; ++q) {
-            float sum = 0;
-#pragma unroll
-            for (int i = 0; i < kW; ++i) {
-                const u32x4_t w = xq[n][q][i];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sum += bf16_to_f32(w[e] & 0xFFFFu) + __builtin_bit_cast(float, w[e] & 0xFFFF0000u);
-                uint32_t in[4] = {w.x, w.y, w.z, w.w}, pr[4];
-                x_pairs_for_biased(in, pr);
-                xq[n][q][i] = u32x4_t{pr[0], pr[1], pr[2], pr[3]};
-            }
-            xs[n][q] = row_sum(sum);
-            const float x0 = -128.0f * xs[n][q];
-            xstart[n][q] = f32x4_t{x0, x0, x0, x0};
-        }
-    }
-
+    f32x4_t xstart[kNB][kG];  // -128 X
+    float xs[kNB][kG];        // X
     f32x4_t o[kNB][kG][kJ], ones_sum[kNB][kG];  // of ones_sum only element 0 counts
     float extra[kNB][kG], m[kNB], l[kNB];
     float means[kNB][kG], scales[kNB][kG];  // sums of p m and p s since the last settling
+    u32x4_t pop[kNB][kG];  // p s of the tile, the second product's operand
+
+    // Sends for the queries of rows r0 ..; past the last row that one again, unseen.
+    __device__ __forceinline__ void fetch(const AttnArgs& a, const Request& req, int head, int r0, int rows, int lane) {
+        const int c = lane & 15, g = lane >> 4, first_pos = req.kv - req.rows;
 #pragma unroll
-    for (int n = 0; n < kNB; ++n) {
-        m[n] = -INFINITY;
-        l[n] = 0;
+        for (int n = 0; n < kNB; ++n) {
+            const int mine = r0 + 16 * n + c, r = min(mine, rows - 1);
+            pos[n] = mine < rows ? max(first_pos + r / a.g, -1) : -1;
+            const uint16_t* src = a.q + (int64_t)(req.first + r / a.g) * a.q_stride + (size_t)(head * a.g + r % a.g) * D;
 #pragma unroll
-        for (int q = 0; q < kG; ++q) {
-            extra[n][q] = means[n][q] = scales[n][q] = 0;
-            ones_sum[n][q] = f32x4_t{0, 0, 0, 0};
+            for (int q = 0; q < kG; ++q)
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) o[n][q][j] = f32x4_t{0, 0, 0, 0};
+                for (int i = 0; i < kW; ++i)
+                    xq[n][q][i] = *reinterpret_cast<const u32x4_t*>(src + q * W4_KV4_GROUP + (kW * g + i) * 8);
         }
     }
 
-    // The running maximum moves only when a score passes it by 2^8: weights up
-    // to 256 lose nothing, and a move costs a pass over the outputs.
-    const float slack = 8.0f / a.scale2;
-    const uint32_t bias = vgpr_const(kInt4BiasPair);
-    const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-    // takes 136 times the weights' sum off the outputs; p (m + 8 s) so far
-    const auto settle = [&]() {
+    // The queries as the score product's operand, their sums; empty outputs.
+    __device__ __forceinline__ void start() {
+#pragma unroll
+        for (int n = 0; n < kNB; ++n) {
+            m[n] = -INFINITY;
+            l[n] = 0;
+#pragma unroll
+            for (int q = 0; q < kG; ++q) {
+                float sum = 0;
+#pragma unroll
+                for (int i = 0; i < kW; ++i) {
+                    const u32x4_t w = xq[n][q][i];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum += bf16_to_f32(w[e] & 0xFFFFu) + __builtin_bit_cast(float, w[e] & 0xFFFF0000u);
+                    uint32_t in[4] = {w.x, w.y, w.z, w.w}, pr[4];
+                    x_pairs_for_biased(in, pr);
+                    xq[n][q][i] = u32x4_t{pr[0], pr[1], pr[2], pr[3]};
+                }
+                xs[n][q] = row_sum(sum);
+                const float x0 = -128.0f * xs[n][q];
+                xstart[n][q] = f32x4_t{x0, x0, x0, x0};
+                extra[n][q] = means[n][q] = scales[n][q] = 0;
+                ones_sum[n][q] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) o[n][q][j] = f32x4_t{0, 0, 0, 0};
+            }
+        }
+    }
+
+    // Scores of a tile, from key(h, q, i): the operand of half h's word i of group q.
+    // Word by word over halves and groups, so that products that follow each
+    // other do not wait for each other.
+    template <int kAhead, typename F>
+    __device__ __forceinline__ void scores(float s[kNB][2][4], F key, const u32x4_t km[2][kG]) {
+        f32x4_t acc[kNB][2][kG];
+#pragma unroll
+        for (int i = 0; i < kW; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int q = 0; q < kG; ++q) {
+                    const u32x4_t kop = key(h, q, i);
+#pragma unroll
+                    for (int n = 0; n < kNB; ++n)
+                        acc[n][h][q] = mfma(kop, xq[n][q][i], i == 0 ? xstart[n][q] : acc[n][h][q]);
+                }
+        if constexpr (kAhead > 0) in_order<2 * kG * kW, kAhead, kNB>();
 #pragma unroll
         for (int n = 0; n < kNB; ++n)
 #pragma unroll
-            for (int q = 0; q < kG; ++q) {
-                const float off = -136.0f * ones_sum[n][q][0];
-                ones_sum[n][q] = f32x4_t{0, 0, 0, 0};
-                extra[n][q] += fmaf(8.0f, scales[n][q], means[n][q]);
-                means[n][q] = scales[n][q] = 0;
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int j = 0; j < kJ; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) o[n][q][j][r] += off;
-            }
-    };
-    const uint32_t half_sel = (D == 64 && (c & 1)) ? 0x07060302u : 0x05040100u;
-
-    // The next tile's keys are fetched when the scores are done with this
-    // one's, its values behind the outputs; page numbers a tile earlier.  The
-    // last tile fetches itself again: under a condition the compiler would
-    // load into other registers and wait for them to copy them over.
-    int t0 = tiles.at(clamped(v)) * kTile, t1 = tiles.at(clamped(v + kWaves)) * kTile;
-    if (!any) v = v1;
-    for (int done = 1; v < v1; v += kWaves, ++done) {
-        int coming[2];
-        pages_of<kWide>(a, next, t1, high, coming);
-        const Place<kWide> ahead = place_of<D, kWide>(a, t1, head, coming);
-        const int t2 = tiles.at(clamped(v + 2 * kWaves)) * kTile;
-        next = entries_of<kWide>(a, table, t2);
-        // Whether every row sees every token of the tile.
-        const bool whole = t0 + kTile - 1 <= low && (a.window == 0 || t0 > high - a.window || t0 + kTile <= a.sinks) &&
-                           page[0] >= 0 && page[1] >= 0 && r0 + kCols <= rows;
-
-        // scores
-        float s[kNB][2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int q = 0; q < kG; ++q) {
-                u32x4_t kop[kW];
-#pragma unroll
-                for (int i = 0; i < kW; ++i) kop[i] = key_operand(f.k[h][q][i], bias);
-#pragma unroll
-                for (int n = 0; n < kNB; ++n) {
-                    f32x4_t acc = xstart[n][q];
-#pragma unroll
-                    for (int i = 0; i < kW; ++i) acc = mfma(kop[i], xq[n][q][i], acc);
+                for (int q = 0; q < kG; ++q)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float base = q == 0 ? 0.0f : s[n][h][r];
-                        s[n][h][r] = fmaf(lo16(f.km[h][q][r]), acc[r], fmaf(hi16(f.km[h][q][r]), xs[n][q], base));
+                        s[n][h][r] = fmaf(lo16(km[h][q][r]), acc[n][h][q][r], fmaf(hi16(km[h][q][r]), xs[n][q], base));
                     }
-                }
-            }
-        }
-        __builtin_amdgcn_sched_barrier(0);  // else loads above the last use of these registers land in others
-        load_keys<D, kWide>(a, f, ahead, offs);
-        __builtin_amdgcn_sched_barrier(0);
-        uint32_t seen[kNB];  // bit 4 h + r
-#pragma unroll
-        for (int n = 0; n < kNB; ++n) seen[n] = 0xFFu;
-        if (!whole) {
-#pragma unroll
-            for (int n = 0; n < kNB; ++n) {
-                seen[n] = 0;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int t = t0 + 16 * h + 4 * g + r;
-                        // no short cuts: branches would cost more than the comparisons
-                        const bool see = (t <= pos[n]) & ((a.window == 0) | (t > pos[n] - a.window) | (t < a.sinks));
-                        if (see) seen[n] |= 1u << (4 * h + r);
-                        s[n][h][r] = !see ? -INFINITY : page[h] < 0 ? NAN : s[n][h][r];
-                    }
-            }
-        }
+    }
 
-        // softmax and the second product's operand, per row block
-        u32x4_t pop[kNB][kG];
+    // Takes scores a row does not see out (and makes those of a bad page NaN);
+    // seen: bit 4 h + r.
+    __device__ __forceinline__ void mask(const AttnArgs& a, float s[kNB][2][4], uint32_t seen[kNB], int t0,
+                                         const int page[2], int g) {
+#pragma unroll
+        for (int n = 0; n < kNB; ++n) {
+            seen[n] = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = t0 + 16 * h + 4 * g + r;
+                    // no short cuts: branches would cost more than the comparisons
+                    const bool see = (t <= pos[n]) & ((a.window == 0) | (t > pos[n] - a.window) | (t < a.sinks));
+                    if (see) seen[n] |= 1u << (4 * h + r);
+                    s[n][h][r] = !see ? -INFINITY : page[h] < 0 ? NAN : s[n][h][r];
+                }
+        }
+    }
+
+    // Softmax weights of the tile, and with the values' scales the operand pop.
+    __device__ __forceinline__ void weigh(const float s[kNB][2][4], const u32x4_t vm[2][kG], bool whole,
+                                          const uint32_t seen[kNB], float scale2, float slack) {
 #pragma unroll
         for (int n = 0; n < kNB; ++n) {
             float top = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
@@ -418,7 +348,7 @@ __global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
             top = row_max(top);
             if (__any(top > m[n] + slack)) {
                 const float now = fmaxf(m[n], top);
-                const float keep = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[n] - now) * a.scale2);
+                const float keep = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[n] - now) * scale2);
                 m[n] = now;
                 l[n] *= keep;
 #pragma unroll
@@ -433,17 +363,17 @@ __global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
                         for (int r = 0; r < 4; ++r) o[n][q][j][r] *= keep;
                 }
             }
-            const float base = m[n] == -INFINITY ? 0.0f : m[n] * a.scale2;
+            const float base = m[n] == -INFINITY ? 0.0f : m[n] * scale2;
             float p[2][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    p[h][r] = __builtin_amdgcn_exp2f(fmaf(s[n][h][r], a.scale2, -base));
+                    p[h][r] = __builtin_amdgcn_exp2f(fmaf(s[n][h][r], scale2, -base));
                     l[n] += p[h][r];
                 }
             // what a row does not see may hold anything, an infinity or a NaN too
-            const auto weigh = [&](auto masked) {
+            const auto by_scale = [&](auto masked) {
 #pragma unroll
                 for (int q = 0; q < kG; ++q) {
                     float ps[2][4];
@@ -451,83 +381,278 @@ __global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            uint32_t meta = f.vm[h][q][r];
+                            uint32_t meta = vm[h][q][r];
                             if constexpr (masked.value) meta = seen[n] >> (4 * h + r) & 1 ? meta : 0;
                             ps[h][r] = p[h][r] * lo16(meta);
                             means[n][q] = fmaf(p[h][r], hi16(meta), means[n][q]);
                             scales[n][q] += ps[h][r];
                         }
-                    // here, not put off behind the loads that reuse f.vm's registers
+                    // here, not put off behind the loads that reuse vm's registers
                     asm volatile("" : "+v"(means[n][q]), "+v"(scales[n][q]));
                     pop[n][q] = u32x4_t{pack_bf16x2(ps[0][0], ps[0][1]), pack_bf16x2(ps[0][2], ps[0][3]),
                                         pack_bf16x2(ps[1][0], ps[1][1]), pack_bf16x2(ps[1][2], ps[1][3])};
                 }
             };
             if (whole) {
-                weigh(std::false_type{});
+                by_scale(std::false_type{});
             } else {
-                weigh(std::true_type{});
+                by_scale(std::true_type{});
             }
         }
+    }
 
-        // outputs
+    // Adds the tile's values, from value(q, j): the operand of block j of group q.
+    // kAhead: how many operands are read from LDS ahead of their products (0:
+    // none are).
+    template <int kAhead, typename F>
+    __device__ __forceinline__ void outputs(F value, const u32x4_t& ones) {
 #pragma unroll
         for (int q = 0; q < kG; ++q) {
 #pragma unroll
-            for (int z = 0; z < (D == 64 ? 1 : 2); ++z) {
-                // codes 4 z .. 4 z + 3 of each token pair, one token in each half
-                uint32_t pr[4];
-                const uint32_t sel = D == 64 ? half_sel : z ? 0x07060302u : 0x05040100u;
+            for (int j = 0; j < kJ; ++j) {
+                const u32x4_t vop = value(q, j);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const u32x4_t w = f.v[i >> 1][q];
-                    pr[i] = __builtin_amdgcn_perm(w[2 * (i & 1) + 1], w[2 * (i & 1)], sel);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    u32x4_t vop;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) vop[i] = ((pr[i] >> (4 * j)) & 0x000F000Fu) | bias;
-#pragma unroll
-                    for (int n = 0; n < kNB; ++n)
-                        o[n][q][4 * z + j] = mfma(vop, pop[n][q], o[n][q][4 * z + j]);
-                }
+                for (int n = 0; n < kNB; ++n) o[n][q][j] = mfma(vop, pop[n][q], o[n][q][j]);
             }
 #pragma unroll
             for (int n = 0; n < kNB; ++n) ones_sum[n][q] = mfma(ones, pop[n][q], ones_sum[n][q]);
         }
+        if constexpr (kAhead > 0) in_order<kG * kJ, kAhead, kNB>();
+    }
+
+    // Asks the scheduler for kAhead reads from LDS, then a read after each
+    // kEach products: left alone it reads an operand just before its use.
+    template <int kReads, int kAhead, int kEach>
+    static __device__ __forceinline__ void in_order() {
+        constexpr int kRead = 0x100, kProduct = 0x008;
+        __builtin_amdgcn_sched_group_barrier(kRead, kAhead, 0);
+#pragma unroll
+        for (int i = 0; i < kReads - kAhead; ++i) {
+            __builtin_amdgcn_sched_group_barrier(kProduct, kEach, 0);
+            __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(kProduct, kAhead * kEach, 0);
+    }
+
+    // Takes 136 times the weights' sum off the outputs; p (m + 8 s) so far.
+    __device__ __forceinline__ void settle() {
+#pragma unroll
+        for (int n = 0; n < kNB; ++n)
+#pragma unroll
+            for (int q = 0; q < kG; ++q) {
+                const float off = -136.0f * ones_sum[n][q][0];
+                ones_sum[n][q] = f32x4_t{0, 0, 0, 0};
+                extra[n][q] += fmaf(8.0f, scales[n][q], means[n][q]);
+                means[n][q] = scales[n][q] = 0;
+#pragma unroll
+                for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[n][q][j][r] += off;
+            }
+    }
+
+    // Sums over a row's four lanes: its outputs and weights are whole after that.
+    __device__ __forceinline__ void finish(const AttnArgs& a) {
+        settle();
+#pragma unroll
+        for (int n = 0; n < kNB; ++n) {
+            l[n] = row_sum(l[n]);
+            if (a.width <= 0 && pos[n] >= 0) l[n] = NAN;  // no table: what the row sees lies past it
+#pragma unroll
+            for (int q = 0; q < kG; ++q) {
+                const float e = row_sum(extra[n][q]);
+#pragma unroll
+                for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[n][q][j][r] += e;
+            }
+        }
+    }
+
+    // d of (q, j, r) is this + j: 128 q + 8 (4 g + r), or 4 (4 g + r) for heads of 64
+    static __device__ __forceinline__ int place(int q, int r, int g) {
+        return D == 64 ? 4 * (4 * g + r) : q * W4_KV4_GROUP + 8 * (4 * g + r);
+    }
+
+    // The rows' results, or with splits their part.
+    __device__ __forceinline__ void store(const AttnArgs& a, const Request& req, int head, int split, int r0, int rows,
+                                          int lane) const {
+        const int c = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int n = 0; n < kNB; ++n) {
+            const int row = r0 + 16 * n + c;
+            if (row >= rows) continue;
+            const int t = req.first + row / a.g, h = head * a.g + row % a.g;
+            if (a.splits == 1) {
+                const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
+                uint16_t* dst = a.out + (int64_t)t * a.out_stride + (size_t)h * D;
+#pragma unroll
+                for (int q = 0; q < kG; ++q)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        uint32_t w[kJ / 2];
+#pragma unroll
+                        for (int j = 0; j < kJ; j += 2)
+                            w[j / 2] = pack_bf16x2(o[n][q][j][r] * inv, o[n][q][j + 1][r] * inv);
+                        if constexpr (kJ == 8) {
+                            *reinterpret_cast<u32x4_t*>(dst + place(q, r, g)) = u32x4_t{w[0], w[1], w[2], w[3]};
+                        } else {
+                            *reinterpret_cast<u32x2_t*>(dst + place(q, r, g)) = u32x2_t{w[0], w[1]};
+                        }
+                    }
+            } else {
+                const size_t at = ((size_t)t * a.g * a.c.heads + h) * a.splits + split;
+                if (g == 0) {
+                    a.part_ml[2 * at] = m[n];
+                    a.part_ml[2 * at + 1] = l[n];
+                }
+                float* dst = a.part_o + at * D;
+#pragma unroll
+                for (int q = 0; q < kG; ++q)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int j = 0; j < kJ; j += 4)
+                            *reinterpret_cast<f32x4_t*>(dst + place(q, r, g) + j) =
+                                f32x4_t{o[n][q][j][r], o[n][q][j + 1][r], o[n][q][j + 2][r], o[n][q][j + 3][r]};
+            }
+        }
+    }
+};
+
+// The operand of block j of a group's values, from the words of a lane's eight
+// tokens: codes j % 4 + 4 z of each, a token in each half of a register.
+template <int D>
+__device__ __forceinline__ u32x4_t value_operand(const u32x4_t& first, const u32x4_t& second, int j, int c, uint32_t bias) {
+    const uint32_t sel = D == 64 ? ((c & 1) ? 0x07060302u : 0x05040100u) : j >= 4 ? 0x07060302u : 0x05040100u;
+    u32x4_t op;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const u32x4_t& w = i < 2 ? first : second;
+        const uint32_t pair = __builtin_amdgcn_perm(w[2 * (i & 1) + 1], w[2 * (i & 1)], sel);
+        op[i] = ((pair >> (4 * (j % 4))) & 0x000F000Fu) | bias;
+    }
+    return op;
+}
+
+// Where a workgroup's work lies.
+struct Share {
+    int head, split, row_tile, b;
+};
+__device__ __forceinline__ Share share_of(const AttnArgs& a) {
+    // key/value heads innermost: workgroups that share a head's pages meet on one XCD
+    int id = blockIdx.x;
+    Share s;
+    s.head = id % a.c.heads;
+    id /= a.c.heads;
+    s.split = id % a.splits;
+    id /= a.splits;
+    // Late rows see most tokens.  Where all workgroups are on the chip at once
+    // (two a compute unit, the second 256 after the first) the second half
+    // goes the other way, so that a long one shares its unit with a short
+    // one; else the longest come first.
+    const int t = id % a.row_tiles;
+    s.row_tile = a.in_turn && 2 * t >= a.row_tiles ? t - (a.row_tiles + 1) / 2 : a.row_tiles - 1 - t;
+    s.b = id / a.row_tiles;
+    return s;
+}
+
+// Few rows: the waves take a row tile's token tiles in turn.
+template <int D, int kNB, int kWaves, bool kWide>
+__global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
+    typedef Rows<D, kNB> R;
+    constexpr int kG = R::kG, kJ = R::kJ, kCols = 16 * kNB;
+    __shared__ float so[kWaves / 2][kCols][D + 4];
+    __shared__ float sm[kWaves][kCols], sl[kWaves][kCols];
+
+    const int lane = threadIdx.x & (kWave - 1), wave = (int)sgpr(threadIdx.x / kWave);
+    const int c = lane & 15, g = lane >> 4;
+    const Share mine = share_of(a);
+    const int head = mine.head;
+    const Request req = request_of(a, mine.b);
+    const int rows = min(req.rows, a.max_q) * a.g;  // < 2^31: checked on the host
+    const int r0 = mine.row_tile * kCols;
+    if (r0 >= rows) return;
+    const int first_pos = req.kv - req.rows;
+    const int low = first_pos + r0 / a.g, high = first_pos + (min(r0 + kCols, rows) - 1) / a.g;
+    const Tiles tiles = tiles_of(a, low, high);
+    const table_ptr table = as_table(a.table + (size_t)mine.b * a.width);
+
+    // this split's tiles, in turn over the waves
+    const int per = (tiles.count + a.splits - 1) / a.splits;
+    const int v1 = min(tiles.count, (mine.split + 1) * per);
+    int v = mine.split * per + wave;
+    const bool any = v < v1 && a.width > 0;
+    const auto clamped = [&](int x) { return x < v1 ? x : v1 - 1; };
+
+    R rw;
+    rw.fetch(a, req, head, r0, rows, lane);
+    const Offsets offs = offsets_of<D>(lane);
+    Frag<D> f;
+    int page[2] = {-1, -1};
+    Entries next = {};
+    int t0 = 0, t1 = 0;
+    if (any) {
+        t0 = tiles.at(v) * kTile;
+        t1 = tiles.at(clamped(v + kWaves)) * kTile;
+        const Entries now = entries_of<kWide>(a, table, t0);
+        next = entries_of<kWide>(a, table, t1);
+        pages_of<kWide>(a, now, t0, high, page);
+        const Place<kWide> p = place_of<D, kWide>(a, t0, head, page);
+        load_keys<D, kWide>(a, f, p, offs);
+        load_values<D, kWide>(a, f, p, offs);
+    } else {
+        v = v1;
+    }
+    rw.start();
+
+    // The running maximum moves only when a score passes it by 2^8: weights up
+    // to 256 lose nothing, and a move costs a pass over the outputs.
+    const float slack = 8.0f / a.scale2;
+    const uint32_t bias = vgpr_const(kInt4BiasPair);
+    const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    // The next tile's keys are fetched when the scores are done with this
+    // one's, its values behind the outputs; page numbers a tile earlier.  The
+    // last tile fetches itself again: under a condition the compiler would
+    // load into other registers and wait for them to copy them over.
+    for (int done = 1; v < v1; v += kWaves, ++done) {
+        int coming[2];
+        pages_of<kWide>(a, next, t1, high, coming);
+        const Place<kWide> ahead = place_of<D, kWide>(a, t1, head, coming);
+        const int t2 = tiles.at(clamped(v + 2 * kWaves)) * kTile;
+        next = entries_of<kWide>(a, table, t2);
+        // Whether every row sees every token of the tile.
+        const bool whole = t0 + kTile - 1 <= low && (a.window == 0 || t0 > high - a.window || t0 + kTile <= a.sinks) &&
+                           page[0] >= 0 && page[1] >= 0 && r0 + kCols <= rows;
+
+        float s[kNB][2][4];
+        rw.template scores<0>(s, [&](int h, int q, int i) { return key_operand(f.k[h][q][i], bias); }, f.km);
+        __builtin_amdgcn_sched_barrier(0);  // else loads above the last use of these registers land in others
+        load_keys<D, kWide>(a, f, ahead, offs);
+        __builtin_amdgcn_sched_barrier(0);
+        uint32_t seen[kNB];
+#pragma unroll
+        for (int n = 0; n < kNB; ++n) seen[n] = 0xFFu;
+        if (!whole) rw.mask(a, s, seen, t0, page, g);
+        rw.weigh(s, f.vm, whole, seen, a.scale2, slack);
+        rw.template outputs<0>([&](int q, int j) { return value_operand<D>(f.v[0][q], f.v[1][q], j, c, bias); }, ones);
         __builtin_amdgcn_sched_barrier(0);
         load_values<D, kWide>(a, f, ahead, offs);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            page[h] = coming[h];
-        }
+        for (int h = 0; h < 2; ++h) page[h] = coming[h];
         t0 = t1;
         t1 = t2;
-        if (done % 8 == 0) settle();
+        if (done % 8 == 0) rw.settle();
     }
-    settle();
+    rw.finish(a);
 
-    // each wave's own part, whole over its tokens
-#pragma unroll
-    for (int n = 0; n < kNB; ++n) {
-        l[n] = row_sum(l[n]);
-#pragma unroll
-        for (int q = 0; q < kG; ++q) {
-            const float e = row_sum(extra[n][q]);
-#pragma unroll
-            for (int j = 0; j < kJ; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[n][q][j][r] += e;
-        }
-    }
     // join the waves: common maximum, then pairwise through LDS
     if (lane < 16) {
 #pragma unroll
         for (int n = 0; n < kNB; ++n) {
-            sm[wave][16 * n + c] = m[n];
-            sl[wave][16 * n + c] = l[n];
+            sm[wave][16 * n + c] = rw.m[n];
+            sl[wave][16 * n + c] = rw.l[n];
         }
     }
     __syncthreads();
@@ -545,19 +670,17 @@ __global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
             const float lw = sl[w][col];
             sum += lw == 0.0f ? 0.0f : lw * weight(sm[w][col]);
         }
-        const float mine = l[n] == 0.0f ? 0.0f : weight(m[n]);
-        l[n] = sum;
-        m[n] = now;
+        const float scale = rw.l[n] == 0.0f ? 0.0f : weight(rw.m[n]);
+        rw.l[n] = sum;
+        rw.m[n] = now;
 #pragma unroll
         for (int q = 0; q < kG; ++q)
 #pragma unroll
             for (int j = 0; j < kJ; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) o[n][q][j][r] *= mine;
+                for (int r = 0; r < 4; ++r) rw.o[n][q][j][r] *= scale;
     }
-    // d of (q, j, r): 128 q + 8 (4 g + r) + j, or 4 (4 g + r) + j for heads of 64
-    const auto place = [&](int q, int r) { return D == 64 ? 4 * (4 * g + r) : q * W4_KV4_GROUP + 8 * (4 * g + r); };
-    const auto put = [&](int slot) {
+    const auto exchange = [&](int slot, auto put) {
 #pragma unroll
         for (int n = 0; n < kNB; ++n)
 #pragma unroll
@@ -565,66 +688,196 @@ __global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
 #pragma unroll
-                    for (int j = 0; j < kJ; ++j) so[slot][16 * n + c][place(q, r) + j] = o[n][q][j][r];
-    };
-    const auto take = [&](int slot) {
-#pragma unroll
-        for (int n = 0; n < kNB; ++n)
-#pragma unroll
-            for (int q = 0; q < kG; ++q)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int j = 0; j < kJ; ++j) o[n][q][j][r] += so[slot][16 * n + c][place(q, r) + j];
+                    for (int j = 0; j < kJ; ++j) {
+                        float& x = so[slot][16 * n + c][R::place(q, r, g) + j];
+                        if constexpr (put.value) {
+                            x = rw.o[n][q][j][r];
+                        } else {
+                            rw.o[n][q][j][r] += x;
+                        }
+                    }
     };
 #pragma unroll
     for (int step = 1; step < kWaves; step *= 2) {
         const int pair = wave / (2 * step);
-        if (wave % (2 * step) == step) put(pair);
+        if (wave % (2 * step) == step) exchange(pair, std::true_type{});
         __syncthreads();
-        if (wave % (2 * step) == 0) take(pair);
+        if (wave % (2 * step) == 0) exchange(pair, std::false_type{});
         if (2 * step < kWaves) __syncthreads();
     }
-    if (wave != 0) return;
+    if (wave == 0) rw.store(a, req, head, mine.split, r0, rows, lane);
+}
 
+// Waits for a workgroup's LDS accesses and meets the others; loads from
+// memory stay on their way.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Many rows (prompts): four waves with rows of their own against the same
+// tiles.  Unpacking a tile costs the vector unit as much as 16 rows' softmax
+// does, so each wave unpacks a quarter of it, and the operands go through LDS,
+// a register's 64 lanes together (16 bytes a lane, no conflicts either way).
+// Two buffers: while a tile is worked on, the next one is unpacked and the
+// one after is on its way from memory.
+template <int D, int kNB, bool kWide>
+__global__ __launch_bounds__(256, 2) void kv4_attn_many_kernel(AttnArgs a) {
+    typedef Rows<D, kNB> R;
+    constexpr int kWaves = 4, kG = R::kG, kW = R::kW, kJ = R::kJ, kCols = 16 * kNB;
+    constexpr int kKeys = 2 * kG * kW, kValues = kG * kJ;  // operands of a tile
+    constexpr int kMyKeys = kKeys / kWaves, kMyValues = kValues / kWaves;
+    constexpr int kAheadKeys = kKeys < 6 ? kKeys : 6, kAheadValues = kValues < 8 ? kValues : 8;
+    __shared__ u32x4_t ops[2][kKeys + kValues][kWave];
+
+    const int lane = threadIdx.x & (kWave - 1), wave = (int)sgpr(threadIdx.x / kWave);
+    const int c = lane & 15, g = lane >> 4;
+    const Share mine = share_of(a);
+    const int head = mine.head;
+    const Request req = request_of(a, mine.b);
+    const int rows = min(req.rows, a.max_q) * a.g;
+    const int base = mine.row_tile * kWaves * kCols;
+    if (base >= rows) return;
+    const int first_pos = req.kv - req.rows;
+    const int high = first_pos + (min(base + kWaves * kCols, rows) - 1) / a.g;
+    const Tiles tiles = tiles_of(a, first_pos + base / a.g, high);
+    const table_ptr table = as_table(a.table + (size_t)mine.b * a.width);
+    // this wave's rows; past the last there may be none
+    const int r0 = min(base + wave * kCols, rows);
+    const int my_low = first_pos + min(r0, rows - 1) / a.g, my_high = first_pos + (min(r0 + kCols, rows) - 1) / a.g;
+
+    const int per = (tiles.count + a.splits - 1) / a.splits;
+    int v = mine.split * per;
+    const int v1 = min(tiles.count, v + per);
+    if (a.width <= 0) v = v1;
+    const auto tile_at = [&](int x) { return tiles.at(max(min(x, v1 - 1), 0)) * kTile; };
+
+    R rw;
+    rw.fetch(a, req, head, r0, rows, lane);
+    const Offsets offs = offsets_of<D>(lane);
+    const uint32_t bias = vgpr_const(kInt4BiasPair);
+
+    // A wave's part: kMyKeys words of one half and group, and kMyValues blocks
+    // of one group (for which it needs the words of all 32 tokens).
+    const int kh = wave * kMyKeys / (kG * kW), kq = wave * kMyKeys / kW % kG, kw = wave * kMyKeys % kW;
+    const int vq = wave * kMyValues / kJ, vj = wave * kMyValues % kJ;
+    uint32_t raw_k[kMyKeys];
+    u32x4_t raw_v[2];
+    const auto fetch_codes = [&](const Place<kWide>& p) {
+        const uint64_t key = kWide ? p.code[0] + kh * 16 * (D / 2) : p.code[kh % Place<kWide>::kN];
+        if constexpr (kMyKeys == 4) {
+            const u32x4_t w = fetch<u32x4_t>(a.c.kc, key + kq * 64, offs.k);
 #pragma unroll
-    for (int n = 0; n < kNB; ++n) {
-        const int row = r0 + 16 * n + c;
-        if (row >= rows) continue;
-        const int t = req.first + row / a.g, h = head * a.g + row % a.g;
-        if (a.splits == 1) {
-            const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
-            uint16_t* dst = a.out + (int64_t)t * a.out_stride + (size_t)h * D;
-#pragma unroll
-            for (int q = 0; q < kG; ++q)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    uint32_t w[kJ / 2];
-#pragma unroll
-                    for (int j = 0; j < kJ; j += 2) w[j / 2] = pack_bf16x2(o[n][q][j][r] * inv, o[n][q][j + 1][r] * inv);
-                    if constexpr (kJ == 8) {
-                        *reinterpret_cast<u32x4_t*>(dst + place(q, r)) = u32x4_t{w[0], w[1], w[2], w[3]};
-                    } else {
-                        *reinterpret_cast<u32x2_t*>(dst + place(q, r)) = u32x2_t{w[0], w[1]};
-                    }
-                }
+            for (int i = 0; i < 4; ++i) raw_k[i] = w[i];
+        } else if constexpr (kMyKeys == 2) {
+            const u32x2_t w = fetch<u32x2_t>(a.c.kc, key + kq * 64 + 4 * kw, offs.k);
+            raw_k[0] = w.x;
+            raw_k[1] = w.y;
         } else {
-            const size_t at = ((size_t)t * a.g * a.c.heads + h) * a.splits + split;
-            if (g == 0) {
-                a.part_ml[2 * at] = m[n];
-                a.part_ml[2 * at + 1] = l[n];
+            raw_k[0] = fetch<uint32_t>(a.c.kc, key + 4 * kw, offs.k);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            raw_v[h] = fetch<u32x4_t>(a.c.vc, (kWide ? p.code[0] + h * 16 * (D / 2) : p.code[h % Place<kWide>::kN]) + vq * 256, offs.v);
+    };
+    const auto unpack = [&](int buffer) {
+#pragma unroll
+        for (int i = 0; i < kMyKeys; ++i) ops[buffer][wave * kMyKeys + i][lane] = key_operand(raw_k[i], bias);
+        // the shift by 4 (j % 4) is uniform, but not known here for kMyValues < 4
+#pragma unroll
+        for (int i = 0; i < kMyValues; ++i) {
+            const int j = vj + i;
+            const uint32_t sel = D == 64 ? ((c & 1) ? 0x07060302u : 0x05040100u) : j >= 4 ? 0x07060302u : 0x05040100u;
+            u32x4_t op;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const u32x4_t& w = raw_v[e >> 1];
+                const uint32_t pair = __builtin_amdgcn_perm(w[2 * (e & 1) + 1], w[2 * (e & 1)], sel);
+                op[e] = ((pair >> (4 * (j % 4))) & 0x000F000Fu) | bias;
             }
-            float* dst = a.part_o + at * D;
+            ops[buffer][kKeys + wave * kMyValues + i][lane] = op;
+        }
+    };
+    u32x4_t km[2][kG], vm[2][kG];
+    const auto fetch_meta = [&](const Place<kWide>& p, const uint32_t* from, u32x4_t to[2][kG]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int q = 0; q < kG; ++q)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int j = 0; j < kJ; j += 4)
-                        *reinterpret_cast<f32x4_t*>(dst + place(q, r) + j) =
-                            f32x4_t{o[n][q][j][r], o[n][q][j + 1][r], o[n][q][j + 2][r], o[n][q][j + 3][r]};
-        }
+                to[h][q] = fetch<u32x4_t>(from, (kWide ? p.meta[0] + h * 64 : p.meta[h % Place<kWide>::kN]) +
+                                          (q ? (uint64_t)(4u * q << a.c.shift) : 0), offs.meta);
+    };
+
+    int t0 = 0, t1 = 0, page[2] = {-1, -1}, coming[2] = {-1, -1};
+    Entries next = {};
+    Place<kWide> ahead = {};
+    if (v < v1) {
+        t0 = tile_at(v);
+        t1 = tile_at(v + 1);
+        const Entries now = entries_of<kWide>(a, table, t0), then = entries_of<kWide>(a, table, t1);
+        pages_of<kWide>(a, now, t0, high, page);
+        const Place<kWide> p = place_of<D, kWide>(a, t0, head, page);
+        fetch_codes(p);
+        fetch_meta(p, a.c.km, km);
+        fetch_meta(p, a.c.vm, vm);
+        unpack(0);
+        pages_of<kWide>(a, then, t1, high, coming);
+        ahead = place_of<D, kWide>(a, t1, head, coming);
+        fetch_codes(ahead);
+        next = entries_of<kWide>(a, table, tile_at(v + 2));
     }
+    rw.start();
+    lds_barrier();
+
+    const float slack = 8.0f / a.scale2;
+    const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    for (int done = 1; v < v1; ++v, ++done) {
+        const int buffer = (done - 1) & 1;
+        // the next tile's codes into the other buffer, the one after's sent for
+        // (at the end the last tile again: loads under a condition would be
+        // waited for and copied)
+        unpack(buffer ^ 1);
+        const int t2 = tile_at(v + 2);
+        int after[2];
+        pages_of<kWide>(a, next, t2, high, after);
+        const Place<kWide> place = ahead;
+        ahead = place_of<D, kWide>(a, t2, head, after);
+        next = entries_of<kWide>(a, table, tile_at(v + 3));
+        __builtin_amdgcn_sched_barrier(0);
+        fetch_codes(ahead);
+        __builtin_amdgcn_sched_barrier(0);
+
+        // Rows of a wave that lie before the tile, or before whose window it ends, pass it over.
+        const bool sees = r0 < rows && t0 <= my_high && (a.window == 0 || t0 + kTile - 1 > my_low - a.window || t0 < a.sinks);
+        if (sees) {
+            const bool whole = t0 + kTile - 1 <= my_low && (a.window == 0 || t0 > my_high - a.window || t0 + kTile <= a.sinks) &&
+                               page[0] >= 0 && page[1] >= 0 && r0 + kCols <= rows;
+            float s[kNB][2][4];
+            rw.template scores<kAheadKeys>(s, [&](int h, int q, int i) { return ops[buffer][(h * kG + q) * kW + i][lane]; }, km);
+            uint32_t seen[kNB];
+#pragma unroll
+            for (int n = 0; n < kNB; ++n) seen[n] = 0xFFu;
+            if (!whole) rw.mask(a, s, seen, t0, page, g);
+            rw.weigh(s, vm, whole, seen, a.scale2, slack);
+            rw.template outputs<kAheadValues>([&](int q, int j) { return ops[buffer][kKeys + q * kJ + j][lane]; }, ones);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        fetch_meta(place, a.c.km, km);
+        fetch_meta(place, a.c.vm, vm);
+        __builtin_amdgcn_sched_barrier(0);
+        if (done % 8 == 0) rw.settle();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            page[h] = coming[h];
+            coming[h] = after[h];
+        }
+        t0 = t1;
+        t1 = t2;
+        lds_barrier();
+    }
+    rw.finish(a);
+    if (r0 < rows) rw.store(a, req, head, mine.split, r0, rows, lane);
 }
 
 // Joins the splits of one row, a workgroup a row: D / 4 lanes hold its values,
@@ -689,37 +942,49 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_join_kernel(AttnArgs a) {
         u32x2_t{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
 }
 
+// How a call is cut into workgroups.
+struct Cut {
+    bool many;      // kv4_attn_many_kernel
+    int row_tiles;  // of a request, each a workgroup's rows
+    int splits;     // workgroups that share a row tile's tokens
+};
+constexpr int kFewWaves = 4;
+// 16-row blocks of a wave: as many as leave two waves a SIMD.
+constexpr int many_blocks(int d) { return d == 256 ? 1 : 2; }
+
 #ifndef W4_ATTN_GROUPS
 #define W4_ATTN_GROUPS 512
 #endif
-#ifndef W4_ATTN_WAVES
-#define W4_ATTN_WAVES 4
+#ifndef W4_ATTN_MANY
+#define W4_ATTN_MANY 64
 #endif
-constexpr int kNBDefault = 1;
-
-int row_tiles_of(const w4_attn_args& a, const w4_kv4_cache& c) {
+Cut cut_of(const w4_attn_args& a, const w4_kv4_cache& c) {
+    Cut k;
     const int64_t rows = (int64_t)a.max_q * (a.q_heads / c.kv_heads);
-    return (int)((rows + 16 * kNBDefault - 1) / (16 * kNBDefault));
-}
-
-// How many workgroups share one row tile's tokens: enough to fill the chip
-// twice, at least two tiles for each of a workgroup's waves.
-int splits_of(const w4_attn_args& a, const w4_kv4_cache& c) {
-    const int64_t groups = (int64_t)a.B * c.kv_heads * row_tiles_of(a, c);
+    k.many = rows >= W4_ATTN_MANY;
+    const int tile = k.many ? 64 * many_blocks(c.head_dim) : 16;
+    k.row_tiles = (int)((rows + tile - 1) / tile);
+    // enough workgroups to fill the chip twice, with two tiles at least for
+    // each of the waves that share them
+    const int64_t groups = (int64_t)a.B * c.kv_heads * k.row_tiles;
     int64_t tokens = a.max_kv;
     if (a.window > 0) tokens = tokens < (int64_t)a.window + a.sinks + a.max_q ? tokens : (int64_t)a.window + a.sinks + a.max_q;
     const int64_t tiles = (tokens + kTile - 1) / kTile;
     int64_t want = (W4_ATTN_GROUPS + groups - 1) / (groups > 0 ? groups : 1);
-    const int64_t most = tiles / (2 * W4_ATTN_WAVES);
+    const int64_t most = tiles / (2 * kFewWaves);
     want = want < most ? want : most;
-    return (int)(want < 1 ? 1 : want > kMaxSplits ? kMaxSplits : want);
+    k.splits = (int)(want < 1 ? 1 : want > kMaxSplits ? kMaxSplits : want);
+    return k;
 }
 
 template <int D, bool kWide>
-hipError_t launch_d(AttnArgs& k, int64_t groups, hipStream_t stream) {
-    constexpr int kWaves = W4_ATTN_WAVES;
-    kv4_attn_kernel<D, kNBDefault, kWaves, kWide><<<dim3((unsigned)groups), dim3(kWaves * kWave), 0, stream>>>(k);
-    hipError_t err = hipGetLastError();
+hipError_t launch_d(const AttnArgs& k, bool many, int64_t groups, hipStream_t stream) {
+    if (many) {
+        kv4_attn_many_kernel<D, many_blocks(D), kWide><<<dim3((unsigned)groups), dim3(256), 0, stream>>>(k);
+    } else {
+        kv4_attn_kernel<D, 1, kFewWaves, kWide><<<dim3((unsigned)groups), dim3(kFewWaves * kWave), 0, stream>>>(k);
+    }
+    const hipError_t err = hipGetLastError();
     if (err != hipSuccess || k.splits == 1) return err;
     const int64_t units = (int64_t)k.B * k.max_q * k.g * k.c.heads;
     kv4_attn_join_kernel<D><<<dim3((unsigned)units), dim3(kThreads), 0, stream>>>(k);
@@ -727,14 +992,14 @@ hipError_t launch_d(AttnArgs& k, int64_t groups, hipStream_t stream) {
 }
 
 template <int D>
-hipError_t launch_w(AttnArgs& k, int64_t groups, hipStream_t stream) {
-    return k.c.shift >= 5 ? launch_d<D, true>(k, groups, stream) : launch_d<D, false>(k, groups, stream);
+hipError_t launch_w(const AttnArgs& k, bool many, int64_t groups, hipStream_t stream) {
+    return k.c.shift >= 5 ? launch_d<D, true>(k, many, groups, stream) : launch_d<D, false>(k, many, groups, stream);
 }
 
 }  // namespace
 
 size_t kv4_attn_workspace_bytes(const w4_attn_args& a, const w4_kv4_cache& c) {
-    const int splits = splits_of(a, c);
+    const int splits = cut_of(a, c).splits;
     if (splits == 1) return 0;
     return (size_t)a.T * a.q_heads * splits * (c.head_dim + 2) * sizeof(float);
 }
@@ -754,8 +1019,10 @@ hipError_t launch_kv4_attn(const w4_attn_args& a, const w4_kv4_cache& c, void* w
     k.g = a.q_heads / c.kv_heads;
     k.width = a.max_blocks;
     k.max_q = a.max_q;
-    k.row_tiles = row_tiles_of(a, c);
-    k.splits = splits_of(a, c);
+    const Cut cut = cut_of(a, c);
+    k.row_tiles = cut.row_tiles;
+    k.splits = cut.splits;
+    k.in_turn = cut.many && a.B == 1 && (int64_t)c.kv_heads * k.row_tiles * k.splits <= 512;
     k.window = a.window;
     k.sinks = a.sinks;
     k.scale2 = a.scale * 1.4426950408889634f;
@@ -765,9 +1032,9 @@ hipError_t launch_kv4_attn(const w4_attn_args& a, const w4_kv4_cache& c, void* w
     }
     const int64_t groups = (int64_t)a.B * c.kv_heads * k.row_tiles * k.splits;
     switch (c.head_dim) {
-        case 64: return launch_w<64>(k, groups, stream);
-        case 128: return launch_w<128>(k, groups, stream);
-        default: return launch_w<256>(k, groups, stream);
+        case 64: return launch_w<64>(k, cut.many, groups, stream);
+        case 128: return launch_w<128>(k, cut.many, groups, stream);
+        default: return launch_w<256>(k, cut.many, groups, stream);
     }
 }
 
