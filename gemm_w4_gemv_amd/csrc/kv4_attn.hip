@@ -161,12 +161,11 @@ __device__ __forceinline__ Offsets offsets_of(int lane) {
 }
 
 template <int D, bool kWide>
-__device__ __forceinline__ void load_keys(const AttnArgs& a, Frag<D>& f, const Place<kWide>& p, const Offsets& l) {
+__device__ __forceinline__ void load_key_codes(const AttnArgs& a, Frag<D>& f, const Place<kWide>& p, const Offsets& l) {
     constexpr int kG = Frag<D>::kG, kW = Frag<D>::kW;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint64_t code = kWide ? p.code[0] + h * 16 * (D / 2) : p.code[h % Place<kWide>::kN];
-        const uint64_t meta = kWide ? p.meta[0] + h * 64 : p.meta[h % Place<kWide>::kN];
 #pragma unroll
         for (int q = 0; q < kG; ++q) {
             if constexpr (kW == 4) {
@@ -178,24 +177,39 @@ __device__ __forceinline__ void load_keys(const AttnArgs& a, Frag<D>& f, const P
                 f.k[h][q][0] = w.x;
                 f.k[h][q][1] = w.y;
             }
-            f.km[h][q] = fetch<u32x4_t>(a.c.km, meta + (q ? (uint64_t)(4u * q << a.c.shift) : 0), l.meta);
         }
     }
 }
-
 template <int D, bool kWide>
-__device__ __forceinline__ void load_values(const AttnArgs& a, Frag<D>& f, const Place<kWide>& p, const Offsets& l) {
-    constexpr int kG = Frag<D>::kG;
+__device__ __forceinline__ void load_value_codes(const AttnArgs& a, Frag<D>& f, const Place<kWide>& p, const Offsets& l) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint64_t code = kWide ? p.code[0] + h * 16 * (D / 2) : p.code[h % Place<kWide>::kN];
+#pragma unroll
+        for (int q = 0; q < Frag<D>::kG; ++q) f.v[h][q] = fetch<u32x4_t>(a.c.vc, code + q * 256, l.v);
+    }
+}
+// The (s, m) pairs of a tile, four tokens a lane.
+template <int D, bool kWide>
+__device__ __forceinline__ void load_meta(const AttnArgs& a, const uint32_t* from, u32x4_t to[2][Frag<D>::kG],
+                                          const Place<kWide>& p, const Offsets& l) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
         const uint64_t meta = kWide ? p.meta[0] + h * 64 : p.meta[h % Place<kWide>::kN];
 #pragma unroll
-        for (int q = 0; q < kG; ++q) {
-            f.v[h][q] = fetch<u32x4_t>(a.c.vc, code + q * 256, l.v);
-            f.vm[h][q] = fetch<u32x4_t>(a.c.vm, meta + (q ? (uint64_t)(4u * q << a.c.shift) : 0), l.meta);
-        }
+        for (int q = 0; q < Frag<D>::kG; ++q)
+            to[h][q] = fetch<u32x4_t>(from, meta + (q ? (uint64_t)(4u * q << a.c.shift) : 0), l.meta);
     }
+}
+template <int D, bool kWide>
+__device__ __forceinline__ void load_keys(const AttnArgs& a, Frag<D>& f, const Place<kWide>& p, const Offsets& l) {
+    load_key_codes<D, kWide>(a, f, p, l);
+    load_meta<D, kWide>(a, a.c.km, f.km, p, l);
+}
+template <int D, bool kWide>
+__device__ __forceinline__ void load_values(const AttnArgs& a, Frag<D>& f, const Place<kWide>& p, const Offsets& l) {
+    load_value_codes<D, kWide>(a, f, p, l);
+    load_meta<D, kWide>(a, a.c.vm, f.vm, p, l);
 }
 
 // The table's entries for a tile's halves, as they are (0 for none): nothing
@@ -708,6 +722,386 @@ __global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
     if (wave == 0) rw.store(a, req, head, mine.split, r0, rows, lane);
 }
 
+// Value of lane l ^ kOff within a row of 16, for any set of other lane bits.
+template <int kOff>
+__device__ __forceinline__ float lane_xor(float v) {
+    if constexpr (kOff == 4) {  // half mirror (^ 7), then the quad reversed (^ 3)
+        const int b = __builtin_bit_cast(int, v);
+        const int m = __builtin_amdgcn_update_dpp(b, b, 0x141, 0xF, 0xF, false);
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(m, m, 0x1B, 0xF, 0xF, false));
+    } else {
+        return dpp_partner<kOff>(v);
+    }
+}
+
+// Sums n values over the lanes whose column differs in bits kOff, kOff / 2,
+// ... kLast, each step leaving a lane half of the values: on return it holds
+// v[0 .. n / steps) of the part that its bits (the highest first) select.
+template <int kOff, int kLast, int kN>
+__device__ __forceinline__ void halving_sum(float* v, int c) {
+    if constexpr (kOff >= kLast) {
+        const bool upper = (c & kOff) != 0;
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) {
+            const float keep = upper ? v[i + kN / 2] : v[i], send = upper ? v[i] : v[i + kN / 2];
+            v[i] = keep + lane_xor<kOff>(send);
+        }
+        halving_sum<kOff / 2, kLast, kN / 2>(v, c);
+    }
+}
+template <int kOff, int kLast, typename F>
+__device__ __forceinline__ float over_sets(float v, F f) {
+    if constexpr (kOff >= kLast) return over_sets<kOff / 2, kLast>(f(v, lane_xor<kOff>(v)), f);
+    return v;
+}
+
+// Very few rows (a decode step: the query heads of one key/value head, 8 at
+// most).  Of the 16 columns of a product only those rows' would be of use, and
+// softmax and scaling would be done 16 / rows times over.  So the columns are
+// cut into kSets sets of 16 / kSets rows, all holding the same queries: set s
+// keeps the scores of the s-th run of 16 tokens, a lane then has four scores
+// of kSets * 16 tokens, and its own maximum and sum; in the second product a
+// set's weights are 0 against the other sets' tokens.  The sets are joined at
+// the end as the waves are.
+// Per 32 tokens of D = 128 and 4 rows that is some 160 vector instructions
+// instead of 260.
+template <int D, int kSets, bool kWide>
+__global__ __launch_bounds__(256, 2) void kv4_attn_sets_kernel(AttnArgs a) {
+    constexpr int kWaves = 4, kT = kSets / 2, kCols = 16 / kSets;  // tiles at a time; rows
+    constexpr int kG = Frag<D>::kG, kW = Frag<D>::kW, kJ = D == 64 ? 4 : 8;
+    constexpr int kAll = kG * 4 * kJ, kMine = kAll / kSets;  // a lane's outputs, before and after the sets are joined
+    __shared__ float so[kWaves][kMine][kWave];
+    __shared__ float sm[kWaves][kCols], sl[kWaves][kCols];
+
+    const int lane = threadIdx.x & (kWave - 1), wave = (int)sgpr(threadIdx.x / kWave);
+    const int c = lane & 15, g = lane >> 4, set = c / kCols;
+    const Share mine = share_of(a);
+    const int head = mine.head;
+    const Request req = request_of(a, mine.b);
+    const int rows = min(min(req.rows, a.max_q) * a.g, kCols);
+    if (rows <= 0) return;
+    const int first_pos = req.kv - req.rows;
+    const int low = first_pos, high = first_pos + (rows - 1) / a.g;
+    const Tiles tiles = tiles_of(a, low, high);
+    const table_ptr table = as_table(a.table + (size_t)mine.b * a.width);
+
+    // this split's tiles, kT at a time in turn over the waves
+    const int per = ((tiles.count + a.splits - 1) / a.splits + kT - 1) / kT * kT;
+    const int v1 = min(tiles.count, (mine.split + 1) * per);
+    int v = mine.split * per + wave * kT;
+    if (a.width <= 0) v = max(v, v1);
+    const auto tile_at = [&](int x) { return tiles.at(max(min(x, v1 - 1), 0)) * kTile; };
+
+    // the lane's row (past the last one: that one again, unseen)
+    const int row = c % kCols, r = min(row, rows - 1);
+    const int pos = row < rows ? max(first_pos + r / a.g, -1) : -1;
+    u32x4_t xq[kG][kW];
+    {
+        const uint16_t* src = a.q + (int64_t)(req.first + r / a.g) * a.q_stride + (size_t)(head * a.g + r % a.g) * D;
+#pragma unroll
+        for (int q = 0; q < kG; ++q)
+#pragma unroll
+            for (int i = 0; i < kW; ++i)
+                xq[q][i] = *reinterpret_cast<const u32x4_t*>(src + q * W4_KV4_GROUP + (kW * g + i) * 8);
+    }
+
+    // Tiles v .. v + kT - 1: where they begin, their pages and places; a lane's
+    // own run of 16 tokens among them.
+    struct Group {
+        int t0[kT], page[kT][2];
+        Place<kWide> place[kT];
+    };
+    const Offsets offs = offsets_of<D>(lane);
+    Entries entries[kT];
+    const auto send_entries = [&](int at) {
+#pragma unroll
+        for (int t = 0; t < kT; ++t) entries[t] = entries_of<kWide>(a, table, tile_at(at + t));
+    };
+    const auto group_at = [&](int at) {
+        Group x;
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+            x.t0[t] = tile_at(at + t);
+            pages_of<kWide>(a, entries[t], x.t0[t], high, x.page[t]);
+            x.place[t] = place_of<D, kWide>(a, x.t0[t], head, x.page[t]);
+        }
+        return x;
+    };
+    const auto of_set = [&](auto f) {  // f(tile, half) of the lane's set
+        auto x = f(0, 0);
+#pragma unroll
+        for (int k = 1; k < kSets; ++k) {
+            const auto y = f(k / 2, k % 2);  // before the choice: a choice of addresses would put all in memory
+            x = set == k ? y : x;
+        }
+        return x;
+    };
+    Frag<D> f[kT];  // codes; the pairs below are the lane's set's alone
+    u32x4_t km[kG], vm[kG];
+    const auto fetch_meta = [&](const Group& x, const uint32_t* from, u32x4_t to[kG]) {
+        const uint64_t at = of_set([&](int t, int h) { return kWide ? x.place[t].meta[0] + h * 64 : x.place[t].meta[h % Place<kWide>::kN]; });
+#pragma unroll
+        for (int q = 0; q < kG; ++q)
+            to[q] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const char*>(from) + at + ((uint64_t)(4u * q) << a.c.shift) + offs.meta);
+    };
+    Group now = {};
+    if (v < v1) {
+        send_entries(v);
+        now = group_at(v);
+        send_entries(v + kWaves * kT);
+#pragma unroll
+        for (int t = 0; t < kT; ++t) load_key_codes<D, kWide>(a, f[t], now.place[t], offs);
+        fetch_meta(now, a.c.km, km);
+        fetch_meta(now, a.c.vm, vm);
+#pragma unroll
+        for (int t = 0; t < kT; ++t) load_value_codes<D, kWide>(a, f[t], now.place[t], offs);
+    }
+
+    f32x4_t xstart[kG];
+    float xs[kG];
+#pragma unroll
+    for (int q = 0; q < kG; ++q) {
+        float sum = 0;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+            const u32x4_t w = xq[q][i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += bf16_to_f32(w[e] & 0xFFFFu) + __builtin_bit_cast(float, w[e] & 0xFFFF0000u);
+            uint32_t in[4] = {w.x, w.y, w.z, w.w}, pr[4];
+            x_pairs_for_biased(in, pr);
+            xq[q][i] = u32x4_t{pr[0], pr[1], pr[2], pr[3]};
+        }
+        xs[q] = row_sum(sum);
+        const float x0 = -128.0f * xs[q];
+        xstart[q] = f32x4_t{x0, x0, x0, x0};
+    }
+    f32x4_t o[kG][kJ], ones_sum[kG];
+    float extra[kG], means[kG], scales[kG], m = -INFINITY, l = 0;
+#pragma unroll
+    for (int q = 0; q < kG; ++q) {
+        extra[q] = means[q] = scales[q] = 0;
+        ones_sum[q] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) o[q][j] = f32x4_t{0, 0, 0, 0};
+    }
+    const auto settle = [&]() {
+#pragma unroll
+        for (int q = 0; q < kG; ++q) {
+            const float off = -136.0f * ones_sum[q][0];
+            ones_sum[q] = f32x4_t{0, 0, 0, 0};
+            extra[q] += fmaf(8.0f, scales[q], means[q]);
+            means[q] = scales[q] = 0;
+#pragma unroll
+            for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[q][j][e] += off;
+        }
+    };
+
+    const float slack = 8.0f / a.scale2;
+    const uint32_t bias = vgpr_const(kInt4BiasPair);
+    const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    for (int done = 1; v < v1; v += kWaves * kT, ++done) {
+        const Group next = group_at(v + kWaves * kT);
+        send_entries(v + 2 * kWaves * kT);
+        bool whole = v + kT <= v1 && rows == kCols;
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+            whole = whole && now.t0[t] + kTile - 1 <= low &&
+                    (a.window == 0 || now.t0[t] > high - a.window || now.t0[t] + kTile <= a.sinks) &&
+                    now.page[t][0] >= 0 && now.page[t][1] >= 0;
+
+        // scores: each run's products, of which its set keeps its columns
+        f32x4_t acc[kG];
+#pragma unroll
+        for (int q = 0; q < kG; ++q) acc[q] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+            if (v + t < v1) {
+                f32x4_t x[2][kG];
+#pragma unroll
+                for (int i = 0; i < kW; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int q = 0; q < kG; ++q)
+                            x[h][q] = mfma(key_operand(f[t].k[h][q][i], bias), xq[q][i], i == 0 ? xstart[q] : x[h][q]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int q = 0; q < kG; ++q)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[q][e] = set == 2 * t + h ? x[h][q][e] : acc[q][e];
+            }
+            __builtin_amdgcn_sched_barrier(0);  // else loads above the last use of these registers land in others
+            load_key_codes<D, kWide>(a, f[t], next.place[t], offs);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        float s[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s[e] = 0;
+#pragma unroll
+            for (int q = 0; q < kG; ++q) s[e] = fmaf(lo16(km[q][e]), acc[q][e], fmaf(hi16(km[q][e]), xs[q], s[e]));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        fetch_meta(next, a.c.km, km);
+        __builtin_amdgcn_sched_barrier(0);
+        if (!whole) {
+            const int t0 = of_set([&](int t, int h) { return now.t0[t] + 16 * h; }) + 4 * g;
+            const bool bad = of_set([&](int t, int h) { return now.page[t][h] < 0; });
+            const bool run = of_set([&](int t, int) { return v + t < v1; });
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = t0 + e;
+                const bool see = run & (t <= pos) & ((a.window == 0) | (t > pos - a.window) | (t < a.sinks));
+                s[e] = !see ? -INFINITY : bad ? NAN : s[e];
+                // what a row does not see may hold anything, an infinity or a NaN too
+#pragma unroll
+                for (int q = 0; q < kG; ++q) vm[q][e] = see ? vm[q][e] : 0;
+            }
+        }
+
+        // softmax of the lane's four scores
+        const float top = row_max(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])));
+        if (__any(top > m + slack)) {
+            const float top_now = fmaxf(m, top);
+            const float keep = top_now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - top_now) * a.scale2);
+            m = top_now;
+            l *= keep;
+#pragma unroll
+            for (int q = 0; q < kG; ++q) {
+                extra[q] *= keep;
+                means[q] *= keep;
+                scales[q] *= keep;
+                ones_sum[q][0] *= keep;
+#pragma unroll
+                for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[q][j][e] *= keep;
+            }
+        }
+        const float base = m == -INFINITY ? 0.0f : m * a.scale2;
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], a.scale2, -base));
+            l += p[e];
+        }
+        uint32_t weights[kG][2];
+#pragma unroll
+        for (int q = 0; q < kG; ++q) {
+            float ps[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                ps[e] = p[e] * lo16(vm[q][e]);
+                means[q] = fmaf(p[e], hi16(vm[q][e]), means[q]);
+                scales[q] += ps[e];
+            }
+            // here, not put off behind the loads that reuse vm's registers
+            asm volatile("" : "+v"(means[q]), "+v"(scales[q]));
+            weights[q][0] = pack_bf16x2(ps[0], ps[1]);
+            weights[q][1] = pack_bf16x2(ps[2], ps[3]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        fetch_meta(next, a.c.vm, vm);
+        __builtin_amdgcn_sched_barrier(0);
+
+        // outputs: a tile's tokens against its two sets' weights
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+            if (v + t < v1) {
+#pragma unroll
+                for (int q = 0; q < kG; ++q) {
+                    const bool first = set == 2 * t, second = set == 2 * t + 1;
+                    const u32x4_t pop = {first ? weights[q][0] : 0, first ? weights[q][1] : 0,
+                                         second ? weights[q][0] : 0, second ? weights[q][1] : 0};
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j)
+                        o[q][j] = mfma(value_operand<D>(f[t].v[0][q], f[t].v[1][q], j, c, bias), pop, o[q][j]);
+                    ones_sum[q] = mfma(ones, pop, ones_sum[q]);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            load_value_codes<D, kWide>(a, f[t], next.place[t], offs);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        now = next;
+        if (done % 8 == 0) settle();
+    }
+    settle();
+
+    // The sets of a wave: common maximum, sums, a part of the outputs for each lane.
+    constexpr int kBit = 8;
+    l = row_sum(l);
+    if (a.width <= 0 && pos >= 0) l = NAN;  // no table: what the row sees lies past it
+    const float top = over_sets<kBit, kCols>(m, [](float x, float y) { return fmaxf(x, y); });
+    const float scale = l == 0.0f ? 0.0f : m == -INFINITY ? NAN : __builtin_amdgcn_exp2f((m - top) * a.scale2);
+    l = over_sets<kBit, kCols>(l == 0.0f ? 0.0f : l * scale, [](float x, float y) { return x + y; });
+    float out[kAll];  // (q, r, j)
+#pragma unroll
+    for (int q = 0; q < kG; ++q) {
+        const float e = row_sum(extra[q]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) out[(q * 4 + x) * kJ + j] = l == 0.0f ? 0.0f : (o[q][j][x] + e) * scale;
+    }
+    halving_sum<kBit, kCols, kAll>(out, c);
+
+    // The waves.
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) so[wave][i][lane] = out[i];
+    if (lane < kCols) {
+        sm[wave][lane] = top;
+        sl[wave][lane] = l;
+    }
+    __syncthreads();
+    float now_top = sm[0][row];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) now_top = fmaxf(now_top, sm[w][row]);
+    float by[kWaves], sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        // a wave that saw nothing has l = 0; a NaN stays one
+        const float lw = sl[w][row], mw = sm[w][row];
+        by[w] = lw == 0.0f ? 0.0f : mw == -INFINITY ? NAN : __builtin_amdgcn_exp2f((mw - now_top) * a.scale2);
+        sum += lw == 0.0f ? 0.0f : lw * by[w];
+    }
+    if (row >= rows) return;
+    // Each wave finishes a share of the lane's values, neighbours in d.
+    constexpr int kEnd = kMine >= kWaves ? kMine / kWaves : 1;
+    if (wave * kEnd >= kMine) return;
+    float end[kEnd];
+#pragma unroll
+    for (int i = 0; i < kEnd; ++i) {
+        end[i] = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) end[i] = fmaf(by[w], so[w][wave * kEnd + i][lane], end[i]);
+    }
+    const int at = set * kMine + wave * kEnd;  // (q, r, j) as one number
+    const int d = Rows<D, 1>::place(at / kJ / 4, at / kJ % 4, g) + at % kJ;
+    const int t = req.first + row / a.g, h = head * a.g + row % a.g;
+    if (a.splits == 1) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint16_t* dst = a.out + (int64_t)t * a.out_stride + (size_t)h * D + d;
+        if constexpr (kEnd % 2 == 0) {
+#pragma unroll
+            for (int i = 0; i < kEnd; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(end[i] * inv, end[i + 1] * inv);
+        } else {
+            dst[0] = f32_to_bf16(end[0] * inv);
+        }
+    } else {
+        const size_t part = ((size_t)t * a.g * a.c.heads + h) * a.splits + mine.split;
+        if (g == 0 && wave == 0 && set == 0) {
+            a.part_ml[2 * part] = now_top;
+            a.part_ml[2 * part + 1] = sum;
+        }
+#pragma unroll
+        for (int i = 0; i < kEnd; ++i) a.part_o[part * D + d + i] = end[i];
+    }
+}
+
 // Waits for a workgroup's LDS accesses and meets the others; loads from
 // memory stay on their way.
 __device__ __forceinline__ void lds_barrier() {
@@ -801,12 +1195,7 @@ __global__ __launch_bounds__(256, 2) void kv4_attn_many_kernel(AttnArgs a) {
     };
     u32x4_t km[2][kG], vm[2][kG];
     const auto fetch_meta = [&](const Place<kWide>& p, const uint32_t* from, u32x4_t to[2][kG]) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int q = 0; q < kG; ++q)
-                to[h][q] = fetch<u32x4_t>(from, (kWide ? p.meta[0] + h * 64 : p.meta[h % Place<kWide>::kN]) +
-                                          (q ? (uint64_t)(4u * q << a.c.shift) : 0), offs.meta);
+        load_meta<D, kWide>(a, from, to, p, offs);
     };
 
     int t0 = 0, t1 = 0, page[2] = {-1, -1}, coming[2] = {-1, -1};
@@ -945,6 +1334,7 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_join_kernel(AttnArgs a) {
 // How a call is cut into workgroups.
 struct Cut {
     bool many;      // kv4_attn_many_kernel
+    int sets;       // kv4_attn_sets_kernel if over 1
     int row_tiles;  // of a request, each a workgroup's rows
     int splits;     // workgroups that share a row tile's tokens
 };
@@ -962,6 +1352,12 @@ Cut cut_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     Cut k;
     const int64_t rows = (int64_t)a.max_q * (a.q_heads / c.kv_heads);
     k.many = rows >= W4_ATTN_MANY;
+    // as many sets as leave a column for each row; with heads of 256 four, for
+    // the registers of a group's codes
+    k.sets = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 || c.head_dim == 256 ? 4 : 8;
+#ifdef W4_NO_SETS
+    k.sets = 1;
+#endif
     const int tile = k.many ? 64 * many_blocks(c.head_dim) : 16;
     k.row_tiles = (int)((rows + tile - 1) / tile);
     // enough workgroups to fill the chip twice, with two tiles at least for
@@ -978,11 +1374,18 @@ Cut cut_of(const w4_attn_args& a, const w4_kv4_cache& c) {
 }
 
 template <int D, bool kWide>
-hipError_t launch_d(const AttnArgs& k, bool many, int64_t groups, hipStream_t stream) {
-    if (many) {
-        kv4_attn_many_kernel<D, many_blocks(D), kWide><<<dim3((unsigned)groups), dim3(256), 0, stream>>>(k);
+hipError_t launch_d(const AttnArgs& k, const Cut& cut, int64_t groups, hipStream_t stream) {
+    const dim3 grid((unsigned)groups), block(256);
+    if (cut.sets == 2) {
+        kv4_attn_sets_kernel<D, 2, kWide><<<grid, block, 0, stream>>>(k);
+    } else if (cut.sets == 4) {
+        kv4_attn_sets_kernel<D, 4, kWide><<<grid, block, 0, stream>>>(k);
+    } else if (cut.sets == 8) {
+        if constexpr (D < 256) kv4_attn_sets_kernel<D, 8, kWide><<<grid, block, 0, stream>>>(k);
+    } else if (cut.many) {
+        kv4_attn_many_kernel<D, many_blocks(D), kWide><<<grid, block, 0, stream>>>(k);
     } else {
-        kv4_attn_kernel<D, 1, kFewWaves, kWide><<<dim3((unsigned)groups), dim3(kFewWaves * kWave), 0, stream>>>(k);
+        kv4_attn_kernel<D, 1, kFewWaves, kWide><<<grid, block, 0, stream>>>(k);
     }
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || k.splits == 1) return err;
@@ -992,8 +1395,8 @@ hipError_t launch_d(const AttnArgs& k, bool many, int64_t groups, hipStream_t st
 }
 
 template <int D>
-hipError_t launch_w(const AttnArgs& k, bool many, int64_t groups, hipStream_t stream) {
-    return k.c.shift >= 5 ? launch_d<D, true>(k, many, groups, stream) : launch_d<D, false>(k, many, groups, stream);
+hipError_t launch_w(const AttnArgs& k, const Cut& cut, int64_t groups, hipStream_t stream) {
+    return k.c.shift >= 5 ? launch_d<D, true>(k, cut, groups, stream) : launch_d<D, false>(k, cut, groups, stream);
 }
 
 }  // namespace
@@ -1032,9 +1435,9 @@ hipError_t launch_kv4_attn(const w4_attn_args& a, const w4_kv4_cache& c, void* w
     }
     const int64_t groups = (int64_t)a.B * c.kv_heads * k.row_tiles * k.splits;
     switch (c.head_dim) {
-        case 64: return launch_w<64>(k, cut.many, groups, stream);
-        case 128: return launch_w<128>(k, cut.many, groups, stream);
-        default: return launch_w<256>(k, cut.many, groups, stream);
+        case 64: return launch_w<64>(k, cut, groups, stream);
+        case 128: return launch_w<128>(k, cut, groups, stream);
+        default: return launch_w<256>(k, cut, groups, stream);
     }
 }
 
