@@ -144,10 +144,13 @@ __device__ __forceinline__ Place<kWide> place_of(const AttnArgs& a, int t0, int 
     return p;
 }
 
-// One of a lane's loads: uniform base, the lane's offset, a constant.
-template <typename T>
+// One of a lane's loads: uniform base, the lane's offset, a constant.  With
+// kOnce nobody reads it again, and it need not stay in the caches.
+template <typename T, bool kOnce = false>
 __device__ __forceinline__ T fetch(const uint32_t* base, uint64_t uniform, uint32_t lane_off) {
-    return *reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + uniform + lane_off);
+    const T* p = reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + uniform + lane_off);
+    if constexpr (kOnce) return __builtin_nontemporal_load(p);
+    return *p;
 }
 
 // A lane's offsets within a tile.
@@ -160,7 +163,7 @@ __device__ __forceinline__ Offsets offsets_of(int lane) {
     return {c * (D / 2) + (D == 64 ? 8 : 16) * g, g * (D * 2) + 16 * (D == 64 ? c >> 1 : c), 16 * g};
 }
 
-template <int D, bool kWide>
+template <int D, bool kWide, bool kOnce = false>
 __device__ __forceinline__ void load_key_codes(const AttnArgs& a, Frag<D>& f, const Place<kWide>& p, const Offsets& l) {
     constexpr int kG = Frag<D>::kG, kW = Frag<D>::kW;
 #pragma unroll
@@ -169,24 +172,24 @@ __device__ __forceinline__ void load_key_codes(const AttnArgs& a, Frag<D>& f, co
 #pragma unroll
         for (int q = 0; q < kG; ++q) {
             if constexpr (kW == 4) {
-                const u32x4_t w = fetch<u32x4_t>(a.c.kc, code + q * 64, l.k);
+                const u32x4_t w = fetch<u32x4_t, kOnce>(a.c.kc, code + q * 64, l.k);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) f.k[h][q][i] = w[i];
             } else {
-                const u32x2_t w = fetch<u32x2_t>(a.c.kc, code, l.k);
+                const u32x2_t w = fetch<u32x2_t, kOnce>(a.c.kc, code, l.k);
                 f.k[h][q][0] = w.x;
                 f.k[h][q][1] = w.y;
             }
         }
     }
 }
-template <int D, bool kWide>
+template <int D, bool kWide, bool kOnce = false>
 __device__ __forceinline__ void load_value_codes(const AttnArgs& a, Frag<D>& f, const Place<kWide>& p, const Offsets& l) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint64_t code = kWide ? p.code[0] + h * 16 * (D / 2) : p.code[h % Place<kWide>::kN];
 #pragma unroll
-        for (int q = 0; q < Frag<D>::kG; ++q) f.v[h][q] = fetch<u32x4_t>(a.c.vc, code + q * 256, l.v);
+        for (int q = 0; q < Frag<D>::kG; ++q) f.v[h][q] = fetch<u32x4_t, kOnce>(a.c.vc, code + q * 256, l.v);
     }
 }
 // The (s, m) pairs of a tile, four tokens a lane.
@@ -850,11 +853,11 @@ __global__ __launch_bounds__(256, 2) void kv4_attn_sets_kernel(AttnArgs a) {
         now = group_at(v);
         send_entries(v + kWaves * kT);
 #pragma unroll
-        for (int t = 0; t < kT; ++t) load_key_codes<D, kWide>(a, f[t], now.place[t], offs);
+        for (int t = 0; t < kT; ++t) load_key_codes<D, kWide, true>(a, f[t], now.place[t], offs);
         fetch_meta(now, a.c.km, km);
         fetch_meta(now, a.c.vm, vm);
 #pragma unroll
-        for (int t = 0; t < kT; ++t) load_value_codes<D, kWide>(a, f[t], now.place[t], offs);
+        for (int t = 0; t < kT; ++t) load_value_codes<D, kWide, true>(a, f[t], now.place[t], offs);
     }
 
     f32x4_t xstart[kG];
@@ -934,7 +937,7 @@ __global__ __launch_bounds__(256, 2) void kv4_attn_sets_kernel(AttnArgs a) {
                         for (int e = 0; e < 4; ++e) acc[q][e] = set == 2 * t + h ? x[h][q][e] : acc[q][e];
             }
             __builtin_amdgcn_sched_barrier(0);  // else loads above the last use of these registers land in others
-            load_key_codes<D, kWide>(a, f[t], next.place[t], offs);
+            load_key_codes<D, kWide, true>(a, f[t], next.place[t], offs);
             __builtin_amdgcn_sched_barrier(0);
         }
         float s[4];
@@ -1023,7 +1026,7 @@ __global__ __launch_bounds__(256, 2) void kv4_attn_sets_kernel(AttnArgs a) {
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
-            load_value_codes<D, kWide>(a, f[t], next.place[t], offs);
+            load_value_codes<D, kWide, true>(a, f[t], next.place[t], offs);
             __builtin_amdgcn_sched_barrier(0);
         }
         now = next;
@@ -1342,31 +1345,26 @@ constexpr int kFewWaves = 4;
 // 16-row blocks of a wave: as many as leave two waves a SIMD.
 constexpr int many_blocks(int d) { return d == 256 ? 1 : 2; }
 
-#ifndef W4_ATTN_GROUPS
-#define W4_ATTN_GROUPS 512
-#endif
-#ifndef W4_ATTN_MANY
-#define W4_ATTN_MANY 64
-#endif
 Cut cut_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     Cut k;
     const int64_t rows = (int64_t)a.max_q * (a.q_heads / c.kv_heads);
-    k.many = rows >= W4_ATTN_MANY;
+    k.many = rows >= 64;
     // as many sets as leave a column for each row; with heads of 256 four, for
     // the registers of a group's codes
     k.sets = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 || c.head_dim == 256 ? 4 : 8;
-#ifdef W4_NO_SETS
-    k.sets = 1;
-#endif
     const int tile = k.many ? 64 * many_blocks(c.head_dim) : 16;
     k.row_tiles = (int)((rows + tile - 1) / tile);
-    // enough workgroups to fill the chip twice, with two tiles at least for
-    // each of the waves that share them
+    // Enough workgroups to fill the chip twice, with two tiles at least for
+    // each of the waves that share them.  Twice that number where requests
+    // differ in length (a window makes them alike): 32 requests of up to 8192
+    // tokens take 80 us then, 86 without; one of 131071 tokens 33 instead
+    // of 32, and 64 that a window holds to 1024 tokens 20 instead of 14.
     const int64_t groups = (int64_t)a.B * c.kv_heads * k.row_tiles;
     int64_t tokens = a.max_kv;
     if (a.window > 0) tokens = tokens < (int64_t)a.window + a.sinks + a.max_q ? tokens : (int64_t)a.window + a.sinks + a.max_q;
     const int64_t tiles = (tokens + kTile - 1) / kTile;
-    int64_t want = (W4_ATTN_GROUPS + groups - 1) / (groups > 0 ? groups : 1);
+    const int64_t fill = a.B > 1 && a.window == 0 ? 1024 : 512;
+    int64_t want = (fill + groups - 1) / (groups > 0 ? groups : 1);
     const int64_t most = tiles / (2 * kFewWaves);
     want = want < most ? want : most;
     k.splits = (int)(want < 1 ? 1 : want > kMaxSplits ? kMaxSplits : want);
