@@ -54,6 +54,17 @@ __device__ __forceinline__ f32x4_t mfma(const u32x4_t& a, const u32x4_t& b, cons
                                                    0, 0, 0);
 }
 
+// A pair of weights in two parts, each of BF16: as one part, a weight would be
+// off by 2^-9 of itself, and with few tokens an output by as much as its own
+// rounding to BF16 adds.
+struct Pair {
+    uint32_t high, low;
+};
+__device__ __forceinline__ Pair two_parts(float x, float y) {
+    const uint32_t high = pack_bf16x2(x, y);
+    return {high, pack_bf16x2(x - __builtin_bit_cast(float, high << 16), y - __builtin_bit_cast(float, high & 0xFFFF0000u))};
+}
+
 // Over the four lanes of one row (lane bits 4 and 5).
 __device__ __forceinline__ float row_sum(float v) { return pair_sum<32>(pair_sum<16>(v)); }
 __device__ __forceinline__ float row_max(float v) {
@@ -245,7 +256,8 @@ __device__ __forceinline__ void pages_of(const AttnArgs& a, const Entries& x, in
 // What a wave holds of its 16 * kNB rows: queries, running softmax and outputs.
 // A lane's rows are those of its column (lane % 16) of each block of 16; of
 // the tokens and of the outputs it has the share of its lane / 16.
-template <int D, int kNB>
+// kParts: how many BF16 parts a weight of the second product has (see two_parts).
+template <int D, int kNB, int kParts>
 struct Rows {
     static constexpr int kG = Frag<D>::kG, kW = Frag<D>::kW;
     static constexpr int kJ = D == 64 ? 4 : 8;  // blocks of 16 d per group
@@ -257,7 +269,7 @@ struct Rows {
     f32x4_t o[kNB][kG][kJ], ones_sum[kNB][kG];  // of ones_sum only element 0 counts
     float extra[kNB][kG], m[kNB], l[kNB];
     float means[kNB][kG], scales[kNB][kG];  // sums of p m and p s since the last settling
-    u32x4_t pop[kNB][kG];  // p s of the tile, the second product's operand
+    u32x4_t pop[kParts][kNB][kG];  // p s of the tile and what its rounding left, the second product's operands
 
     // Sends for the queries of rows r0 ..; past the last row that one again, unseen.
     __device__ __forceinline__ void fetch(const AttnArgs& a, const Request& req, int head, int r0, int rows, int lane) {
@@ -406,8 +418,14 @@ struct Rows {
                         }
                     // here, not put off behind the loads that reuse vm's registers
                     asm volatile("" : "+v"(means[n][q]), "+v"(scales[n][q]));
-                    pop[n][q] = u32x4_t{pack_bf16x2(ps[0][0], ps[0][1]), pack_bf16x2(ps[0][2], ps[0][3]),
-                                        pack_bf16x2(ps[1][0], ps[1][1]), pack_bf16x2(ps[1][2], ps[1][3])};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int r = 0; r < 4; r += 2) {
+                            const Pair w = two_parts(ps[h][r], ps[h][r + 1]);
+                            pop[0][n][q][2 * h + r / 2] = w.high;
+                            if constexpr (kParts == 2) pop[1][n][q][2 * h + r / 2] = w.low;
+                        }
                 }
             };
             if (whole) {
@@ -425,16 +443,28 @@ struct Rows {
     __device__ __forceinline__ void outputs(F value, const u32x4_t& ones) {
 #pragma unroll
         for (int q = 0; q < kG; ++q) {
+            // a block's second product a block later: it waits for the first one's sums
+            u32x4_t last;
 #pragma unroll
             for (int j = 0; j < kJ; ++j) {
                 const u32x4_t vop = value(q, j);
 #pragma unroll
-                for (int n = 0; n < kNB; ++n) o[n][q][j] = mfma(vop, pop[n][q], o[n][q][j]);
+                for (int n = 0; n < kNB; ++n) {
+                    o[n][q][j] = mfma(vop, pop[0][n][q], o[n][q][j]);
+                    if (kParts == 2 && j > 0) o[n][q][j - 1] = mfma(last, pop[kParts - 1][n][q], o[n][q][j - 1]);
+                }
+                last = vop;
             }
 #pragma unroll
-            for (int n = 0; n < kNB; ++n) ones_sum[n][q] = mfma(ones, pop[n][q], ones_sum[n][q]);
+            for (int n = 0; n < kNB; ++n) {
+                ones_sum[n][q] = mfma(ones, pop[0][n][q], ones_sum[n][q]);
+                if constexpr (kParts == 2) {
+                    o[n][q][kJ - 1] = mfma(last, pop[1][n][q], o[n][q][kJ - 1]);
+                    ones_sum[n][q] = mfma(ones, pop[1][n][q], ones_sum[n][q]);
+                }
+            }
         }
-        if constexpr (kAhead > 0) in_order<kG * kJ, kAhead, kNB>();
+        if constexpr (kAhead > 0) in_order<kG * kJ, kAhead, kParts * kNB>();
     }
 
     // Asks the scheduler for kAhead reads from LDS, then a read after each
@@ -568,16 +598,16 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a) {
     // (two a compute unit, the second 256 after the first) the second half
     // goes the other way, so that a long one shares its unit with a short
     // one; else the longest come first.
-    const int t = id % a.row_tiles;
+    s.b = id % a.B;
+    const int t = id / a.B;
     s.row_tile = a.in_turn && 2 * t >= a.row_tiles ? t - (a.row_tiles + 1) / 2 : a.row_tiles - 1 - t;
-    s.b = id / a.row_tiles;
     return s;
 }
 
 // Few rows: the waves take a row tile's token tiles in turn.
 template <int D, int kNB, int kWaves, bool kWide>
 __global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
-    typedef Rows<D, kNB> R;
+    typedef Rows<D, kNB, 2> R;
     constexpr int kG = R::kG, kJ = R::kJ, kCols = 16 * kNB;
     __shared__ float so[kWaves / 2][kCols][D + 4];
     __shared__ float sm[kWaves][kCols], sl[kWaves][kCols];
@@ -991,7 +1021,7 @@ __global__ __launch_bounds__(256, 2) void kv4_attn_sets_kernel(AttnArgs a) {
             p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], a.scale2, -base));
             l += p[e];
         }
-        uint32_t weights[kG][2];
+        Pair weights[kG][2];
 #pragma unroll
         for (int q = 0; q < kG; ++q) {
             float ps[4];
@@ -1003,8 +1033,8 @@ __global__ __launch_bounds__(256, 2) void kv4_attn_sets_kernel(AttnArgs a) {
             }
             // here, not put off behind the loads that reuse vm's registers
             asm volatile("" : "+v"(means[q]), "+v"(scales[q]));
-            weights[q][0] = pack_bf16x2(ps[0], ps[1]);
-            weights[q][1] = pack_bf16x2(ps[2], ps[3]);
+            weights[q][0] = two_parts(ps[0], ps[1]);
+            weights[q][1] = two_parts(ps[2], ps[3]);
         }
         __builtin_amdgcn_sched_barrier(0);
         fetch_meta(next, a.c.vm, vm);
@@ -1017,12 +1047,23 @@ __global__ __launch_bounds__(256, 2) void kv4_attn_sets_kernel(AttnArgs a) {
 #pragma unroll
                 for (int q = 0; q < kG; ++q) {
                     const bool first = set == 2 * t, second = set == 2 * t + 1;
-                    const u32x4_t pop = {first ? weights[q][0] : 0, first ? weights[q][1] : 0,
-                                         second ? weights[q][0] : 0, second ? weights[q][1] : 0};
+                    const auto part = [&](uint32_t w0, uint32_t w1) {
+                        return u32x4_t{first ? w0 : 0, first ? w1 : 0, second ? w0 : 0, second ? w1 : 0};
+                    };
+                    const u32x4_t high = part(weights[q][0].high, weights[q][1].high);
+                    const u32x4_t low = part(weights[q][0].low, weights[q][1].low);
+                    // a block's second product a block later: it waits for the first one's sums
+                    u32x4_t last;
 #pragma unroll
-                    for (int j = 0; j < kJ; ++j)
-                        o[q][j] = mfma(value_operand<D>(f[t].v[0][q], f[t].v[1][q], j, c, bias), pop, o[q][j]);
-                    ones_sum[q] = mfma(ones, pop, ones_sum[q]);
+                    for (int j = 0; j < kJ; ++j) {
+                        const u32x4_t vop = value_operand<D>(f[t].v[0][q], f[t].v[1][q], j, c, bias);
+                        o[q][j] = mfma(vop, high, o[q][j]);
+                        if (j > 0) o[q][j - 1] = mfma(last, low, o[q][j - 1]);
+                        last = vop;
+                    }
+                    ones_sum[q] = mfma(ones, high, ones_sum[q]);
+                    o[q][kJ - 1] = mfma(last, low, o[q][kJ - 1]);
+                    ones_sum[q] = mfma(ones, low, ones_sum[q]);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -1083,7 +1124,7 @@ __global__ __launch_bounds__(256, 2) void kv4_attn_sets_kernel(AttnArgs a) {
         for (int w = 0; w < kWaves; ++w) end[i] = fmaf(by[w], so[w][wave * kEnd + i][lane], end[i]);
     }
     const int at = set * kMine + wave * kEnd;  // (q, r, j) as one number
-    const int d = Rows<D, 1>::place(at / kJ / 4, at / kJ % 4, g) + at % kJ;
+    const int d = Rows<D, 1, 2>::place(at / kJ / 4, at / kJ % 4, g) + at % kJ;
     const int t = req.first + row / a.g, h = head * a.g + row % a.g;
     if (a.splits == 1) {
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -1121,7 +1162,7 @@ __device__ __forceinline__ void lds_barrier() {
 // one after is on its way from memory.
 template <int D, int kNB, bool kWide>
 __global__ __launch_bounds__(256, 2) void kv4_attn_many_kernel(AttnArgs a) {
-    typedef Rows<D, kNB> R;
+    typedef Rows<D, kNB, 1> R;
     constexpr int kWaves = 4, kG = R::kG, kW = R::kW, kJ = R::kJ, kCols = 16 * kNB;
     constexpr int kKeys = 2 * kG * kW, kValues = kG * kJ;  // operands of a tile
     constexpr int kMyKeys = kKeys / kWaves, kMyValues = kValues / kWaves;
@@ -1144,10 +1185,8 @@ __global__ __launch_bounds__(256, 2) void kv4_attn_many_kernel(AttnArgs a) {
     const int r0 = min(base + wave * kCols, rows);
     const int my_low = first_pos + min(r0, rows - 1) / a.g, my_high = first_pos + (min(r0 + kCols, rows) - 1) / a.g;
 
-    const int per = (tiles.count + a.splits - 1) / a.splits;
-    int v = mine.split * per;
-    const int v1 = min(tiles.count, v + per);
-    if (a.width <= 0) v = v1;
+    int v = 0;
+    const int v1 = a.width <= 0 ? 0 : tiles.count;
     const auto tile_at = [&](int x) { return tiles.at(max(min(x, v1 - 1), 0)) * kTile; };
 
     R rw;
@@ -1269,7 +1308,7 @@ __global__ __launch_bounds__(256, 2) void kv4_attn_many_kernel(AttnArgs a) {
         lds_barrier();
     }
     rw.finish(a);
-    if (r0 < rows) rw.store(a, req, head, mine.split, r0, rows, lane);
+    if (r0 < rows) rw.store(a, req, head, 0, r0, rows, lane);
 }
 
 // Joins the splits of one row, a workgroup a row: D / 4 lanes hold its values,
@@ -1348,11 +1387,25 @@ constexpr int many_blocks(int d) { return d == 256 ? 1 : 2; }
 Cut cut_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     Cut k;
     const int64_t rows = (int64_t)a.max_q * (a.q_heads / c.kv_heads);
-    k.many = rows >= 64;
-    // as many sets as leave a column for each row; with heads of 256 four, for
-    // the registers of a group's codes
-    k.sets = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 || c.head_dim == 256 ? 4 : 8;
-    const int tile = k.many ? 64 * many_blocks(c.head_dim) : 16;
+    // Shared tiles take the fewest instructions, but a workgroup passes over all
+    // of its rows' tokens a tile at a time, where kv4_attn_kernel's four waves
+    // share them: it pays where nearly every compute unit has two workgroups (heads
+    // of 64, whose tiles are the least work, four), for then the shortest can go with
+    // the longest.  us of both kernels, shared tiles first: heads of 256, 256
+    // workgroups 89 and 69 (1024 tokens after 1024), 512 189 and 207 (2048 after
+    // 2048), 1024 137 and 187 (4096 in two prompts); heads of 128, 352 workgroups 111
+    // and 98, 456 84 and 106, 512 318 and 382; heads of 64, 512 57 and 40 (four
+    // prompts of 1000), 1024 119 and 123, 2048 203 and 250.
+    const int64_t many_rows = 64 * many_blocks(c.head_dim);
+    const int64_t shared = (int64_t)a.B * c.kv_heads * ((rows + many_rows - 1) / many_rows);
+    k.many = rows >= many_rows && shared >= (c.head_dim == 64 ? 1024 : 448);
+    // Sets: four with up to 4 rows, but two with heads of 256, for the registers
+    // of a group's codes (32 requests of 4096 tokens, 8 key/value heads: heads
+    // of 128 32 us with four and 35 with two, heads of 256 with pages of 64 58
+    // and 57, with pages of 16 79 and 60; without sets 38, 63 and 66; eight sets
+    // take 37 us where four take 32).
+    k.sets = rows > 8 ? 1 : rows > 4 || c.head_dim == 256 ? 2 : 4;
+    const int64_t tile = k.many ? many_rows : 16;
     k.row_tiles = (int)((rows + tile - 1) / tile);
     // Enough workgroups to fill the chip twice, with two tiles at least for
     // each of the waves that share them.  Twice that number where requests
@@ -1364,7 +1417,7 @@ Cut cut_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     if (a.window > 0) tokens = tokens < (int64_t)a.window + a.sinks + a.max_q ? tokens : (int64_t)a.window + a.sinks + a.max_q;
     const int64_t tiles = (tokens + kTile - 1) / kTile;
     const int64_t fill = a.B > 1 && a.window == 0 ? 1024 : 512;
-    int64_t want = (fill + groups - 1) / (groups > 0 ? groups : 1);
+    int64_t want = k.many ? 1 : (fill + groups - 1) / (groups > 0 ? groups : 1);
     const int64_t most = tiles / (2 * kFewWaves);
     want = want < most ? want : most;
     k.splits = (int)(want < 1 ? 1 : want > kMaxSplits ? kMaxSplits : want);
@@ -1377,9 +1430,7 @@ hipError_t launch_d(const AttnArgs& k, const Cut& cut, int64_t groups, hipStream
     if (cut.sets == 2) {
         kv4_attn_sets_kernel<D, 2, kWide><<<grid, block, 0, stream>>>(k);
     } else if (cut.sets == 4) {
-        kv4_attn_sets_kernel<D, 4, kWide><<<grid, block, 0, stream>>>(k);
-    } else if (cut.sets == 8) {
-        if constexpr (D < 256) kv4_attn_sets_kernel<D, 8, kWide><<<grid, block, 0, stream>>>(k);
+        if constexpr (D < 256) kv4_attn_sets_kernel<D, 4, kWide><<<grid, block, 0, stream>>>(k);
     } else if (cut.many) {
         kv4_attn_many_kernel<D, many_blocks(D), kWide><<<grid, block, 0, stream>>>(k);
     } else {
@@ -1423,7 +1474,7 @@ hipError_t launch_kv4_attn(const w4_attn_args& a, const w4_kv4_cache& c, void* w
     const Cut cut = cut_of(a, c);
     k.row_tiles = cut.row_tiles;
     k.splits = cut.splits;
-    k.in_turn = cut.many && a.B == 1 && (int64_t)c.kv_heads * k.row_tiles * k.splits <= 512;
+    k.in_turn = cut.many && (int64_t)a.B * c.kv_heads * k.row_tiles * k.splits <= 512;
     k.window = a.window;
     k.sinks = a.sinks;
     k.scale2 = a.scale * 1.4426950408889634f;

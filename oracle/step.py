@@ -124,12 +124,12 @@ def visible(pos, kv, window, sinks):
     return see
 
 
-def attention(q_bits, cache: Cache, table, kv_lens, q_start, scale, window=0, sinks=0):
+def attention(q_bits, cache: Cache, table, kv_lens, q_start, scale, window=0, sinks=0, weights=2.0 ** -8):
     """(out, noise) float64 [T, q_heads, D]; rows in no request are NaN.
 
     ``noise`` bounds the error of a computation that forms scores in FP32 from
-    exact products, rounds each weight times its value's scale once to BF16
-    and sums in FP32: see ``tests/test_gpu_step.py``."""
+    exact products, rounds each weight times its value's scale by ``weights``
+    of itself (once to BF16: 2^-8; to two BF16 parts: 2^-16) and sums in FP32: see ``tests/test_gpu_step.py``."""
     T, hq, d = q_bits.shape
     g = hq // cache.heads
     out = np.full((T, hq, d), np.nan)
@@ -167,7 +167,7 @@ def attention(q_bits, cache: Cache, table, kv_lens, q_start, scale, window=0, si
                 size_of = (136.0 * ks[see, h // g, :, 0] + np.abs(ks[see, h // g, :, 1])) @ x
                 delta = 2.0 ** -24 * (40 * scale * size_of + 4 * np.abs(z) + 4 * abs(top) + 8)
                 noise[i, h] = (2 * (w * delta) @ np.abs(v - out[i, h]) + 2 * (w @ delta) * np.abs(w @ (v - out[i, h])) +
-                               2.0 ** -8 * (w @ np.abs(vs[see, h // g] * (codes[see, h // g] - 8))) +
+                               weights * (w @ np.abs(vs[see, h // g] * (codes[see, h // g] - 8))) +
                                2.0 ** -18 * (w @ np.abs(v)) + 2.0 ** -8 * np.abs(out[i, h]))
     return out, noise
 
