@@ -9,6 +9,7 @@
 //   outputs  O[d][r] = sum_t p s_t (q_td - 8) + sum_t p (m_t + 8 s_t)
 //
 // 128 + q is exact in BF16 and is one shift and one and-or per two codes.
+// (p s is rounded to BF16, in one part or two: see two_parts.)
 // In the outputs the 136 = 128 + 8 comes off as 136 times the sum of the
 // rounded weights, which one more product per group (with ones) keeps, every
 // few tiles: left in until the end, the sums of a long context would be
@@ -24,6 +25,12 @@
 // A workgroup's waves take a request's tiles in turn and join their sums in
 // LDS; a launch with few rows splits the tiles over workgroups too,
 // and a second kernel joins those.
+//
+// Measured: 32 requests of up to 8192 tokens, 16 query and 8 key/value heads of
+// 256: 77 us, 4.7 TB/s of codes and pairs (the same loads with a sum instead of
+// the attention: 76); one of 131071 tokens, 32 and 8 heads of 128: 32 us, 4.4
+// TB/s; a prompt's 2048 tokens after 2048 others, 16 and 8 heads of 256: 186 us, 555
+// TFLOP/s.
 #include <type_traits>
 
 #include "kv4.hpp"
@@ -54,9 +61,13 @@ __device__ __forceinline__ f32x4_t mfma(const u32x4_t& a, const u32x4_t& b, cons
                                                    0, 0, 0);
 }
 
-// A pair of weights in two parts, each of BF16: as one part, a weight would be
-// off by 2^-9 of itself, and with few tokens an output by as much as its own
-// rounding to BF16 adds.
+// A pair of weights in two parts, each of BF16.  As one part a weight is off by
+// up to 2^-8 of itself, which moves an output by about as much as its own
+// rounding to BF16 (error against 64 bits 2.3e-3 instead of 1.7e-3); the second
+// part costs one more product a block of values.  Memory bounds the decode
+// kernels, which take it (32 requests up to 8192 tokens: 77 us either way); for
+// long prompts, bound by instructions, it would cost a sixth (190 -> 216 us for
+// 2048 tokens after 2048, heads of 256), so kv4_attn_many_kernel does without.
 struct Pair {
     uint32_t high, low;
 };

@@ -10,7 +10,9 @@
 // lane or in one lane of the same head, taken as raw BF16 (four exchanges).  A
 // lane's eight 4-bit codes are one word of the cache.
 // Memory bounds it for prompts, as long as enough of it is asked for at once
-// (four heads' loads ahead); launch and latency for a decode step, where the
+// (four heads' loads ahead): 8192 tokens of 40 heads of 128 without a cache 39 us,
+// 4.4 TB/s; 4099 tokens of 32 heads of 256 into the cache 40 us, where the keys'
+// FP64 and the codes cost about as much as the memory; launch and latency for a decode step, where the
 // token's heads are spread over waves instead.
 #include <type_traits>
 
