@@ -16,7 +16,7 @@
 //      exp(z), FP64) of those up to the k-th, the cuts and the draw; then the
 //      chunk, and in it the index, of the drawn value's j-th place.
 // What bounds it: the count by the turns that LDS atomics take (64 rows of
-// 262144: 21 us, 1.6 TB/s of logits), the pick by the length of its chain of
+// 262144: 18 us, 1.8 TB/s of logits), the pick by the length of its chain of
 // dependent steps (17 us for one row, 22 for 64, a compute unit each).
 // Counts are whole numbers and masses are summed in a fixed order, so a
 // result depends on no order in which anything finishes.
@@ -31,6 +31,7 @@ constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kMaxChunk = 32768;  // four 16-byte loads a thread, and counts that fit 16 bits
 constexpr int kMinChunk = 8192;
+constexpr int kBlocks = kBins / 2 / kWave;  // of 128 bins, a word a lane
 constexpr int kRun = 256;  // entries of a list that a wave joins at a time
 constexpr int kMaxChunks = W4_SAMPLE_MAX_VOCAB / kMinChunk;
 
@@ -78,94 +79,6 @@ struct Space {
     int chunk, chunks;
 };
 
-__global__ __launch_bounds__(kThreads) void sample_count_kernel(SampleArgs a, Space sp) {
-    __shared__ uint32_t bins[kBins / 2];  // two 16-bit counts a word
-    __shared__ uint32_t wave_entries[kWaves], wave_largest[kWaves];
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = (int)sgpr(tid / kWave);
-    const int i0 = blockIdx.x * sp.chunk, i1 = min(i0 + sp.chunk, a.vocab);
-    const uint16_t* row = a.logits + (int64_t)blockIdx.y * a.stride;
-
-    // 16-byte loads from the first aligned logit on, on their way while LDS is cleared
-    const int skew = (int)((reinterpret_cast<uintptr_t>(row + i0) >> 1) & 7);
-    const int first = min(i0 + ((8 - skew) & 7), i1), wide = (i1 - first) / 8, tail = first + 8 * wide;
-    constexpr int kLoads = kMaxChunk / 8 / kThreads;
-    u32x4_t w[kLoads];
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u)
-        if (tid + u * kThreads < wide) w[u] = *reinterpret_cast<const u32x4_t*>(row + first + 8 * (tid + u * kThreads));
-    uint32_t edge = 0;
-    const bool has_edge = tid < first - i0 || (tid >= 8 && tid - 8 < i1 - tail);
-    if (has_edge) edge = row[tid < 8 ? i0 + tid : tail + tid - 8];
-    u32x4_t* clear = reinterpret_cast<u32x4_t*>(bins);
-#pragma unroll
-    for (int i = 0; i < kBins / 8 / kThreads; ++i) clear[i * kThreads + tid] = u32x4_t{0, 0, 0, 0};
-    __syncthreads();
-    const auto count = [&](uint32_t bin) { atomicAdd(&bins[bin >> 1], bin & 1 ? 0x10000u : 1u); };
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u)
-        if (tid + u * kThreads < wide) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t pair = bins_of_pair(w[u][e]);
-                count(pair & 0xFFFFu);
-                count(pair >> 16);
-            }
-        }
-    if (has_edge) count(bins_of_pair(edge) & 0xFFFFu);
-    __syncthreads();
-    if (tid == 0) {
-        bins[kPlusZero >> 1] += bins[kMinusZero >> 1] << 16;
-        bins[kMinusZero >> 1] &= 0xFFFF0000u;
-        bins[kFirstBin >> 1] &= 0xFFFF0000u;  // 0x7F is the upper half of its word
-    }
-    __syncthreads();
-
-    // A wave's 4096 bins, 128 at a time: the rounds with any in use (most
-    // values are far from any logit), how many those are, then the list.
-    constexpr int kRounds = kBins / 2 / kThreads;
-    const auto word_of = [&](int i) { return (wave * kRounds + i) * kWave + lane; };
-    // the words wholly outside the lists: before +infinity's, and from -infinity's on
-    const auto in_list = [&](uint32_t word) { return word - (kFirstBin >> 1) < (kEndBin >> 1) - (kFirstBin >> 1); };
-    uint32_t used = 0;
-#pragma unroll 8
-    for (int i = 0; i < kRounds; ++i) {
-        const uint32_t c = bins[word_of(i)];
-        used |= (uint32_t)(__any((c != 0) & in_list(word_of(i))) != 0) << i;
-    }
-    uint32_t total = 0, largest = 0;
-    used = sgpr(used);
-#pragma unroll 1
-    for (uint32_t rest = used; rest; rest &= rest - 1) {
-        const uint32_t word = word_of(__ffs(rest) - 1), c = bins[word] * (uint32_t)in_list(word);
-        total += __popcll(__ballot(c & 0xFFFFu)) + __popcll(__ballot(c >> 16));
-        largest = max(largest, max(c & 0xFFFFu, c >> 16));
-    }
-#pragma unroll
-    for (int m = 1; m < kWave; m <<= 1) largest = max(largest, (uint32_t)__shfl_xor((int)largest, m));
-    if (lane == 0) wave_entries[wave] = total, wave_largest[wave] = largest;
-    __syncthreads();
-    uint32_t at = 0, sum = 0;
-#pragma unroll 4
-    for (int u = 0; u < kWaves; ++u) {
-        if (u == wave) at = sum;
-        sum += wave_entries[u];
-        largest = max(largest, wave_largest[u]);
-    }
-    const size_t mine = (size_t)blockIdx.y * sp.chunks + blockIdx.x;
-    if (tid == 0) sp.infos[mine] = {sum, largest};
-    uint32_t* list = sp.lists + mine * sp.chunk;
-    const uint64_t below = (1ull << lane) - 1;
-#pragma unroll 1
-    for (uint32_t rest = used; rest; rest &= rest - 1) {
-        const uint32_t word = word_of(__ffs(rest) - 1), c = bins[word] * (uint32_t)in_list(word);
-        const uint64_t lo = __ballot(c & 0xFFFFu), hi = __ballot(c >> 16);
-        uint32_t to = at + __popcll(lo & below) + __popcll(hi & below);
-        if (c & 0xFFFFu) list[to++] = 2 * word << 16 | (c & 0xFFFFu);
-        if (c >> 16) list[to] = (2 * word + 1) << 16 | c >> 16;
-        at += __popcll(lo) + __popcll(hi);
-    }
-}
-
 // Running sums over a wave in six DPP steps (row_shr 1, 2, 4, 8, then the last
 // lane of a row of 16, and of the lower half, to the rows above).
 template <int kCtrl, int kRows>
@@ -207,6 +120,107 @@ __device__ __forceinline__ T shared_by_all(T v) {
     }
 }
 
+__global__ __launch_bounds__(kThreads) void sample_count_kernel(SampleArgs a, Space sp) {
+    __shared__ uint32_t bins[kBins / 2];  // two 16-bit counts a word
+    __shared__ uint32_t block_entries[kBlocks], wave_largest[kWaves];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = (int)sgpr(tid / kWave);
+    const int i0 = blockIdx.x * sp.chunk, i1 = min(i0 + sp.chunk, a.vocab);
+    const uint16_t* row = a.logits + (int64_t)blockIdx.y * a.stride;
+
+    // 16-byte loads from the first aligned logit on, on their way while LDS is cleared
+    const int skew = (int)((reinterpret_cast<uintptr_t>(row + i0) >> 1) & 7);
+    const int first = min(i0 + ((8 - skew) & 7), i1), wide = (i1 - first) / 8, tail = first + 8 * wide;
+    constexpr int kLoads = kMaxChunk / 8 / kThreads;
+    u32x4_t w[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+        if (tid + u * kThreads < wide) w[u] = *reinterpret_cast<const u32x4_t*>(row + first + 8 * (tid + u * kThreads));
+    uint32_t edge = 0;
+    const bool has_edge = tid < first - i0 || (tid >= 8 && tid - 8 < i1 - tail);
+    if (has_edge) edge = row[tid < 8 ? i0 + tid : tail + tid - 8];
+    u32x4_t* clear = reinterpret_cast<u32x4_t*>(bins);
+#pragma unroll
+    for (int i = 0; i < kBins / 8 / kThreads; ++i) clear[i * kThreads + tid] = u32x4_t{0, 0, 0, 0};
+    if (tid < kBlocks) block_entries[tid] = 0;
+    __syncthreads();
+    const auto count = [&](uint32_t bin) { atomicAdd(&bins[bin >> 1], bin & 1 ? 0x10000u : 1u); };
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+        if (tid + u * kThreads < wide) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t pair = bins_of_pair(w[u][e]);
+                count(pair & 0xFFFFu);
+                count(pair >> 16);
+            }
+        }
+    if (has_edge) count(bins_of_pair(edge) & 0xFFFFu);
+    __syncthreads();
+    if (tid == 0) {
+        bins[kPlusZero >> 1] += bins[kMinusZero >> 1] << 16;
+        bins[kMinusZero >> 1] &= 0xFFFF0000u;
+        bins[kFirstBin >> 1] &= 0xFFFF0000u;  // 0x7F is the upper half of its word
+    }
+    __syncthreads();
+
+    // Blocks of 128 bins in turn over the waves, since those in use lie
+    // together (a wave with 4096 bins of its own made a workgroup 1.5 us
+    // longer): which are in use at all, how many entries each has, the
+    // entries before each, then the list.
+    constexpr int kRounds = kBlocks / kWaves;
+    const auto word_of = [&](int i) { return (i * kWaves + wave) * kWave + lane; };
+    // the words wholly outside the lists: before +infinity's, and from -infinity's on
+    const auto in_list = [&](uint32_t word) { return word - (kFirstBin >> 1) < (kEndBin >> 1) - (kFirstBin >> 1); };
+    uint32_t used = 0;
+#pragma unroll 8
+    for (int i = 0; i < kRounds; ++i) {
+        const uint32_t c = bins[word_of(i)];
+        used |= (uint32_t)(__any((c != 0) & in_list(word_of(i))) != 0) << i;
+    }
+    uint32_t largest = 0;
+    used = sgpr(used);
+#pragma unroll 1
+    for (uint32_t rest = used; rest; rest &= rest - 1) {
+        const int i = __ffs(rest) - 1;
+        const uint32_t c = bins[word_of(i)] * (uint32_t)in_list(word_of(i));
+        const int n = __popcll(__ballot(c & 0xFFFFu)) + __popcll(__ballot(c >> 16));
+        if (lane == 0) block_entries[i * kWaves + wave] = n;
+        largest = max(largest, max(c & 0xFFFFu, c >> 16));
+    }
+#pragma unroll
+    for (int m = 1; m < kWave; m <<= 1) largest = max(largest, (uint32_t)__shfl_xor((int)largest, m));
+    if (lane == 0) wave_largest[wave] = largest;
+    __syncthreads();
+    // a lane's eight blocks: the wave's block of round i is one of lane 2 i + wave / 8
+    constexpr int kEach = kBlocks / kWave;
+    static_assert(kEach == 8 && kWaves == 16, "a lane's blocks and the waves' turns");
+    int all = 0, before = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int n = (int)block_entries[lane * kEach + k];
+        if (k < wave % kEach) before += n;
+        all += n;
+    }
+    const int upto = wave_scan(all);
+    before += upto - all;
+    const int sum = last_of(upto);
+#pragma unroll 4
+    for (int u = 0; u < kWaves; ++u) largest = max(largest, wave_largest[u]);
+    const size_t mine = (size_t)blockIdx.y * sp.chunks + blockIdx.x;
+    if (tid == 0) sp.infos[mine] = {(uint32_t)sum, largest};
+    uint32_t* list = sp.lists + mine * sp.chunk;
+    const uint64_t below = (1ull << lane) - 1;
+#pragma unroll 1
+    for (uint32_t rest = used; rest; rest &= rest - 1) {
+        const int i = __ffs(rest) - 1;
+        const uint32_t word = word_of(i), c = bins[word] * (uint32_t)in_list(word);
+        const uint64_t lo = __ballot(c & 0xFFFFu), hi = __ballot(c >> 16);
+        uint32_t to = lane_of(before, 2 * i + wave / kEach) + __popcll(lo & below) + __popcll(hi & below);
+        if (c & 0xFFFFu) list[to++] = 2 * word << 16 | (c & 0xFFFFu);
+        if (c >> 16) list[to] = (2 * word + 1) << 16 | c >> 16;
+    }
+}
+
 __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Space sp) {
     __shared__ uint32_t bins[kBins / 2];
     __shared__ int cnt[kThreads + 1];      // tokens before a segment of 64 bins
@@ -224,12 +238,26 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
     const uint32_t* lists = sp.lists + (size_t)row * sp.chunks * sp.chunk;
     uint32_t* far = sp.counts + (size_t)row * kBins;
 
-    // the row's settings, on their way from the start
-    const float heat = shared_by_all(a.temperature ? a.temperature[row] : 1.0f);
-    const float floor_p = shared_by_all(a.min_p ? a.min_p[row] : 0.0f);
-    const float p = shared_by_all(a.top_p ? a.top_p[row] : 1.0f);
-    const int top_k = shared_by_all(a.top_k ? a.top_k[row] : 0);
-    const double uniform = shared_by_all(a.uniform[row]);
+    // the row's settings and the first 64 chunks' infos, on their way while LDS is cleared
+    const float own_heat = a.temperature ? a.temperature[row] : 1.0f, own_floor = a.min_p ? a.min_p[row] : 0.0f;
+    const float own_p = a.top_p ? a.top_p[row] : 1.0f;
+    const int own_k = a.top_k ? a.top_k[row] : 0;
+    const double own_uniform = a.uniform[row];
+    ChunkInfo first_info = {0, 0};
+    uint32_t first_entry = 0;
+    if (lane < sp.chunks) {
+        first_info = infos[lane];
+        first_entry = lists[(size_t)lane * sp.chunk];
+    }
+    u32x4_t* clear = reinterpret_cast<u32x4_t*>(bins);
+#pragma unroll
+    for (int i = 0; i < kBins / 8 / kThreads; ++i) clear[i * kThreads + tid] = u32x4_t{0, 0, 0, 0};
+    own_cnt[tid] = 0;
+    own_mass[tid] = 0;
+    if (tid == 0) strong = 0;
+    const float heat = shared_by_all(own_heat), floor_p = shared_by_all(own_floor), p = shared_by_all(own_p);
+    const int top_k = shared_by_all(own_k);
+    const double uniform = shared_by_all(own_uniform);
     const bool greedy = !(heat > 0.0f);
     int keep = a.vocab;
     if (top_k > 0) keep = min(keep, top_k);
@@ -242,12 +270,16 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
     int run_base = 0;
     for (int c0 = 0; c0 < sp.chunks; c0 += kWave) {
         const int c = c0 + lane;
-        ChunkInfo info = {0, 0};
-        if (c < sp.chunks) {
-            info = infos[c];
-            const int first = (int)(lists[(size_t)c * sp.chunk] >> 16);  // of no meaning in an empty list
-            if (info.entries) top = min(top, first);
+        ChunkInfo info = first_info;
+        uint32_t first = first_entry;  // of no meaning in an empty list
+        if (c0 > 0) {
+            info = {0, 0};
+            if (c < sp.chunks) {
+                info = infos[c];
+                first = lists[(size_t)c * sp.chunk];
+            }
         }
+        if (info.entries) top = min(top, (int)(first >> 16));
         most += info.largest;
         const int joined = min((int)info.entries, keep);
         const int upto = run_base + wave_scan((joined + kRun - 1) / kRun);
@@ -269,17 +301,10 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
         if (tid == 0) a.tokens[row] = -1;
         return;
     }
-    if (near) {
-        u32x4_t* clear = reinterpret_cast<u32x4_t*>(bins);
-#pragma unroll
-        for (int i = 0; i < kBins / 8 / kThreads; ++i) clear[i * kThreads + tid] = u32x4_t{0, 0, 0, 0};
-    } else {
+    if (!near) {
         for (int i = tid; i < kBins; i += kThreads) __hip_atomic_store(&far[i], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __threadfence();
     }
-    own_cnt[tid] = 0;
-    own_mass[tid] = 0;
-    if (tid == 0) strong = 0;
     __syncthreads();
     // A wave takes every 16th run, four of them in flight.
 #pragma unroll 1
