@@ -423,7 +423,7 @@ struct Rows {
                         for (int r = 0; r < 4; ++r) {
                             uint32_t meta = vm[h][q][r];
                             if constexpr (masked.value) meta = seen[n] >> (4 * h + r) & 1 ? meta : 0;
-                            ps[h][r] = p[h][r] * lo16(meta);
+                            ps[h][r] = fmaf(p[h][r], lo16(meta), 0.0f);  // one mixed instruction, conversion and all
                             means[n][q] = fmaf(p[h][r], hi16(meta), means[n][q]);
                             scales[n][q] += ps[h][r];
                         }
@@ -1038,7 +1038,7 @@ __global__ __launch_bounds__(256, 2) void kv4_attn_sets_kernel(AttnArgs a) {
             float ps[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                ps[e] = p[e] * lo16(vm[q][e]);
+                ps[e] = fmaf(p[e], lo16(vm[q][e]), 0.0f);  // one mixed instruction, conversion and all
                 means[q] = fmaf(p[e], hi16(vm[q][e]), means[q]);
                 scales[q] += ps[e];
             }
