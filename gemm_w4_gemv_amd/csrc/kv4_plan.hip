@@ -8,7 +8,7 @@
 // are read by nobody, and the result does not depend on any order.
 // What bounds it is latency: a launch, the lengths' loads, a scan, then one
 // binary search in LDS and one dependent load per row (8 us a call, host time
-// included, for 256 requests of one token and for 32 of up to 2048).
+// included, for 256 requests of one token and for 1000 of up to 300).
 #include "kv4.hpp"
 #include "w4_device.hpp"
 
