@@ -121,17 +121,22 @@ __device__ __forceinline__ Request request_of(const AttnArgs& a, int b) {
 }
 
 // The tiles that some of a run of rows (positions low .. high) see: those of
-// the first tokens, then those of the window.
+// the first tokens, then those of the window.  A row that sees any token past
+// the table is NaN, so of those only as far as every such row sees one: a
+// length of no sense takes no longer than the table is.
 struct Tiles {
     int head, from, count;  // tile v of 0 .. count - 1 is v < head ? v : v - head + from
     __device__ __forceinline__ int at(int v) const { return v < head ? v : v - head + from; }
 };
 __device__ __forceinline__ Tiles tiles_of(const AttnArgs& a, int low, int high) {
     if (high < 0) return {0, 0, 0};
-    const int end = high / kTile + 1;
-    if (a.window == 0) return {0, 0, end};
+    const int past = (int)min((int64_t)a.width << a.c.shift, (int64_t)0x7FFFFFFF);
+    if (a.window == 0) return {0, 0, min(high, past) / kTile + 1};
+    const int end = min(high, max(past, high - a.window + 1)) / kTile + 1;
     const int from = max(max(low, 0) - a.window + 1, 0) / kTile;
-    const int head = min((min(a.sinks, high + 1) + kTile - 1) / kTile, from);
+    // tokens 0 .. last of the first ones (a.sinks = 0: none)
+    const int last = min(min(a.sinks - 1, high), past);
+    const int head = min(last < 0 ? 0 : last / kTile + 1, from);
     return {head, from, head + end - from};
 }
 
@@ -666,7 +671,7 @@ __global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
 
     // The running maximum moves only when a score passes it by 2^8: weights up
     // to 256 lose nothing, and a move costs a pass over the outputs.
-    const float slack = 8.0f / a.scale2;
+    const float slack = fminf(8.0f / a.scale2, 3e38f);
     const uint32_t bias = vgpr_const(kInt4BiasPair);
     const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
     // The next tile's keys are fetched when the scores are done with this
@@ -942,7 +947,7 @@ __global__ __launch_bounds__(256, 2) void kv4_attn_sets_kernel(AttnArgs a) {
         }
     };
 
-    const float slack = 8.0f / a.scale2;
+    const float slack = fminf(8.0f / a.scale2, 3e38f);
     const uint32_t bias = vgpr_const(kInt4BiasPair);
     const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
     for (int done = 1; v < v1; v += kWaves * kT, ++done) {
@@ -1272,7 +1277,7 @@ __global__ __launch_bounds__(256, 2) void kv4_attn_many_kernel(AttnArgs a) {
     rw.start();
     lds_barrier();
 
-    const float slack = 8.0f / a.scale2;
+    const float slack = fminf(8.0f / a.scale2, 3e38f);
     const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
     for (int done = 1; v < v1; ++v, ++done) {
         const int buffer = (done - 1) & 1;

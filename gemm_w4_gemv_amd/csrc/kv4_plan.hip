@@ -112,8 +112,10 @@ __global__ __launch_bounds__(kThreads) void kv4_plan_kernel(PlanArgs a) {
         }
     }
     // rows
-    for (int r0 = blockIdx.x * kRowsPer; r0 < a.rows; r0 += gridDim.x * kRowsPer) {
-        for (int r = r0 + tid; r < min(r0 + kRowsPer, a.rows); r += kThreads) {
+    for (int64_t r0 = (int64_t)blockIdx.x * kRowsPer; r0 < a.rows; r0 += (int64_t)gridDim.x * kRowsPer) {
+        const int end = (int)min(r0 + kRowsPer, (int64_t)a.rows) - (int)r0;
+        for (int i = tid; i < end; i += kThreads) {
+            const int r = (int)r0 + i;
             int pos = -1, slot = -1;
             if (r < total) {
                 const int b = last_at_most(start, a.B, r);

@@ -79,7 +79,8 @@ w4_status check_attn_shape(const char* fn, const w4_attn_args* a, const w4_kv4_c
         return fail(W4_ERR_SHAPE, "%s: %d query heads are no multiple of %d key/value heads", fn, a->q_heads, c->kv_heads);
     if (a->window < 0 || a->sinks < 0) return fail(W4_ERR_ARG, "%s: window and sinks must not be negative", fn);
     const int64_t rows = (int64_t)a->max_q * a->q_heads;
-    if (rows > (1ll << 28) || (rows > 0 && a->B > kMaxGrid / 256 / rows))
+    // workgroups of 256 threads, 16 rows of a key/value head each at least
+    if (rows > (1ll << 28) || (int64_t)a->B * (rows / 16 + c->kv_heads) > kMaxGrid / 256)
         return fail(W4_ERR_SHAPE, "%s: %d requests of %d rows of %d heads are too many for one call", fn, a->B, a->max_q,
                     a->q_heads);
     return W4_OK;

@@ -208,6 +208,8 @@ class DecodeStep:
         self.attention, self.sampler = attention, sampler
         self.linears = list(linears)
         self.stream = stream if stream is not None else torch.cuda.Stream()
+        if attention is not None or sampler is not None:  # their buffers are filled on the current stream
+            self.stream.wait_stream(torch.cuda.current_stream(self.stream.device))
         self.mode = mode
         self.graph: W4Graph | None = None
         self.chain = None

@@ -273,7 +273,7 @@ def w4_kv4_read(cache, slots, k_out=None, v_out=None, stream=None) -> None:
 
 def w4_kv4_attn_workspace_bytes(cache, T: int, B: int, q_heads: int, max_q: int, max_kv: int, window: int = 0,
                                 sinks: int = 0) -> int:
-    a = _AttnArgs(T=T, B=B, q_heads=q_heads, max_q=max_q, max_kv=min(max_kv, _INT_MAX), window=min(window, _INT_MAX),
+    a = _AttnArgs(T=T, B=B, q_heads=q_heads, max_q=min(max_q, _INT_MAX), max_kv=min(max_kv, _INT_MAX), window=min(window, _INT_MAX),
                   sinks=min(sinks, _INT_MAX))
     return lib.w4_kv4_attn_workspace_bytes(ctypes.byref(a), cache.ref)
 
@@ -300,7 +300,7 @@ def w4_kv4_attn(q, cache, block_table, kv_lens, out, q_start=None, max_q: int = 
         max_kv = width * cache.block_size
     a = _AttnArgs(qp, op, qs, os, _ptr(block_table, "block_table", _int32, i),
                   _vector(kv_lens, "kv_lens", _int32, i, B),
-                  None if q_start is None else _vector(q_start, "q_start", _int32, i, B + 1), T, B, q_heads, width, max_q,
+                  None if q_start is None else _vector(q_start, "q_start", _int32, i, B + 1), T, B, q_heads, width, min(max_q, _INT_MAX),
                   min(max_kv, _INT_MAX), min(window, _INT_MAX), min(sinks, _INT_MAX),
                   1.0 / math.sqrt(d) if scale is None else scale)
     pw, nbytes = None, 0

@@ -150,6 +150,75 @@ def test_no_table(kind, hq, hkv, dim, block):
     assert np.isnan(got[0]).all() and np.all(got[1] == 0)
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (3, 0), (40, 0), (1000, 0), (3, 30), (3, 10 ** 9), (2 ** 30, 5)])
+@pytest.mark.parametrize("kind,hq,hkv,dim,block", KINDS)
+def test_tokens_past_the_table(kind, hq, hkv, dim, block, window, sinks):
+    """Rows before, at and past the table's end, and lengths far past it: NaN exactly where a row sees a token there."""
+    reach = 2 * block
+    lens, news = [reach + 2, reach + 70, 2 ** 31 - 1, reach], [4, 2, 1, 1]
+    cache, table, q_start, q = attn_case(71, [reach] * 4, news, hq, hkv, dim, block)
+    got = attn(to_device(cache), q, table[:, :2], lens, q_start, rows_of(kind, hq, hkv, news), window=window, sinks=sinks,
+               scale=0.1, max_kv=reach + 70)
+    for b, (kv, n) in enumerate(zip(lens, news)):
+        for i in range(n):
+            row, pos = int(q_start[b]) + i, kv - n + i
+            near = max(pos - window + 1, 0) if window else 0  # the window's first token
+            past = pos >= reach and (near <= pos) and (max(near, reach) <= pos or sinks > reach)
+            if past:
+                assert np.isnan(got[row]).all(), (b, i)
+            else:
+                want, noise = ref.attention(q[row:row + 1], cache, table[b:b + 1], [pos + 1], [0, 1], 0.1, window, sinks)
+                check_attn(got[row:row + 1], want, noise, f"request {b} row {i}")
+
+
+@pytest.mark.parametrize("kind,hq,hkv,dim,block", KINDS)
+def test_tiny_scale(kind, hq, hkv, dim, block):
+    """A scale at the end of FP32: every visible token weighs the same."""
+    cache, table, q_start, q = attn_case(72, [70], [2], hq, hkv, dim, block)
+    got = attn(to_device(cache), q, table, [70], q_start, rows_of(kind, hq, hkv, [2]), scale=1.2e-38)
+    check_attn(got, *ref.attention(q, cache, table, [70], q_start, 0.0))
+
+
+def test_many_requests_of_long_prompts_are_one_call():
+    """256 requests with room for 2048 rows of 64 heads each, of which few are used."""
+    lens, news = [3] * 256, [1, 2] * 128
+    cache, table, q_start, q = attn_case(73, lens, news, 64, 8, 64, 16)
+    got = attn(to_device(cache), q, table, lens, q_start, 2048, scale=0.1)
+    want, noise = ref.attention(q[:6], cache, table[:4], lens[:4], q_start[:5], 0.1)
+    check_attn(got[:6], want, noise)
+    assert np.isfinite(got).all() and not np.any(got == 7.0)
+
+
+@pytest.mark.parametrize("kind,hq,hkv,dim,block", KINDS)
+def test_shared_pages_and_strided_rows(kind, hq, hkv, dim, block):
+    """Requests that share their first pages; q and out as strided rows of one buffer, side by side."""
+    lens, news = [3 * block, 2 * block + 5, 3 * block], [1, 2, 1]
+    cache, table, q_start, q = attn_case(74, lens, news, hq, hkv, dim, block)
+    table[1, :2] = table[0, :2]
+    table[2] = table[0]
+    T, wide = q.shape[0], hq * dim
+    space = torch.full((T, 2 * wide + 16), 7.0, dtype=bf16, device=DEV)
+    rows, out = (space[:, at:at + wide].unflatten(1, (hq, dim)) for at in (0, wide + 8))
+    rows.copy_(host.bf16_tensor(q))
+    with pytest.raises(w4.W4Error):  # the rows' spans overlap: refused, for out must not overlap an input
+        w4.w4_kv4_attn(rows, to_device(cache), ints(table), ints(lens), out, q_start=ints(q_start), max_q=2, max_kv=1)
+    out = torch.full((T, wide + 24), 7.0, dtype=bf16, device=DEV)[:, 8:8 + wide].unflatten(1, (hq, dim))
+    max_q = rows_of(kind, hq, hkv, news)
+    w4.w4_kv4_attn(rows, to_device(cache), ints(table), ints(lens), out, q_start=ints(q_start), max_q=max_q, max_kv=1, scale=0.1)
+    torch.cuda.synchronize()
+    check_attn(host.bf16_values(out.contiguous()), *ref.attention(q, cache, table, lens, q_start, 0.1))
+    around = out._base if out._base is not None else out
+    assert torch.all(around.view(T, -1)[:, :8] == 7.0) and torch.all(around.view(T, -1)[:, 8 + wide:] == 7.0)
+
+
+@pytest.mark.parametrize("hq,dim,block", [(128, 64, 16), (100, 256, 64), (17, 128, 32)])
+def test_many_heads_to_a_key_head(hq, dim, block):
+    lens = [70, 1, 400]
+    cache, table, q_start, q = attn_case(75, lens, [1] * 3, hq, 1, dim, block)
+    got = attn(to_device(cache), q, table, lens, q_start, 1)
+    check_attn(got, *ref.attention(q, cache, table, lens, q_start, float(np.float32(dim ** -0.5)), 0, 0, TWO_PARTS))
+
+
 @pytest.mark.parametrize("max_q", [1, 2, 30])
 def test_rows_past_max_q_are_left(max_q):
     lens, news = [80, 9], [40, 1]
