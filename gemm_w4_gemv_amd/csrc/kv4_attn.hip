@@ -27,9 +27,9 @@
 // and a second kernel joins those.
 //
 // Measured: 32 requests of up to 8192 tokens, 16 query and 8 key/value heads of
-// 256: 77 us, 4.7 TB/s of codes and pairs (the same loads with a sum instead of
-// the attention: 76); one of 131071 tokens, 32 and 8 heads of 128: 32 us, 4.4
-// TB/s; a prompt's 2048 tokens after 2048 others, 16 and 8 heads of 256: 186 us, 555
+// 256: 77 us, 4.7 TB/s of codes and pairs (with exclusive-ors for the products and
+// the same loads: 76); one of 131071 tokens, 32 and 8 heads of 128: 31 us, 4.6
+// TB/s; a prompt's 2048 tokens after 2048 others, 16 and 8 heads of 256: 179 us, 576
 // TFLOP/s.
 #include <type_traits>
 
@@ -814,9 +814,9 @@ __device__ __forceinline__ float over_sets(float v, F f) {
 // the end as the waves are.
 // Per 32 tokens of D = 128 and 4 rows that is some 160 vector instructions
 // instead of 260.
-template <int D, int kSets, bool kWide>
-__global__ __launch_bounds__(256, 2) void kv4_attn_sets_kernel(AttnArgs a) {
-    constexpr int kWaves = 4, kT = kSets / 2, kCols = 16 / kSets;  // tiles at a time; rows
+template <int D, int kSets, int kWaves, bool kWide>
+__global__ __launch_bounds__(kWaves * kWave, 2) void kv4_attn_sets_kernel(AttnArgs a) {
+    constexpr int kT = kSets / 2, kCols = 16 / kSets;  // tiles at a time; rows
     constexpr int kG = Frag<D>::kG, kW = Frag<D>::kW, kJ = D == 64 ? 4 : 8;
     constexpr int kAll = kG * 4 * kJ, kMine = kAll / kSets;  // a lane's outputs, before and after the sets are joined
     __shared__ float so[kWaves][kMine][kWave];
@@ -1395,6 +1395,7 @@ struct Cut {
     int sets;       // kv4_attn_sets_kernel if over 1
     int row_tiles;  // of a request, each a workgroup's rows
     int splits;     // workgroups that share a row tile's tokens
+    int waves;      // of a workgroup
 };
 constexpr int kFewWaves = 4;
 // 16-row blocks of a wave: as many as leave two waves a SIMD.
@@ -1423,30 +1424,54 @@ Cut cut_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     k.sets = rows > 8 ? 1 : rows > 4 || c.head_dim == 256 ? 2 : 4;
     const int64_t tile = k.many ? many_rows : 16;
     k.row_tiles = (int)((rows + tile - 1) / tile);
-    // Enough workgroups to fill the chip twice, with two tiles at least for
-    // each of the waves that share them.  Twice that number where requests
-    // differ in length (a window makes them alike): 32 requests of up to 8192
-    // tokens take 80 us then, 86 without; one of 131071 tokens 33 instead
-    // of 32, and 64 that a window holds to 1024 tokens 20 instead of 14.
+    // As many workgroups as are on the chip at once, two a compute unit: with a
+    // few more, the rest would run after them.  Twice that number where requests
+    // differ in length (a window makes them alike) and a wave keeps four tiles: 32
+    // requests of up to 8192 tokens take 80 us then, 86 without; one of 131071
+    // tokens 33 instead of 32.  Two tiles at least for each of the waves, eight
+    // where there is a workgroup a compute unit without splits: 56 requests of
+    // 1000 tokens, 16 query and 8 key/value heads of 256, 27 us instead of 41 (of
+    // 8000 tokens 178 either way).
     const int64_t groups = (int64_t)a.B * c.kv_heads * k.row_tiles;
     int64_t tokens = a.max_kv;
     if (a.window > 0) tokens = tokens < (int64_t)a.window + a.sinks + a.max_q ? tokens : (int64_t)a.window + a.sinks + a.max_q;
     const int64_t tiles = (tokens + kTile - 1) / kTile;
-    const int64_t fill = a.B > 1 && a.window == 0 ? 1024 : 512;
-    int64_t want = k.many ? 1 : (fill + groups - 1) / (groups > 0 ? groups : 1);
-    const int64_t most = tiles / (2 * kFewWaves);
+    const int64_t fill = a.B > 1 && a.window == 0 && tiles * groups >= 1024 * 4 * kFewWaves ? 1024 : 512;
+    int64_t want = k.many ? 1 : fill / (groups > 0 ? groups : 1);
+    const int64_t most = tiles / ((groups > 256 ? 8 : 2) * kFewWaves);
     want = want < most ? want : most;
     k.splits = (int)(want < 1 ? 1 : want > kMaxSplits ? kMaxSplits : want);
+    // Up to 256 workgroups (512 with heads of 64, of half the registers) can have
+    // eight waves, each with half the tiles: unsplit they save the join's launch.
+    // Worth it for short contexts (heads of 128, 8 requests of 1000 tokens: 10.2
+    // us, split 11.5; of 2000 14.3, split 13.1) and where splits would share a
+    // compute unit anyway (32 of 1000 tokens 11.0, split 14.8; of 4000 24, split
+    // 27; heads of 256, 32 of 1000 tokens 16.7, split 24.3; but 16, 128
+    // workgroups, of 4000 tokens 44, split 36).
+    k.waves = 4;
+    if (k.sets > 1 && groups <= (c.head_dim == 64 ? 512 : 256) &&
+        (tiles * c.head_dim <= 5120 || (groups >= 160 && tiles <= 128))) {
+        k.waves = 8;
+        k.splits = 1;
+    }
     return k;
 }
 
 template <int D, bool kWide>
 hipError_t launch_d(const AttnArgs& k, const Cut& cut, int64_t groups, hipStream_t stream) {
-    const dim3 grid((unsigned)groups), block(256);
-    if (cut.sets == 2) {
-        kv4_attn_sets_kernel<D, 2, kWide><<<grid, block, 0, stream>>>(k);
+    const dim3 grid((unsigned)groups), block((unsigned)cut.waves * kWave);
+    if (cut.sets == 2 && cut.waves == 8) {
+        kv4_attn_sets_kernel<D, 2, 8, kWide><<<grid, block, 0, stream>>>(k);
+    } else if (cut.sets == 2) {
+        kv4_attn_sets_kernel<D, 2, 4, kWide><<<grid, block, 0, stream>>>(k);
     } else if (cut.sets == 4) {
-        if constexpr (D < 256) kv4_attn_sets_kernel<D, 4, kWide><<<grid, block, 0, stream>>>(k);
+        if constexpr (D < 256) {
+            if (cut.waves == 8) {
+                kv4_attn_sets_kernel<D, 4, 8, kWide><<<grid, block, 0, stream>>>(k);
+            } else {
+                kv4_attn_sets_kernel<D, 4, 4, kWide><<<grid, block, 0, stream>>>(k);
+            }
+        }
     } else if (cut.many) {
         kv4_attn_many_kernel<D, many_blocks(D), kWide><<<grid, block, 0, stream>>>(k);
     } else {

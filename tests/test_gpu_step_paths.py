@@ -189,6 +189,18 @@ def test_many_requests_of_long_prompts_are_one_call():
     assert np.isfinite(got).all() and not np.any(got == 7.0)
 
 
+@pytest.mark.parametrize("hq,dim,block", [(16, 64, 16), (64, 64, 64), (8, 128, 32), (40, 128, 16), (16, 256, 16), (32, 256, 64)])
+@pytest.mark.parametrize("B,max_kv", [(70, 50), (70, 10 ** 6), (3, 50), (3, 1100), (3, 10 ** 6), (25, 3000)])
+def test_any_cut(hq, dim, block, B, max_kv):
+    """Four waves and eight, split and whole, with and without tokens for every part."""
+    g = si.rng(76, B, dim)
+    lens = [int(v) for v in g.integers(0, 90, B)]
+    lens[0], lens[-1] = 0, 300
+    cache, table, q_start, q = attn_case(76, lens, [1] * B, hq, 8, dim, block)
+    got = attn(to_device(cache), q, table, lens, q_start, 1, max_kv=max_kv, scale=0.1)
+    check_attn(got, *ref.attention(q, cache, table, lens, q_start, 0.1, 0, 0, TWO_PARTS))
+
+
 @pytest.mark.parametrize("kind,hq,hkv,dim,block", KINDS)
 def test_shared_pages_and_strided_rows(kind, hq, hkv, dim, block):
     """Requests that share their first pages; q and out as strided rows of one buffer, side by side."""
