@@ -15,6 +15,9 @@
 //      running counts over 1024 segments of 64 values, masses (count *
 //      exp(z), FP64) of those up to the k-th, the cuts and the draw; then the
 //      chunk, and in it the index, of the drawn value's j-th place.
+// Rows of up to 32768 logits are one chunk: the pick counts them itself, in
+// one launch and without lists (one row of 32000: 15 us instead of 21, 300 rows
+// 30 instead of 44).
 // What bounds it: the count by the turns that LDS atomics take (64 rows of
 // 262144: 18 us, 1.8 TB/s of logits), the pick by the length of its chain of
 // dependent steps (17 us for one row, 22 for 64, a compute unit each).
@@ -120,13 +123,10 @@ __device__ __forceinline__ T shared_by_all(T v) {
     }
 }
 
-__global__ __launch_bounds__(kThreads) void sample_count_kernel(SampleArgs a, Space sp) {
-    __shared__ uint32_t bins[kBins / 2];  // two 16-bit counts a word
-    __shared__ uint32_t block_entries[kBlocks], wave_largest[kWaves];
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = (int)sgpr(tid / kWave);
-    const int i0 = blockIdx.x * sp.chunk, i1 = min(i0 + sp.chunk, a.vocab);
-    const uint16_t* row = a.logits + (int64_t)blockIdx.y * a.stride;
-
+// Counts logits i0 .. i1 - 1 of a row into LDS, two 16-bit counts a word, and
+// takes out what is in no list.  On return all counts are there for all.
+__device__ __forceinline__ void count_into(uint32_t* bins, const uint16_t* row, int i0, int i1) {
+    const int tid = threadIdx.x;
     // 16-byte loads from the first aligned logit on, on their way while LDS is cleared
     const int skew = (int)((reinterpret_cast<uintptr_t>(row + i0) >> 1) & 7);
     const int first = min(i0 + ((8 - skew) & 7), i1), wide = (i1 - first) / 8, tail = first + 8 * wide;
@@ -141,7 +141,6 @@ __global__ __launch_bounds__(kThreads) void sample_count_kernel(SampleArgs a, Sp
     u32x4_t* clear = reinterpret_cast<u32x4_t*>(bins);
 #pragma unroll
     for (int i = 0; i < kBins / 8 / kThreads; ++i) clear[i * kThreads + tid] = u32x4_t{0, 0, 0, 0};
-    if (tid < kBlocks) block_entries[tid] = 0;
     __syncthreads();
     const auto count = [&](uint32_t bin) { atomicAdd(&bins[bin >> 1], bin & 1 ? 0x10000u : 1u); };
 #pragma unroll
@@ -156,12 +155,27 @@ __global__ __launch_bounds__(kThreads) void sample_count_kernel(SampleArgs a, Sp
         }
     if (has_edge) count(bins_of_pair(edge) & 0xFFFFu);
     __syncthreads();
-    if (tid == 0) {
+    constexpr int kBefore = kFirstBin >> 1, kAfter = (kBins - kEndBin) >> 1;
+    static_assert(kBefore <= kThreads / 2 && kAfter <= kThreads / 2 && kFirstBin % 2 == 1 && kEndBin % 2 == 0, "a thread a word");
+    if (tid < kBefore) bins[tid] = 0;
+    if (tid >= kThreads / 2 && tid < kThreads / 2 + kAfter) bins[kEndBin / 2 + tid - kThreads / 2] = 0;
+    if (tid == kBefore) {
         bins[kPlusZero >> 1] += bins[kMinusZero >> 1] << 16;
         bins[kMinusZero >> 1] &= 0xFFFF0000u;
-        bins[kFirstBin >> 1] &= 0xFFFF0000u;  // 0x7F is the upper half of its word
+        bins[kBefore] &= 0xFFFF0000u;  // +infinity is the upper half of its word
     }
     __syncthreads();
+}
+
+__global__ __launch_bounds__(kThreads) void sample_count_kernel(SampleArgs a, Space sp) {
+    __shared__ uint32_t bins[kBins / 2];  // two 16-bit counts a word
+    __shared__ uint32_t block_entries[kBlocks], wave_largest[kWaves];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = (int)sgpr(tid / kWave);
+    const int i0 = blockIdx.x * sp.chunk, i1 = min(i0 + sp.chunk, a.vocab);
+    const uint16_t* row = a.logits + (int64_t)blockIdx.y * a.stride;
+
+    if (tid < kBlocks) block_entries[tid] = 0;
+    count_into(bins, row, i0, i1);
 
     // Blocks of 128 bins in turn over the waves, since those in use lie
     // together (a wave with 4096 bins of its own made a workgroup 1.5 us
@@ -169,20 +183,17 @@ __global__ __launch_bounds__(kThreads) void sample_count_kernel(SampleArgs a, Sp
     // entries before each, then the list.
     constexpr int kRounds = kBlocks / kWaves;
     const auto word_of = [&](int i) { return (i * kWaves + wave) * kWave + lane; };
-    // the words wholly outside the lists: before +infinity's, and from -infinity's on
-    const auto in_list = [&](uint32_t word) { return word - (kFirstBin >> 1) < (kEndBin >> 1) - (kFirstBin >> 1); };
     uint32_t used = 0;
 #pragma unroll 8
     for (int i = 0; i < kRounds; ++i) {
-        const uint32_t c = bins[word_of(i)];
-        used |= (uint32_t)(__any((c != 0) & in_list(word_of(i))) != 0) << i;
+        used |= (uint32_t)(__any(bins[word_of(i)] != 0) != 0) << i;
     }
     uint32_t largest = 0;
     used = sgpr(used);
 #pragma unroll 1
     for (uint32_t rest = used; rest; rest &= rest - 1) {
         const int i = __ffs(rest) - 1;
-        const uint32_t c = bins[word_of(i)] * (uint32_t)in_list(word_of(i));
+        const uint32_t c = bins[word_of(i)];
         const int n = __popcll(__ballot(c & 0xFFFFu)) + __popcll(__ballot(c >> 16));
         if (lane == 0) block_entries[i * kWaves + wave] = n;
         largest = max(largest, max(c & 0xFFFFu, c >> 16));
@@ -213,7 +224,7 @@ __global__ __launch_bounds__(kThreads) void sample_count_kernel(SampleArgs a, Sp
 #pragma unroll 1
     for (uint32_t rest = used; rest; rest &= rest - 1) {
         const int i = __ffs(rest) - 1;
-        const uint32_t word = word_of(i), c = bins[word] * (uint32_t)in_list(word);
+        const uint32_t word = word_of(i), c = bins[word];
         const uint64_t lo = __ballot(c & 0xFFFFu), hi = __ballot(c >> 16);
         uint32_t to = lane_of(before, 2 * i + wave / kEach) + __popcll(lo & below) + __popcll(hi & below);
         if (c & 0xFFFFu) list[to++] = 2 * word << 16 | (c & 0xFFFFu);
@@ -221,6 +232,8 @@ __global__ __launch_bounds__(kThreads) void sample_count_kernel(SampleArgs a, Sp
     }
 }
 
+// kWhole: rows of one chunk, counted here; there are no lists.
+template <bool kWhole>
 __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Space sp) {
     __shared__ uint32_t bins[kBins / 2];
     __shared__ int cnt[kThreads + 1];      // tokens before a segment of 64 bins
@@ -231,7 +244,9 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
     __shared__ int wave_cnt[kWaves];
     __shared__ int drawn[2];  // the bin, and the place among its tokens
     __shared__ int strong;  // tokens with w >= min_p
-    __shared__ int at_chunk[kMaxChunks], entries[kMaxChunks], runs[kMaxChunks + 1];
+    constexpr int kLists = kWhole ? 1 : kMaxChunks;
+    __shared__ int at_chunk[kLists], entries[kLists], runs[kLists + 1];
+    __shared__ int first_bin;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = (int)sgpr(tid / kWave);
     const int row = blockIdx.x;
     const ChunkInfo* infos = sp.infos + (size_t)row * sp.chunks;
@@ -245,16 +260,21 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
     const double own_uniform = a.uniform[row];
     ChunkInfo first_info = {0, 0};
     uint32_t first_entry = 0;
-    if (lane < sp.chunks) {
-        first_info = infos[lane];
-        first_entry = lists[(size_t)lane * sp.chunk];
-    }
-    u32x4_t* clear = reinterpret_cast<u32x4_t*>(bins);
+    if constexpr (!kWhole) {
+        if (lane < sp.chunks) {
+            first_info = infos[lane];
+            first_entry = lists[(size_t)lane * sp.chunk];
+        }
+        u32x4_t* clear = reinterpret_cast<u32x4_t*>(bins);
 #pragma unroll
-    for (int i = 0; i < kBins / 8 / kThreads; ++i) clear[i * kThreads + tid] = u32x4_t{0, 0, 0, 0};
+        for (int i = 0; i < kBins / 8 / kThreads; ++i) clear[i * kThreads + tid] = u32x4_t{0, 0, 0, 0};
+    }
     own_cnt[tid] = 0;
     own_mass[tid] = 0;
-    if (tid == 0) strong = 0;
+    if (tid == 0) {
+        strong = 0;
+        first_bin = kBins;
+    }
     const float heat = shared_by_all(own_heat), floor_p = shared_by_all(own_floor), p = shared_by_all(own_p);
     const int top_k = shared_by_all(own_k);
     const double uniform = shared_by_all(own_uniform);
@@ -263,92 +283,90 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
     if (top_k > 0) keep = min(keep, top_k);
     if (greedy) keep = 1;
 
-    // The largest value, whether the joined counts fit 16 bits, and the runs
-    // of entries up to each chunk.
     int top = kBins;
-    uint32_t most = 0;
-    int run_base = 0;
-    for (int c0 = 0; c0 < sp.chunks; c0 += kWave) {
-        const int c = c0 + lane;
-        ChunkInfo info = first_info;
-        uint32_t first = first_entry;  // of no meaning in an empty list
-        if (c0 > 0) {
-            info = {0, 0};
-            if (c < sp.chunks) {
-                info = infos[c];
-                first = lists[(size_t)c * sp.chunk];
+    bool near = true;  // the counts are in LDS, in 16 bits
+    if constexpr (kWhole) {
+        count_into(bins, a.logits + (int64_t)row * a.stride, 0, a.vocab);
+    } else {
+        // The largest value, whether the joined counts fit 16 bits, and the runs
+        // of entries up to each chunk.
+        uint32_t most = 0;
+        int run_base = 0;
+        for (int c0 = 0; c0 < sp.chunks; c0 += kWave) {
+            const int c = c0 + lane;
+            ChunkInfo info = first_info;
+            uint32_t first = first_entry;  // of no meaning in an empty list
+            if (c0 > 0) {
+                info = {0, 0};
+                if (c < sp.chunks) {
+                    info = infos[c];
+                    first = lists[(size_t)c * sp.chunk];
+                }
+            }
+            if (info.entries) top = min(top, (int)(first >> 16));
+            most += info.largest;
+            const int joined = min((int)info.entries, keep);
+            const int upto = run_base + wave_scan((joined + kRun - 1) / kRun);
+            if (wave == 0 && c < sp.chunks) {
+                entries[c] = (int)info.entries;
+                runs[c + 1] = upto;
+            }
+            run_base = last_of(upto);
+        }
+        if (tid == 0) runs[0] = 0;
+#pragma unroll
+        for (int m = 1; m < kWave; m <<= 1) {
+            top = min(top, __shfl_xor(top, m));
+            most += __shfl_xor((int)most, m);
+        }
+        top = shared_by_all(top);
+        near = shared_by_all(most) < 65536u;  // else the counts are kept in memory
+        if (top == kBins) {
+            if (tid == 0) a.tokens[row] = -1;
+            return;
+        }
+        if (!near) {
+            for (int i = tid; i < kBins; i += kThreads) __hip_atomic_store(&far[i], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __threadfence();
+        }
+        __syncthreads();
+        // A wave takes every 16th run, four of them in flight.
+#pragma unroll 1
+        for (int r0 = wave, c = 0; r0 < run_base; r0 += 4 * kWaves) {
+            uint32_t x[4][kRun / kWave] = {};  // 0: none, adds nothing
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = r0 + k * kWaves;
+                if (r >= run_base) continue;
+                while (r >= runs[c + 1]) ++c;
+                const int i = (r - runs[c]) * kRun + lane, n = min(entries[c], keep);
+                const uint32_t* list = lists + (size_t)c * sp.chunk;
+#pragma unroll
+                for (int u = 0; u < kRun / kWave; ++u)
+                    if (i + u * kWave < n) x[k][u] = list[i + u * kWave];
+            }
+            if (near) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int u = 0; u < kRun / kWave; ++u)
+                        if (x[k][u])  // adding 0 to one place from many lanes costs a turn each
+                            atomicAdd(&bins[x[k][u] >> 17], (x[k][u] & 0xFFFFu) << (x[k][u] >> 12 & 16));
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int u = 0; u < kRun / kWave; ++u)
+                        if (x[k][u])
+                            __hip_atomic_fetch_add(&far[x[k][u] >> 16], x[k][u] & 0xFFFFu, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
         }
-        if (info.entries) top = min(top, (int)(first >> 16));
-        most += info.largest;
-        const int joined = min((int)info.entries, keep);
-        const int upto = run_base + wave_scan((joined + kRun - 1) / kRun);
-        if (wave == 0 && c < sp.chunks) {
-            entries[c] = (int)info.entries;
-            runs[c + 1] = upto;
-        }
-        run_base = last_of(upto);
+        if (!near) __threadfence();
+        __syncthreads();
     }
-    if (tid == 0) runs[0] = 0;
-#pragma unroll
-    for (int m = 1; m < kWave; m <<= 1) {
-        top = min(top, __shfl_xor(top, m));
-        most += __shfl_xor((int)most, m);
-    }
-    top = shared_by_all(top);
-    const bool near = shared_by_all(most) < 65536u;  // else the counts are kept in memory
-    if (top == kBins) {
-        if (tid == 0) a.tokens[row] = -1;
-        return;
-    }
-    if (!near) {
-        for (int i = tid; i < kBins; i += kThreads) __hip_atomic_store(&far[i], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __threadfence();
-    }
-    __syncthreads();
-    // A wave takes every 16th run, four of them in flight.
-#pragma unroll 1
-    for (int r0 = wave, c = 0; r0 < run_base; r0 += 4 * kWaves) {
-        uint32_t x[4][kRun / kWave] = {};  // 0: none, adds nothing
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int r = r0 + k * kWaves;
-            if (r >= run_base) continue;
-            while (r >= runs[c + 1]) ++c;
-            const int i = (r - runs[c]) * kRun + lane, n = min(entries[c], keep);
-            const uint32_t* list = lists + (size_t)c * sp.chunk;
-#pragma unroll
-            for (int u = 0; u < kRun / kWave; ++u)
-                if (i + u * kWave < n) x[k][u] = list[i + u * kWave];
-        }
-        if (near) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int u = 0; u < kRun / kWave; ++u)
-                    if (x[k][u])  // adding 0 to one place from many lanes costs a turn each
-                        atomicAdd(&bins[x[k][u] >> 17], (x[k][u] & 0xFFFFu) << (x[k][u] >> 12 & 16));
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int u = 0; u < kRun / kWave; ++u)
-                    if (x[k][u])
-                        __hip_atomic_fetch_add(&far[x[k][u] >> 16], x[k][u] & 0xFFFFu, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-    }
-    if (!near) __threadfence();
-    __syncthreads();
     const auto count = [&](int bin) -> int {
-        if (near) return (int)(bins[bin >> 1] >> (16 * (bin & 1)) & 0xFFFFu);
+        if (kWhole || near) return (int)(bins[bin >> 1] >> (16 * (bin & 1)) & 0xFFFFu);
         return (int)__hip_atomic_load(&far[bin], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    };
-
-    const double largest = bf16_to_f32(bits_of_bin(top));
-    const double rate = greedy ? 1.0 : 1.4426950408889634074 / (double)heat;
-    const auto weight = [&](int bin) {
-        if (bin == top) return 1.0;  // also where the largest is an infinity
-        return exp2_series(((double)bf16_to_f32(bits_of_bin(bin)) - largest) * rate);
     };
 
     // Running sums over the segments, a thread each.
@@ -363,13 +381,20 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
     // use lie together): first which of a wave's 32 pairs are in use.
     const auto pair_of = [&](int i) { return i * kWaves + wave; };
     uint32_t used = 0;
-    if (near) {
+    if (kWhole || near) {
 #pragma unroll
         for (int i = 0; i < kThreads / kWaves / 2; ++i)  // a pair's 128 counts are 64 words
             if (__any(bins[pair_of(i) * kWave + lane] != 0)) used |= 1u << i;
     } else {
         for (int i = 0; i < kThreads / kWaves / 2; ++i)
             if (__any((count(2 * pair_of(i) * kWave + lane) | count((2 * pair_of(i) + 1) * kWave + lane)) != 0)) used |= 1u << i;
+    }
+    if constexpr (kWhole) {
+        if (used) {  // this wave's first value, of which the first of all is the largest logit
+            const int word = pair_of(__ffs(used) - 1) * kWave + lane;
+            const uint64_t some = __ballot(bins[word] != 0);
+            if (lane == __ffsll((unsigned long long)some) - 1) atomicMin(&first_bin, 2 * word + ((bins[word] & 0xFFFFu) == 0));
+        }
     }
 #pragma unroll 1
     for (uint32_t rest = used; rest; rest &= rest - 1) {
@@ -381,6 +406,20 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
         }
     }
     __syncthreads();
+    if constexpr (kWhole) {
+        top = shared_by_all(first_bin);
+        if (top == kBins) {
+            if (tid == 0) a.tokens[row] = -1;
+            return;
+        }
+    }
+    const double largest = bf16_to_f32(bits_of_bin(top));
+    const double rate = greedy ? 1.0 : 1.4426950408889634074 / (double)heat;
+    const auto weight = [&](int bin) {
+        if (bin == top) return 1.0;  // also where the largest is an infinity
+        return exp2_series(((double)bf16_to_f32(bits_of_bin(bin)) - largest) * rate);
+    };
+
     const int own_c = own_cnt[tid];
     const int sc = run_over(own_c, wave_cnt);
     cnt[tid + 1] = sc;
@@ -473,38 +512,40 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
     const uint32_t want = (uint32_t)shared_by_all(drawn[0]);
     const int among = shared_by_all(drawn[1]);
 
-    // How many of them each chunk holds: its list is sorted, so 64 places of
-    // it at a time narrow it down.
-    for (int c = wave; c < sp.chunks; c += kWaves) {
-        const uint32_t* list = lists + (size_t)c * sp.chunk;
-        int lo = 0, n = shared_by_all(entries[c]);  // entries lo .. lo + n - 1 may be the one
-        while (n > kWave) {
-            const int step = (n + kWave - 1) / kWave, i = lane * step;
-            // places at or below the value: a beginning of the lanes
-            const int below = __popcll(__ballot(i < n && list[lo + (i < n ? i : 0)] >> 16 <= want));
-            const int from = max(below - 1, 0) * step;
-            lo += from;
-            n = min(step, n - from);
-        }
-        const uint32_t x = lane < n ? list[lo + lane] : 0;
-        const uint64_t found = __ballot(lane < n && x >> 16 == want);
-        if (lane == 0) at_chunk[c] = 0;
-        if (found >> lane & 1) at_chunk[c] = (int)(x & 0xFFFFu);
-    }
-    __syncthreads();
     int before = 0, chunk = 0;  // the chunk with the among-th, and those before it
-    for (int c0 = 0; c0 < sp.chunks; c0 += kWave) {
-        const int h = c0 + lane < sp.chunks ? at_chunk[c0 + lane] : 0, sum = before + wave_scan(h);
-        const uint64_t past = __ballot(sum > among);
-        if (past) {
-            const int l = __ffsll((unsigned long long)past) - 1;
-            chunk = c0 + l;
-            before = lane_of(sum - h, l);
-            break;
+    if constexpr (!kWhole) {
+        // How many of them each chunk holds: its list is sorted, so 64 places of
+        // it at a time narrow it down.
+        for (int c = wave; c < sp.chunks; c += kWaves) {
+            const uint32_t* list = lists + (size_t)c * sp.chunk;
+            int lo = 0, n = shared_by_all(entries[c]);  // entries lo .. lo + n - 1 may be the one
+            while (n > kWave) {
+                const int step = (n + kWave - 1) / kWave, i = lane * step;
+                // places at or below the value: a beginning of the lanes
+                const int below = __popcll(__ballot(i < n && list[lo + (i < n ? i : 0)] >> 16 <= want));
+                const int from = max(below - 1, 0) * step;
+                lo += from;
+                n = min(step, n - from);
+            }
+            const uint32_t x = lane < n ? list[lo + lane] : 0;
+            const uint64_t found = __ballot(lane < n && x >> 16 == want);
+            if (lane == 0) at_chunk[c] = 0;
+            if (found >> lane & 1) at_chunk[c] = (int)(x & 0xFFFFu);
         }
-        before = last_of(sum);
+        __syncthreads();
+        for (int c0 = 0; c0 < sp.chunks; c0 += kWave) {
+            const int h = c0 + lane < sp.chunks ? at_chunk[c0 + lane] : 0, sum = before + wave_scan(h);
+            const uint64_t past = __ballot(sum > among);
+            if (past) {
+                const int l = __ffsll((unsigned long long)past) - 1;
+                chunk = c0 + l;
+                before = lane_of(sum - h, l);
+                break;
+            }
+            before = last_of(sum);
+        }
+        __syncthreads();
     }
-    __syncthreads();
 
     // Matches in pieces of 512 of its logits (eight a lane, 16-byte aligned),
     // their running sum, then that one piece again.
@@ -582,13 +623,20 @@ int chunk_of(int rows, int vocab) {
 }  // namespace
 
 size_t sample_workspace_bytes(int rows, int vocab) {
+    if (vocab <= kMaxChunk) return 0;
     const int chunk = chunk_of(rows, vocab);
     const size_t chunks = (size_t)rows * ((vocab + chunk - 1) / chunk);
     return chunks * chunk * 4 + chunks * sizeof(ChunkInfo) + (vocab > 65535 ? (size_t)rows * kBins * 4 : 0);
 }
 
 hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t stream) {
-    Space sp;
+    Space sp = {};
+    if (a.vocab <= kMaxChunk) {
+        sp.chunk = kMaxChunk;
+        sp.chunks = 1;
+        sample_pick_kernel<true><<<dim3((unsigned)a.rows), dim3(kThreads), 0, stream>>>(a, sp);
+        return hipGetLastError();
+    }
     sp.chunk = chunk_of(a.rows, a.vocab);
     sp.chunks = (a.vocab + sp.chunk - 1) / sp.chunk;
     const size_t chunks = (size_t)a.rows * sp.chunks;
@@ -598,7 +646,7 @@ hipError_t launch_sample(const SampleArgs& a, void* workspace, hipStream_t strea
     sample_count_kernel<<<dim3((unsigned)sp.chunks, (unsigned)a.rows), dim3(kThreads), 0, stream>>>(a, sp);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    sample_pick_kernel<<<dim3((unsigned)a.rows), dim3(kThreads), 0, stream>>>(a, sp);
+    sample_pick_kernel<false><<<dim3((unsigned)a.rows), dim3(kThreads), 0, stream>>>(a, sp);
     return hipGetLastError();
 }
 

@@ -155,8 +155,8 @@ def test_attn_empty_problem_launches_nothing(kwargs):
 
 
 def sample(**k):
-    return lib.w4_sample(k.get("logits", at(0)), k.get("stride", 1000), k.get("u", at(1)), k.get("t", at(2)), k.get("k", at(3)),
-                         k.get("p", at(4)), k.get("m", at(5)), k.get("tokens", at(6)), k.get("rows", 3), k.get("vocab", 1000),
+    return lib.w4_sample(k.get("logits", at(0)), k.get("stride", 40000), k.get("u", at(1)), k.get("t", at(2)), k.get("k", at(3)),
+                         k.get("p", at(4)), k.get("m", at(5)), k.get("tokens", at(6)), k.get("rows", 3), k.get("vocab", 40000),
                          k.get("ws", at(7)), k.get("wsb", 1 << 30), None)
 
 
