@@ -2,7 +2,8 @@
 
 Each ``.hip`` file is compiled to an object under ``_build/`` in parallel,
 then linked into ``gemm_w4_gemv_amd/libw4.so``, next to this file.  No GPU is
-needed: hipcc cross-compiles for gfx950.
+needed: hipcc cross-compiles for gfx950.  The binding's compiled checks
+(``csrc/marshal.cpp``, host code against torch) become ``_marshal.so`` beside it.
 
     python gemm_w4_gemv_amd/build.py            # build
     python gemm_w4_gemv_amd/build.py --asm      # also write device assembly (.s)
@@ -13,17 +14,20 @@ package first would load the library this builds.)
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import pathlib
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = pathlib.Path(__file__).resolve().parent
 ROOT = PKG.parent
 CSRC = PKG / "csrc"
 BUILD = ROOT / "_build"
 LIB = PKG / "libw4.so"
+MARSHAL = PKG / "_marshal.so"
 ARCH = "gfx950"
 
 
@@ -86,7 +90,28 @@ def build(verbose: bool = False, asm: bool = False, defines=(), lib: pathlib.Pat
         print(out, file=sys.stderr)
         raise RuntimeError("link failed")
     os.replace(tmp, lib)
+    if lib == LIB:
+        build_marshal()
     return lib
+
+
+def build_marshal() -> None:
+    """Compile the binding's tensor checks (csrc/marshal.cpp) against the installed torch.
+
+    The same checks are in step.py; without these a call only takes some 2 us longer."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        raise RuntimeError("torch not found")
+    torch = pathlib.Path(spec.origin).parent
+    tmp = MARSHAL.with_suffix(".so.tmp")
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-I{torch / 'include'}", f"-I{torch / 'include/torch/csrc/api/include'}",
+           f"-I{sysconfig.get_paths()['include']}", str(CSRC / "marshal.cpp"), "-o", str(tmp), f"-L{torch / 'lib'}",
+           "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    rc, out = _run(cmd)
+    if rc:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{out}")
+    os.replace(tmp, MARSHAL)
 
 
 if __name__ == "__main__":

@@ -133,6 +133,30 @@ def _heads(t, name, device, rows=None, heads=None, dim=None):
     return t.data_ptr(), step
 
 
+def _addresses(device, *spec):
+    """Addresses of tensors, each given as (tensor, name, dtype, length; None: any contiguous tensor)."""
+    return tuple(_ptr(t, name, dtype, device) if n is None else _vector(t, name, dtype, device, n)
+                 for t, name, dtype, n in zip(spec[0::4], spec[1::4], spec[2::4], spec[3::4]))
+
+
+def _optional_addresses(device, *spec):
+    """The same; None where a tensor is None."""
+    return tuple(None if t is None else _addresses(device, t, name, dtype, n)[0]
+                 for t, name, dtype, n in zip(spec[0::4], spec[1::4], spec[2::4], spec[3::4]))
+
+
+# The same checks compiled (csrc/marshal.cpp), for host time alone: where a
+# tensor fails one, they call these, which say what is wrong.
+_in_python = (_addresses, _optional_addresses, _heads)
+try:
+    from . import _marshal
+except ImportError:  # built for another torch, or not at all
+    pass
+else:
+    _marshal.begin(*_in_python)
+    _addresses, _optional_addresses, _heads = _marshal.addresses, _marshal.optional_addresses, _marshal.heads
+
+
 def _call(where, fn, args, stream, device):
     """fn(*args, stream) on GPU ``device``."""
     if device != _current_device():
@@ -204,13 +228,11 @@ def w4_kv4_plan(cached, new_tokens, block_table, free_blocks, free_count, block_
         raise ValueError("block_table must be [B, max_blocks]")
     B, width = block_table.shape
     rows, pages, i, v = positions.numel(), free_blocks.numel(), _device_of(block_table, "block_table", _int32), _int32
-    args = (_vector(cached, "cached", v, i, B), _vector(new_tokens, "new_tokens", v, i, B),
-            _ptr(block_table, "block_table", v, i), _vector(free_blocks, "free_blocks", v, i, pages),
-            _vector(free_count, "free_count", v, i, 1), B, width, pages, block_size, rows,
-            _vector(q_start, "q_start", v, i, B + 1), _vector(kv_lens, "kv_lens", v, i, B),
-            _vector(positions, "positions", v, i, rows), _vector(slots, "slots", v, i, rows),
-            _vector(counts, "counts", v, i, 2))
-    _call("w4_kv4_plan", lib.w4_kv4_plan, args, stream, i)
+    p = _addresses(i, cached, "cached", v, B, new_tokens, "new_tokens", v, B, block_table, "block_table", v, None,
+                   free_blocks, "free_blocks", v, pages, free_count, "free_count", v, 1, q_start, "q_start", v, B + 1,
+                   kv_lens, "kv_lens", v, B, positions, "positions", v, rows, slots, "slots", v, rows,
+                   counts, "counts", v, 2)
+    _call("w4_kv4_plan", lib.w4_kv4_plan, (*p[:5], B, width, pages, block_size, rows, *p[5:]), stream, i)
 
 
 def w4_qk_norm_rope(q, k, positions=None, cos_sin=None, q_out=None, k_out=None, q_weight=None, k_weight=None,
@@ -227,7 +249,7 @@ def w4_qk_norm_rope(q, k, positions=None, cos_sin=None, q_out=None, k_out=None, 
     T, kv_heads, dim = k.shape
     qp = qs = vp = vs = qop = qos = kop = kos = 0
     q_heads = reach = rot = 0
-    qw = kw = cs = pos = sp = ref = None
+    sp = ref = None
     if q is not None:
         qp, qs = _heads(q, "q", i, T, None, dim)
         q_heads = q.shape[1]
@@ -236,22 +258,17 @@ def w4_qk_norm_rope(q, k, positions=None, cos_sin=None, q_out=None, k_out=None, 
         qop, qos = _heads(q_out, "q_out", i, T, q_heads, dim)
     if k_out is not None:
         kop, kos = _heads(k_out, "k_out", i, T, kv_heads, dim)
-    if q_weight is not None:
-        qw = _vector(q_weight, "q_weight", _bf16, i, dim)
-    if k_weight is not None:
-        kw = _vector(k_weight, "k_weight", _bf16, i, dim)
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [max_pos, rot_dim]")
         reach, rot = cos_sin.shape
-        cs = _ptr(cos_sin, "cos_sin", _f32, i)
-    if positions is not None:
-        pos = _vector(positions, "positions", _int32, i, T)
+    qw, kw, cs, pos = _optional_addresses(i, q_weight, "q_weight", _bf16, dim, k_weight, "k_weight", _bf16, dim,
+                                          cos_sin, "cos_sin", _f32, None, positions, "positions", _int32, T)
     if cache is not None:
         if v is None or slots is None:
             raise ValueError("v and slots must be given with a cache")
         vp, vs = _heads(v, "v", i, T, kv_heads, dim)
-        sp = _vector(slots, "slots", _int32, i, T)
+        sp, = _addresses(i, slots, "slots", _int32, T)
         ref = _cache_ref(cache, i)
     a = _QkArgs(qp, kp, vp, qs, ks, vs, qw, kw, cs, pos, sp, qop, kop, qos, kos, T, q_heads, kv_heads, dim, rot, reach,
                 1 if interleaved else 0, eps, weight_add)
@@ -263,12 +280,12 @@ def w4_kv4_read(cache, slots, k_out=None, v_out=None, stream=None) -> None:
     if not isinstance(cache, Kv4Cache):
         raise TypeError("cache must be a Kv4Cache")
     i, n = cache.device_index, slots.numel()
-    outs = []
+    shape = (n, cache.kv_heads, cache.head_dim)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None and tuple(t.shape) != (n, cache.kv_heads, cache.head_dim):
-            raise ValueError(f"{name} must be {(n, cache.kv_heads, cache.head_dim)}; got {tuple(t.shape)}")
-        outs.append(None if t is None else _ptr(t, name, _bf16, i))
-    _call("w4_kv4_read", lib.w4_kv4_read, (cache.ref, _vector(slots, "slots", _int32, i, n), n, *outs), stream, i)
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {shape}; got {tuple(t.shape)}")
+    sp, kp, vp = _optional_addresses(i, slots, "slots", _int32, n, k_out, "k_out", _bf16, None, v_out, "v_out", _bf16, None)
+    _call("w4_kv4_read", lib.w4_kv4_read, (cache.ref, sp, n, kp, vp), stream, i)
 
 
 def w4_kv4_attn_workspace_bytes(cache, T: int, B: int, q_heads: int, max_q: int, max_kv: int, window: int = 0,
@@ -298,9 +315,9 @@ def w4_kv4_attn(q, cache, block_table, kv_lens, out, q_start=None, max_q: int = 
     B, width = block_table.shape
     if max_kv is None:
         max_kv = width * cache.block_size
-    a = _AttnArgs(qp, op, qs, os, _ptr(block_table, "block_table", _int32, i),
-                  _vector(kv_lens, "kv_lens", _int32, i, B),
-                  None if q_start is None else _vector(q_start, "q_start", _int32, i, B + 1), T, B, q_heads, width, min(max_q, _INT_MAX),
+    tp, lp = _addresses(i, block_table, "block_table", _int32, None, kv_lens, "kv_lens", _int32, B)
+    sp, = _optional_addresses(i, q_start, "q_start", _int32, B + 1)
+    a = _AttnArgs(qp, op, qs, os, tp, lp, sp, T, B, q_heads, width, min(max_q, _INT_MAX),
                   min(max_kv, _INT_MAX), min(window, _INT_MAX), min(sinks, _INT_MAX),
                   1.0 / math.sqrt(d) if scale is None else scale)
     pw, nbytes = None, 0
@@ -330,11 +347,9 @@ def w4_sample(logits, uniform, tokens, temperature=None, top_k=None, top_p=None,
     pw, nbytes = None, 0
     if workspace is not None:
         pw, nbytes = _ptr(workspace, "workspace", workspace.dtype, i), workspace.numel() * workspace.element_size()
-    args = (logits.data_ptr(), stride, _vector(uniform, "uniform", _f64, i, rows),
-            None if temperature is None else _vector(temperature, "temperature", _f32, i, rows),
-            None if top_k is None else _vector(top_k, "top_k", _int32, i, rows),
-            None if top_p is None else _vector(top_p, "top_p", _f32, i, rows),
-            None if min_p is None else _vector(min_p, "min_p", _f32, i, rows),
-            _vector(tokens, "tokens", _int32, i, rows), rows, vocab, pw, nbytes)
+    up, out = _addresses(i, uniform, "uniform", _f64, rows, tokens, "tokens", _int32, rows)
+    settings = _optional_addresses(i, temperature, "temperature", _f32, rows, top_k, "top_k", _int32, rows,
+                                   top_p, "top_p", _f32, rows, min_p, "min_p", _f32, rows)
+    args = (logits.data_ptr(), stride, up, *settings, out, rows, vocab, pw, nbytes)
     _call("w4_sample", lib.w4_sample, args, stream, i)
     return tokens
