@@ -285,6 +285,9 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
 
     int top = kBins;
     bool near = true;  // the counts are in LDS, in 16 bits
+    bool held = false;
+    uint32_t x[4][kRun / kWave] = {};  // entries of four runs; 0: none, adds nothing
+    int chunk_of_run[4] = {};
     if constexpr (kWhole) {
         count_into(bins, a.logits + (int64_t)row * a.stride, 0, a.vocab);
     } else {
@@ -308,6 +311,7 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
             const int joined = min((int)info.entries, keep);
             const int upto = run_base + wave_scan((joined + kRun - 1) / kRun);
             if (wave == 0 && c < sp.chunks) {
+                at_chunk[c] = 0;
                 entries[c] = (int)info.entries;
                 runs[c + 1] = upto;
             }
@@ -330,15 +334,19 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
             __threadfence();
         }
         __syncthreads();
-        // A wave takes every 16th run, four of them in flight.
+        // A wave takes every 16th run, four of them in flight.  Where that is all
+        // of them, they are kept for the search at the end.
+        held = run_base <= 4 * kWaves;
 #pragma unroll 1
         for (int r0 = wave, c = 0; r0 < run_base; r0 += 4 * kWaves) {
-            uint32_t x[4][kRun / kWave] = {};  // 0: none, adds nothing
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int r = r0 + k * kWaves;
+#pragma unroll
+                for (int u = 0; u < kRun / kWave; ++u) x[k][u] = 0;
                 if (r >= run_base) continue;
                 while (r >= runs[c + 1]) ++c;
+                chunk_of_run[k] = c;
                 const int i = (r - runs[c]) * kRun + lane, n = min(entries[c], keep);
                 const uint32_t* list = lists + (size_t)c * sp.chunk;
 #pragma unroll
@@ -451,16 +459,23 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
     // Five looks into the order, one after the other: what the first ``keep``
     // weigh, where top-p of that is reached, what those weigh that are then
     // kept, where the draw falls, and the value of that rank.  One wave does
-    // them, with one body for all.
+    // them, with one body for all.  The third and the last are answered as a
+    // rule by the one before, in the place that it found.
     if (wave == 0) {
         const bool cut = p < 1.0f && keep > 1;
-        double goal = 0;
-        int rank = 0;
+        double goal = 0, kept_mass = 0;
+        int rank = 0, kept = -1;  // what the first ``kept`` weigh is known
+        // a draw stays below the whole weight by more than the sums' rounding
+        const double part = fmin(fmax(uniform, 0.0), 1.0 - 0x1p-40);
 #pragma unroll 1
         for (int look = cut ? 0 : 2; look < 5; ++look) {
             if (look == 2) {
                 if (floor_p > 0.0f) keep = min(keep, max(shared_by_all(strong), 1));
                 rank = keep - 1;
+                if (keep == kept) {
+                    goal = part * kept_mass;
+                    continue;
+                }
             }
             // looks 0, 2: the token of rank keep - 1; 1: at least goal; 3: past goal; 4: the token of rank
             const bool by_rank = look % 2 == 0;
@@ -491,8 +506,7 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
                     if (lane == 0) drawn[0] = e * kWave + at, drawn[1] = among;
                 } else {
                     const double all = lane_of(weighs, at);
-                    // a draw stays below the whole weight by more than the sums' rounding
-                    goal = look == 0 ? (double)p * all : fmin(fmax(uniform, 0.0), 1.0 - 0x1p-40) * all;
+                    goal = (look == 0 ? (double)p : part) * all;
                 }
             } else {
                 // tokens of this value before the goal: with less than it before them (look 1), or not past it (3)
@@ -500,10 +514,19 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
                 const int most = look == 1 ? n : n - 1;
                 const int more = whole > 0.0 ? (int)fmin(whole, (double)most) : 0;
                 const int at = l >= 0 ? lane_of(c + more, l) : look == 1 ? last : last - 1;
+                const int among = lane_of(more, max(l, 0));
                 if (look == 1) {
                     keep = min(keep, max(at, 1));
+                    if (l >= 0 && among > 0 && keep == at) {
+                        kept = keep;
+                        kept_mass = lane_of(m + w * (double)more, l);
+                    }
                 } else {
                     rank = min(rank, at);
+                    if (l >= 0 && rank == at) {
+                        if (lane == 0) drawn[0] = e * kWave + l, drawn[1] = among;
+                        break;
+                    }
                 }
             }
         }
@@ -514,9 +537,17 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
 
     int before = 0, chunk = 0;  // the chunk with the among-th, and those before it
     if constexpr (!kWhole) {
-        // How many of them each chunk holds: its list is sorted, so 64 places of
-        // it at a time narrow it down.
-        for (int c = wave; c < sp.chunks; c += kWaves) {
+        // How many of them each chunk holds: from the entries joined (with a
+        // top-k those that are not cannot have any), if they are still there; else
+        // its list is sorted, so 64 places of it at a time narrow it down.
+        if (held) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int u = 0; u < kRun / kWave; ++u)
+                    if (x[k][u] && x[k][u] >> 16 == want) at_chunk[chunk_of_run[k]] = (int)(x[k][u] & 0xFFFFu);
+        }
+        for (int c = wave; !held && c < sp.chunks; c += kWaves) {
             const uint32_t* list = lists + (size_t)c * sp.chunk;
             int lo = 0, n = shared_by_all(entries[c]);  // entries lo .. lo + n - 1 may be the one
             while (n > kWave) {
@@ -527,10 +558,9 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(SampleArgs a, Spa
                 lo += from;
                 n = min(step, n - from);
             }
-            const uint32_t x = lane < n ? list[lo + lane] : 0;
-            const uint64_t found = __ballot(lane < n && x >> 16 == want);
-            if (lane == 0) at_chunk[c] = 0;
-            if (found >> lane & 1) at_chunk[c] = (int)(x & 0xFFFFu);
+            const uint32_t y = lane < n ? list[lo + lane] : 0;
+            const uint64_t found = __ballot(lane < n && y >> 16 == want);
+            if (found >> lane & 1) at_chunk[c] = (int)(y & 0xFFFFu);
         }
         __syncthreads();
         for (int c0 = 0; c0 < sp.chunks; c0 += kWave) {
