@@ -1393,6 +1393,7 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_join_kernel(AttnArgs a) {
 struct Cut {
     bool many;      // kv4_attn_many_kernel
     int sets;       // kv4_attn_sets_kernel if over 1
+    bool two;       // 32 rows a wave of kv4_attn_kernel
     int row_tiles;  // of a request, each a workgroup's rows
     int splits;     // workgroups that share a row tile's tokens
     int waves;      // of a workgroup
@@ -1422,7 +1423,12 @@ Cut cut_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     // and 57, with pages of 16 79 and 60; without sets 38, 63 and 66; eight sets
     // take 37 us where four take 32).
     k.sets = rows > 8 ? 1 : rows > 4 || c.head_dim == 256 ? 2 : 4;
-    const int64_t tile = k.many ? many_rows : 16;
+    // Heads of 128: 32 rows a wave unpack half as often, where that still makes
+    // enough workgroups (2000 tokens after 3000, 16 query and 4 key/value heads, 1000
+    // workgroups of 32 rows: 139 us, 168 with 16; half as many 88 and 87; heads of
+    // 64, with half the work in a tile, 106 either way).
+    k.two = !k.many && c.head_dim == 128 && rows > 16 && (int64_t)a.B * c.kv_heads * ((rows + 31) / 32) >= 768;
+    const int64_t tile = k.many ? many_rows : k.two ? 32 : 16;
     k.row_tiles = (int)((rows + tile - 1) / tile);
     // As many workgroups as are on the chip at once, two a compute unit: with a
     // few more, the rest would run after them.  Twice that number where requests
@@ -1474,6 +1480,8 @@ hipError_t launch_d(const AttnArgs& k, const Cut& cut, int64_t groups, hipStream
         }
     } else if (cut.many) {
         kv4_attn_many_kernel<D, many_blocks(D), kWide><<<grid, block, 0, stream>>>(k);
+    } else if (cut.two) {
+        if constexpr (D == 128) kv4_attn_kernel<D, 2, kFewWaves, kWide><<<grid, block, 0, stream>>>(k);
     } else {
         kv4_attn_kernel<D, 1, kFewWaves, kWide><<<grid, block, 0, stream>>>(k);
     }

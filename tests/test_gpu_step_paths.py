@@ -81,6 +81,19 @@ def test_many_rows(lens, news, hq, hkv, dim, block, window, sinks):
     check_attn(got, *ref.attention(q, cache, table, lens, q_start, float(np.float32(dim ** -0.5)), window, sinks))
 
 
+@pytest.mark.parametrize("lens,news,hq,hkv,block,window,sinks", [
+    ([1], [1], 8, 8, 64, 0, 0), ([150], [150], 4, 2, 16, 0, 0), ([300, 70, 0, 9], [100, 70, 0, 1], 4, 2, 64, 0, 0),
+    ([513, 200], [130, 3], 3, 1, 16, 50, 33), ([5, 40], [9, 40], 4, 2, 128, 0, 0), ([33, 300], [33, 20], 16, 2, 32, 1, 1),
+])
+def test_rows_by_32(lens, news, hq, hkv, block, window, sinks):
+    """Heads of 128 with room for 768 workgroups of 32 rows, and for fewer than 448 of 128."""
+    cache, table, q_start, q = attn_case(77, lens, news, hq, hkv, 128, block)
+    max_q = 32 * (800 // (len(lens) * hkv) + 1) * hkv // hq
+    assert max_q >= max(news)
+    got = attn(to_device(cache), q, table, lens, q_start, max_q, window=window, sinks=sinks)
+    check_attn(got, *ref.attention(q, cache, table, lens, q_start, float(np.float32(128 ** -0.5)), window, sinks, TWO_PARTS))
+
+
 @pytest.mark.parametrize("rows,heads", [(57 * 64, 8), (60 * 64 - 5, 8), (64 * 64, 8)])
 def test_many_rows_that_fill_the_chip_once(rows, heads):
     """Up to 512 workgroups the row tiles go in pairs, an odd one too: every row is answered once."""
