@@ -19,8 +19,8 @@
 // one launch and without lists (one row of 32000: 15 us instead of 21, 300 rows
 // 30 instead of 44).
 // What bounds it: the count by the turns that LDS atomics take (64 rows of
-// 262144: 18 us, 1.8 TB/s of logits), the pick by the length of its chain of
-// dependent steps (17 us for one row, 22 for 64, a compute unit each).
+// 262144: 16.5 us, 2 TB/s of logits), the pick by the length of its chain of
+// dependent steps (14 us for one row, 21 for 64, a compute unit each).
 // Counts are whole numbers and masses are summed in a fixed order, so a
 // result depends on no order in which anything finishes.
 #include "kv4.hpp"
