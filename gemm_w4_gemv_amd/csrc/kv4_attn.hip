@@ -1449,14 +1449,15 @@ Cut cut_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     k.splits = (int)(want < 1 ? 1 : want > kMaxSplits ? kMaxSplits : want);
     // Up to 256 workgroups (512 with heads of 64, of half the registers) can have
     // eight waves, each with half the tiles: unsplit they save the join's launch.
-    // Worth it for short contexts (heads of 128, 8 requests of 1000 tokens: 10.2
-    // us, split 11.5; of 2000 14.3, split 13.1) and where splits would share a
+    // Worth it for short contexts, by what a tile takes (heads of 128, 8 requests
+    // of 1000 tokens: 10.2 us, split 11.5; of 2000 14.3, split 13.1; heads of 64,
+    // of 2500 tokens 12.5, split 10.5) and where splits would share a
     // compute unit anyway (32 of 1000 tokens 11.0, split 14.8; of 4000 24, split
     // 27; heads of 256, 32 of 1000 tokens 16.7, split 24.3; but 16, 128
     // workgroups, of 4000 tokens 44, split 36).
     k.waves = 4;
     if (k.sets > 1 && groups <= (c.head_dim == 64 ? 512 : 256) &&
-        (tiles * c.head_dim <= 5120 || (groups >= 160 && tiles <= 128))) {
+        (tiles * (c.head_dim + 64) <= 6800 || (groups >= 160 && tiles <= 128))) {
         k.waves = 8;
         k.splits = 1;
     }
