@@ -1454,10 +1454,13 @@ Cut cut_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     // of 2500 tokens 12.5, split 10.5) and where splits would share a
     // compute unit anyway (32 of 1000 tokens 11.0, split 14.8; of 4000 24, split
     // 27; heads of 256, 32 of 1000 tokens 16.7, split 24.3; but 16, 128
-    // workgroups, of 4000 tokens 44, split 36).
+    // workgroups, of 4000 tokens 44, split 36).  With more than 8 rows only in
+    // place of splits (200 tokens after 500, 16 query and 8 key/value heads of 128:
+    // 11.2 us, split 17.8; joining eight waves there costs 1 to 2 us, which
+    // 30 tokens after 200 do not win back: 8.5, four waves 7.7).
     k.waves = 4;
-    if (k.sets > 1 && groups <= (c.head_dim == 64 ? 512 : 256) &&
-        (tiles * (c.head_dim + 64) <= 6800 || (groups >= 160 && tiles <= 128))) {
+    if (!k.many && !k.two && (k.sets > 1 || k.splits > 1) && groups <= (c.head_dim == 64 ? 512 : 256) &&
+        (tiles * (c.head_dim + 64) <= (k.sets > 1 ? 6800 : 5120) || (groups >= 160 && tiles <= 128))) {
         k.waves = 8;
         k.splits = 1;
     }
@@ -1483,8 +1486,10 @@ hipError_t launch_d(const AttnArgs& k, const Cut& cut, int64_t groups, hipStream
         kv4_attn_many_kernel<D, many_blocks(D), kWide><<<grid, block, 0, stream>>>(k);
     } else if (cut.two) {
         if constexpr (D == 128) kv4_attn_kernel<D, 2, kFewWaves, kWide><<<grid, block, 0, stream>>>(k);
+    } else if (cut.waves == 8) {
+        kv4_attn_kernel<D, 1, 8, kWide><<<grid, block, 0, stream>>>(k);
     } else {
-        kv4_attn_kernel<D, 1, kFewWaves, kWide><<<grid, block, 0, stream>>>(k);
+        kv4_attn_kernel<D, 1, 4, kWide><<<grid, block, 0, stream>>>(k);
     }
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || k.splits == 1) return err;

@@ -214,6 +214,18 @@ def test_any_cut(hq, dim, block, B, max_kv):
     check_attn(got, *ref.attention(q, cache, table, lens, q_start, 0.1, 0, 0, TWO_PARTS))
 
 
+@pytest.mark.parametrize("hq,dim,block", [(16, 64, 16), (16, 64, 64), (16, 128, 16), (16, 256, 16), (16, 256, 64)])
+@pytest.mark.parametrize("lens,news,max_kv,window", [
+    ([300, 9, 70], [20, 9, 1], 600, 0), ([300, 9, 70], [20, 9, 1], 200, 0), ([300, 9, 70], [20, 9, 1], 10 ** 6, 0),
+    ([90] * 9, [10] * 9, 1500, 0), ([90, 40] * 4, [9, 1] * 4, 700, 50),
+])
+def test_any_cut_of_some_rows(hq, dim, block, lens, news, max_kv, window):
+    """16 rows a wave: four waves and eight, split and whole."""
+    cache, table, q_start, q = attn_case(78, lens, news, hq, 8, dim, block)
+    got = attn(to_device(cache), q, table, lens, q_start, max(news), max_kv=max_kv, scale=0.1, window=window)
+    check_attn(got, *ref.attention(q, cache, table, lens, q_start, 0.1, window, 0, TWO_PARTS))
+
+
 @pytest.mark.parametrize("kind,hq,hkv,dim,block", KINDS)
 def test_shared_pages_and_strided_rows(kind, hq, hkv, dim, block):
     """Requests that share their first pages; q and out as strided rows of one buffer, side by side."""
