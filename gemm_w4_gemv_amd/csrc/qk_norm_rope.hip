@@ -70,6 +70,13 @@ __device__ __forceinline__ T head_sum(T v) {
     return head_fold<kLanes>(v, [](T a, T b) { return a + b; });
 }
 
+// A value in FP32, where it is rounded: out of the compiler's sight, which joins
+// two conversions that follow each other (FP64 to FP32 to BF16) into one.
+__device__ __forceinline__ float in_f32(float v) {
+    asm("" : "+v"(v));
+    return v;
+}
+
 __device__ __forceinline__ uint32_t f16_bits(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
 
 // Quantises a lane's eight BF16 values with its group; returns the word of
@@ -142,7 +149,12 @@ __device__ __forceinline__ u32x4_t turned(const u32x4_t& w, const Turn<T>& turn,
         r[i] = ((T)x[i] * turn.own[i] + (T)(rotated ? z[i] : 0.0f) * turn.other[i]) * inv;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[i] = nan ? 0x7FC07FC0u : pack_bf16x2((float)r[2 * i], (float)r[2 * i + 1]);
+    for (int i = 0; i < 8; ++i) {
+        x[i] = (float)r[i];
+        if constexpr (sizeof(T) == 8) x[i] = in_f32(x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = nan ? 0x7FC07FC0u : pack_bf16x2(x[2 * i], x[2 * i + 1]);
     return out;
 }
 

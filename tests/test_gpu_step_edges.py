@@ -1,0 +1,93 @@
+"""GPU: values and sizes at which the decode step's operators could go wrong, against the FP64 oracle.
+
+Tolerances are those of ``test_gpu_step.py``: keys, codes and pairs equal bit for bit, queries within one rounding
+to BF16 and FP32 arithmetic, attention within ``noise`` of ``oracle.step.attention``.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import seeded_inputs as si
+from oracle import step as ref
+from test_gpu_step import DEV, bf16, host, ints, rope_table, same_bits, w4
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+    torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------- stored keys
+def check_cache(cache, want):
+    for name in ("k_codes", "v_codes", "k_meta", "v_meta"):
+        got, w = getattr(cache, name).cpu().numpy(), getattr(want, name)
+        assert np.array_equal(got.view(np.int16), w.view(np.int16)), name
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_keys_go_to_bf16_through_fp32(dim, inter):
+    """Rotations that end 2^-30 beside the middle between two BF16 values: FP32 drops that, and the tie goes to
+    the even one.  Rounded at once from FP64 half of them would go the other way."""
+    half, T, h = dim // 2, 8, 3
+    cs = np.zeros((T, dim), dtype=np.float32)
+    for t in range(T):
+        cs[t, :half] = 1 + (2 * t + 1) * 2.0 ** -8  # the middles above 1
+        cs[t, half:] = 2.0 ** -30 * (-1) ** np.arange(half)
+    bits = ref.round_to_bf16(np.ones((T, h, dim)))
+    y = ref.norm_rope(bits, None, cs, np.arange(T), dim, inter, 1e-6, 0.0)
+    k_bits = ref.round_to_bf16(y)
+    # what a single rounding gives: ties broken by the part that FP32 cannot hold
+    low = (y.astype(np.float32).view(np.uint32) & 0xFFFF0000).view(np.float32).astype(np.float64)
+    once = np.where(y - low > 2.0 ** -8, low + 2.0 ** -7, low)
+    assert bool(np.any(once != oracle.bf16_to_f64(k_bits)))
+    k, v = host.bf16_tensor(bits), host.bf16_tensor(si.bf16_normal(80, (1, dim), (T, h, dim)))
+    want = ref.Cache(1, 16, h, dim)
+    cache = w4.Kv4Cache(*(torch.from_numpy(a.copy()).to(DEV) for a in (want.k_codes, want.k_meta, want.v_codes, want.v_meta)))
+    k_out = torch.zeros_like(k)
+    w4.w4_qk_norm_rope(None, k, ints(np.arange(T)), torch.from_numpy(cs).to(DEV), k_out=k_out, v=v, cache=cache,
+                       slots=ints(np.arange(T)), interleaved=inter)
+    torch.cuda.synchronize()
+    assert same_bits(host.bits_of(k_out), k_bits)
+    for t in range(T):
+        want.put(t, k_bits[t], host.bits_of(v[t]))
+    check_cache(cache, want)
+
+
+def test_prompt_store_bit_for_bit():
+    """A prompt's 4099 tokens, 8 heads of 256, pages in any order: every key, code and pair is the oracle's."""
+    T, h, dim, block = 4099, 8, 256, 64
+    x, w = si.bf16_normal(81, (1,), (2, T, h, dim)), si.bf16_normal(81, (2,), (dim,))
+    cs, pos = rope_table(dim, 5000), np.arange(T) + 17
+    y = oracle.bf16_to_f64(x[0])
+    y = y / np.sqrt(np.mean(y * y, axis=-1, keepdims=True) + float(np.float32(1e-6))) * oracle.bf16_to_f64(w)
+    c, s = (cs[pos, at:at + dim // 2].astype(np.float64)[:, None] for at in (0, dim // 2))
+    a, b = y[..., :dim // 2], y[..., dim // 2:]
+    k_bits = ref.round_to_bf16(np.concatenate((a * c - b * s, b * c + a * s), axis=-1))
+    pages = si.rng(81, 3).permutation(-(-T // block) + 3)
+    place = np.arange(T)
+    slots = pages[place // block] * block + place % block
+    want = ref.Cache(len(pages), block, h, dim)
+    p, o = pages[place // block], place % block
+    q, want.k_meta[p, :, :, o] = ref.quantise(k_bits)
+    want.k_codes[p, :, o] = ref.pack(q)
+    q, want.v_meta[p, :, :, o] = ref.quantise(x[1])
+    want.v_codes[p, :, o // 4, :, o % 4] = ref.pack(q)
+    cache = w4.Kv4Cache(*(torch.from_numpy(np.zeros_like(t)).to(DEV) for t in (want.k_codes, want.k_meta, want.v_codes, want.v_meta)))
+    k, v = host.bf16_tensor(x[0]), host.bf16_tensor(x[1])
+    k_out = torch.zeros_like(k)
+    w4.w4_qk_norm_rope(None, k, ints(pos), torch.from_numpy(cs).to(DEV), k_out=k_out, k_weight=host.bf16_tensor(w), v=v,
+                       cache=cache, slots=ints(slots))
+    torch.cuda.synchronize()
+    assert same_bits(host.bits_of(k_out), k_bits)
+    check_cache(cache, want)
+
+
