@@ -71,7 +71,8 @@ __device__ __forceinline__ T head_sum(T v) {
 }
 
 // A value in FP32, where it is rounded: out of the compiler's sight, which joins
-// two conversions that follow each other (FP64 to FP32 to BF16) into one.
+// two conversions that follow each other (FP64 to FP32 to BF16), and a product
+// with its conversion to FP16, into one rounding.
 __device__ __forceinline__ float in_f32(float v) {
     asm("" : "+v"(v));
     return v;
@@ -98,7 +99,7 @@ __device__ __forceinline__ uint32_t quantise8(const u32x4_t& w, uint32_t& meta) 
     const bool bad = !(lo > -INFINITY && hi < INFINITY);
     lo = fminf(fmaxf(lo, -65504.0f), 65504.0f);
     hi = fminf(fmaxf(hi, -65504.0f), 65504.0f);
-    const float s = (float)(_Float16)((hi - lo) * (1.0f / 15.0f)), m = (float)(_Float16)lo;
+    const float s = (float)(_Float16)in_f32((hi - lo) * (1.0f / 15.0f)), m = (float)(_Float16)lo;
     const float inv = s > 0.0f ? 1.0f / s : 0.0f;
     uint32_t word = 0;
 #pragma unroll

@@ -91,3 +91,35 @@ def test_prompt_store_bit_for_bit():
     check_cache(cache, want)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_scales_go_to_fp16_through_fp32(dim):
+    """Groups whose span over 15 is, in FP32, the middle between two FP16 values: the tie goes to the even one.
+    The product of the span and fp32(1/15) lies above it, so rounded at once it would go up."""
+    pairs = []
+    for n in range(2049, 2345, 4):  # of twelve bits, the even neighbour below
+        for high in np.arange(128, 256) * 128.0:
+            low = high - 15 * n
+            if low <= 0 and oracle.bf16_to_f64(ref.round_to_bf16(low)) == low:
+                pairs.append((low, high))
+    assert len(pairs) >= 8
+    T, groups, size = len(pairs), max(1, dim // 128), min(dim, 128)
+    x = np.zeros((T, 1, groups, size))
+    g = si.rng(82, dim)
+    for t, (low, high) in enumerate(pairs):
+        x[t] = g.uniform(low, high, (1, groups, size))
+        x[t, ..., 3], x[t, ..., size - 2] = low, high
+    bits = ref.round_to_bf16(x.reshape(T, 1, dim))
+    q, meta = ref.quantise(bits)
+    span = np.array([h - lo for lo, h in pairs])
+    once = (span * float(np.float32(1 / 15))).astype(np.float16)
+    assert np.all(once != meta[:, 0, 0, 0])
+    want = ref.Cache(-(-T // 16), 16, 1, dim)
+    cache = w4.Kv4Cache(*(torch.from_numpy(a.copy()).to(DEV) for a in (want.k_codes, want.k_meta, want.v_codes, want.v_meta)))
+    k = host.bf16_tensor(bits)
+    w4.w4_qk_norm_rope(None, k, v=k, cache=cache, slots=ints(np.arange(T)))
+    torch.cuda.synchronize()
+    for t in range(T):
+        want.put(t, bits[t], bits[t])
+    check_cache(cache, want)
+
+
