@@ -112,6 +112,18 @@ __device__ __forceinline__ uint32_t quantise8(const u32x4_t& w, uint32_t& meta) 
     return bad ? 0u : word;
 }
 
+__device__ __forceinline__ double half_of(uint32_t pair, int k) { return bf16_to_f32(k ? pair >> 16 : pair & 0xFFFFu); }
+
+template <int kLanes, typename T>
+__device__ __forceinline__ T mean_square(const u32x4_t& w) {
+    float x[8];
+    unpack8(w, x);
+    T sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += (T)x[i] * (T)x[i];
+    return head_sum<kLanes>(sum) * (T)(1.0 / (8 * kLanes));
+}
+
 // What a token's position and the weights make of a lane's eight values:
 // y = inv * (x * own + partner * other).
 template <typename T>
@@ -120,10 +132,12 @@ struct Turn {
 };
 
 // The eight values of a lane after norm and rotation.  ``partner`` is the lane
-// that holds the other values of its pairs, unless they are neighbours.
+// that holds the other values of its pairs, unless they are neighbours.  far: in
+// FP32, whether the head's mean square lies where its squares or the factor
+// 1 / sqrt(mean square) come near the ends of FP32's range (a NaN does).
 template <int kLanes, bool kNeighbours, typename T>
 __device__ __forceinline__ u32x4_t turned(const u32x4_t& w, const Turn<T>& turn, bool norm, float eps, bool rotated,
-                                          int partner, bool nan) {
+                                          int partner, bool nan, bool& far) {
     float x[8], z[8];
     unpack8(w, x);
     if constexpr (kNeighbours) {
@@ -137,10 +151,9 @@ __device__ __forceinline__ u32x4_t turned(const u32x4_t& w, const Turn<T>& turn,
     }
     T inv = 1;
     if (norm) {
-        T sum = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += (T)x[i] * (T)x[i];
-        inv = (T)1 / sqrt(head_sum<kLanes>(sum) * (T)(1.0 / (8 * kLanes)) + (T)eps);
+        const T square = mean_square<kLanes, T>(w) + (T)eps;
+        far = !(square > (T)0x1p-40 && square < (T)0x1p40);
+        inv = (T)1 / sqrt(square);
     }
     u32x4_t out;
     T r[8];
@@ -234,49 +247,105 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(w4_qk_args a, Kv
         if (li % (kLanes / kGroups) == 0) metas[(ph * kGroups + li / (kLanes / kGroups)) * bs + off] = meta;
     };
     // Calls f(values, head) for this wave's runs of one input, from its run on.
-    const auto each = [&](const void* in, int64_t stride, int heads, int from, auto f) {
+    // f may ask for a call of g instead, with the same, by giving true; it has
+    // then written nothing, so the values are read again (an output may be its
+    // input), in a loop of its own: inside the other it would hold a third of the registers.
+    const auto each = [&](const void* in, int64_t stride, int heads, int from, auto f, auto g) {
         constexpr int kAhead = 4;
         const uint16_t* src = static_cast<const uint16_t*>(in) + t * stride + e;
         const int runs = (heads + kHeads - 1) / kHeads;
+        const auto values = [&](int run) {
+            const int h = min(run * kHeads + hi, heads - 1);  // behind the last head: that one again
+            return *reinterpret_cast<const u32x4_t*>(src + (size_t)h * D);
+        };
         for (int r = from; r < runs; r += kAhead * parts) {
             u32x4_t w[kAhead];
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int h = min((r + u * parts) * kHeads + hi, heads - 1);  // behind the last head: that one again
-                if (r + u * parts < runs) w[u] = *reinterpret_cast<const u32x4_t*>(src + (size_t)h * D);
-            }
+            for (int u = 0; u < kAhead; ++u)
+                if (r + u * parts < runs) w[u] = values(r + u * parts);
+            uint32_t again = 0;
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
-                if (r + u * parts < runs) f(w[u], (r + u * parts) * kHeads + hi);
+                if (r + u * parts < runs) again |= (uint32_t)f(w[u], (r + u * parts) * kHeads + hi) << u;
+            if (__any(again != 0)) {
+#pragma unroll 1
+                for (int u = 0; u < kAhead; ++u) {
+                    const bool mine = again >> u & 1;
+                    if (!__any(mine)) continue;
+                    const u32x4_t x = values(r + u * parts);
+                    g(x, (r + u * parts) * kHeads + hi, mine);
+                }
+            }
         }
         // where the next input's runs go on
         return from < runs ? (parts - (runs - from) % parts) % parts : from - runs;
     };
+    const auto never = [](const u32x4_t&, int, bool) {};
 
     int at = part;
     if (a.q_heads > 0) {
         Turn<float> turn;
         turn_of(a.q_weight, turn);
+        // Weights whose products with a query could pass FP32's range: the token's, so the same for all its heads.
+        float most = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) most = fmaxf(most, fmaxf(fabsf(turn.own[i]), fabsf(turn.other[i])));
+        const bool wild = a.q_weight && __any(!(most < 0x1p60f));
         uint16_t* out = static_cast<uint16_t*>(a.q_out) + t * a.q_out_stride + e;
+        const auto put = [&](const u32x4_t& y, int h) { *reinterpret_cast<u32x4_t*>(out + (size_t)h * D) = y; };
         at = each(a.q, a.q_stride, a.q_heads, at, [&](const u32x4_t& w, int h) {
-            const u32x4_t y = turned<kLanes, kNeighbours>(w, turn, a.q_weight != nullptr, a.eps, rotated, partner, nan);
-            if (h < a.q_heads) *reinterpret_cast<u32x4_t*>(out + (size_t)h * D) = y;
+            bool far = false;
+            const u32x4_t y = turned<kLanes, kNeighbours>(w, turn, a.q_weight != nullptr, a.eps, rotated, partner, nan, far);
+            if (h < a.q_heads && !(far | wild)) put(y, h);
+            return far | wild;
+        }, [&](const u32x4_t& w, int h, bool mine) {
+            // Such a head in FP64, whose range holds all of it; the others have
+            // what they have, whatever stands beside them.  Two values at a time
+            // and with their factors made here: in advance they would hold registers.
+            const u32x4_t* p = reinterpret_cast<const u32x4_t*>(a.q_weight);
+            const u32x4_t g = p[li], gp = p[partner % kLanes];
+            u32x4_t y, z = w;
+            if constexpr (!kNeighbours) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] = __shfl(w[i], partner);
+            }
+            const double inv = 1.0 / sqrt(mean_square<kLanes, double>(w) + (double)a.eps), add = a.weight_add;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                asm volatile("" : "+v"(c[2 * i]), "+v"(c[2 * i + 1]), "+v"(s[2 * i]), "+v"(s[2 * i + 1]));
+                float r[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int pair = kNeighbours ? 1 - k : k;
+                    const double own = (half_of(g[i], k) + add) * c[2 * i + k];
+                    const double other = (half_of(gp[i], pair) + add) * s[2 * i + k];
+                    r[k] = (float)((half_of(w[i], k) * own + (rotated ? half_of(z[i], pair) : 0.0) * other) * inv);
+                }
+                y[i] = nan ? 0x7FC07FC0u : pack_bf16x2(in_f32(r[0]), in_f32(r[1]));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (h < a.q_heads && mine) put(y, h);
         });
     }
     if (at < (a.kv_heads + kHeads - 1) / kHeads) {
         Turn<double> turn;
         turn_of(a.k_weight, turn);
         at = each(a.k, a.k_stride, a.kv_heads, at, [&](const u32x4_t& w, int h) {
-            const u32x4_t y = turned<kLanes, kNeighbours>(w, turn, a.k_weight != nullptr, a.eps, rotated, partner, nan);
+            bool any;
+            const u32x4_t y = turned<kLanes, kNeighbours>(w, turn, a.k_weight != nullptr, a.eps, rotated, partner, nan, any);
             if (h < a.kv_heads && a.k_out)
                 *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.k_out) + t * a.k_out_stride + e + (size_t)h * D) = y;
             if constexpr (kCached) store(y, h, cache.kc, cache.km, false);
-        });
+            return false;
+        }, never);
     } else {
         at -= (a.kv_heads + kHeads - 1) / kHeads;
     }
     if constexpr (kCached)
-        each(a.v, a.v_stride, a.kv_heads, at, [&](const u32x4_t& w, int h) { store(w, h, cache.vc, cache.vm, true); });
+        each(a.v, a.v_stride, a.kv_heads, at, [&](const u32x4_t& w, int h) {
+            store(w, h, cache.vc, cache.vm, true);
+            return false;
+        }, never);
 }
 
 template <int D>

@@ -97,9 +97,10 @@ W4_API w4_status w4_kv4_plan(const int32_t* cached, const int32_t* new_tokens, i
  *   (y_i, y_j) -> (y_i cos - y_j sin, y_j cos + y_i sin) for the pairs
  *   (i, j) = (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved,
  *   i < rot_dim / 2; values from rot_dim on are not rotated
- * Norm and rotation are in FP32 for queries and FP64 for keys (whose result
- * decides a code); each result is rounded to BF16, a key's to FP32 before
- * that.  The cache takes the rounded key and the value as given.
+ * Norm and rotation are in FP32 for queries (in FP64 for a head whose mean
+ * square lies outside 2^-40 .. 2^40, and for weights from 2^60 on) and FP64 for
+ * keys (whose result decides a code); each result is rounded to BF16, one from
+ * FP64 to FP32 before that.  The cache takes the rounded key and the value as given.
  *   q, k, v      device bf16 [T][heads][head_dim], 16-byte aligned; rows
  *                *_stride elements apart (a multiple of 8, at least
  *                heads * head_dim), so the three may lie side by side.

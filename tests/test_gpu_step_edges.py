@@ -12,7 +12,7 @@ import torch
 import oracle
 import seeded_inputs as si
 from oracle import step as ref
-from test_gpu_step import DEV, bf16, host, ints, rope_table, same_bits, w4
+from test_gpu_step import DEV, bf16, check_queries, host, ints, rope_table, same_bits, w4
 
 pytestmark = pytest.mark.gpu
 
@@ -121,5 +121,53 @@ def test_scales_go_to_fp16_through_fp32(dim):
     for t in range(T):
         want.put(t, bits[t], bits[t])
     check_cache(cache, want)
+
+
+# ----------------------------------------------------------------- queries
+FAR = [(1e20, 1e-6), (3e36, 1e-6), (1e-12, 0.0), (1e-25, 0.0), (1e-38, 0.0), (1e-30, 1e-6), (0.0, 1e-6), (1e3, 1e30), (1.0, 1e-6)]
+
+
+@pytest.mark.parametrize("inter,rot,weight", [(False, 1, 1.0), (True, 0.5, 1.0), (False, 0, 1e30), (True, 1, 1e-30), (False, 1, 1e38)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_queries_of_any_size(dim, inter, rot, weight):
+    """Queries whose squares leave FP32's range, above and below, beside ordinary ones of the same row; norm
+    weights at its ends.  A row's ordinary queries keep their bits whatever stands beside them."""
+    T, h, rot = 5, 7, int(rot * dim)
+    w = ref.round_to_bf16(oracle.bf16_to_f64(si.bf16_normal(83, (1, dim), (dim,))) * weight)
+    w[:4] = ref.round_to_bf16([0.5, 1.0, -2.0, 0.0])
+    base = oracle.bf16_to_f64(si.bf16_normal(83, (2, dim), (T, h, dim)))
+    cs, pos = rope_table(rot) if rot else None, np.arange(T) * 90
+    plain = None
+    for size, eps in [(1.0, 1e-6)] + FAR:
+        x = base.copy()
+        x[1, 2:4] *= size
+        x[2] *= size
+        x[4, ::2] *= -size
+        bits = ref.round_to_bf16(x)
+        with np.errstate(all="ignore"):
+            want = ref.norm_rope(bits, w, cs, pos, rot, inter, eps, 0.0)
+        q, k_out = torch.zeros(T, h, dim, dtype=bf16, device=DEV), torch.zeros(T, 1, dim, dtype=bf16, device=DEV)
+        w4.w4_qk_norm_rope(host.bf16_tensor(bits), host.bf16_tensor(bits[:, :1]), ints(pos) if rot else None,
+                           torch.from_numpy(cs).to(DEV) if rot else None, q_out=q, k_out=k_out, q_weight=host.bf16_tensor(w),
+                           k_weight=host.bf16_tensor(w), eps=eps, interleaved=inter)
+        torch.cuda.synchronize()
+        keys = oracle.bf16_to_f64(ref.round_to_bf16(want[:, :1]))  # as numbers: a zero weight's zeros have either sign
+        assert np.array_equal(host.bf16_values(k_out), keys, equal_nan=True)
+        got = host.bf16_values(q)
+        # results past BF16's range, and what is 0 / 0, are what the definition makes of them
+        top = np.abs(want) >= 3.38e38
+        tiny = np.abs(want) < 1e-37  # BF16's last bits there are steps of 2^-133
+        assert np.array_equal(np.isnan(got), np.isnan(want)), (size, eps)
+        assert np.all(np.abs(got[top]) >= 3.376e38)  # the nearest BF16 to 3.38e38
+        sound = ~(top | tiny | np.isnan(want))
+        check_queries(np.where(sound, got, 0.0), np.where(sound, want, 0.0), (size, eps))
+        assert np.all(np.abs(got - want)[tiny] <= 2.0 ** -8 * np.abs(want)[tiny] + 2.0 ** -133)
+        if size == 1.0 and eps == 1e-6:
+            plain = host.bits_of(q) if plain is None else plain
+            assert same_bits(host.bits_of(q), plain)
+        elif eps == 1e-6:
+            keep = np.ones((T, h), dtype=bool)
+            keep[1, 2:4] = keep[2] = keep[4, ::2] = False
+            assert same_bits(host.bits_of(q)[keep], plain[keep])
 
 
