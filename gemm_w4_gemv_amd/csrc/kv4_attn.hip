@@ -1295,8 +1295,10 @@ __global__ __launch_bounds__(256, 2) void kv4_attn_many_kernel(AttnArgs a) {
         fetch_codes(ahead);
         __builtin_amdgcn_sched_barrier(0);
 
-        // Rows of a wave that lie before the tile, or before whose window it ends, pass it over.
-        const bool sees = r0 < rows && t0 <= my_high && (a.window == 0 || t0 + kTile - 1 > my_low - a.window || t0 < a.sinks);
+        // Rows of a wave that lie before the tile, or before whose window it ends, pass
+        // it over.  (Positions below 0 see nothing; less a window they could pass 32 bits.)
+        const bool sees = r0 < rows && t0 <= my_high &&
+                          (a.window == 0 || t0 + kTile - 1 > max(my_low, 0) - a.window || t0 < a.sinks);
         if (sees) {
             const bool whole = t0 + kTile - 1 <= my_low && (a.window == 0 || t0 > my_high - a.window || t0 + kTile <= a.sinks) &&
                                page[0] >= 0 && page[1] >= 0 && r0 + kCols <= rows;

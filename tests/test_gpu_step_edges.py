@@ -12,7 +12,8 @@ import torch
 import oracle
 import seeded_inputs as si
 from oracle import step as ref
-from test_gpu_step import DEV, bf16, check_queries, host, ints, rope_table, same_bits, w4
+from test_gpu_step import DEV, attn_case, bf16, check_attn, check_queries, host, ints, rope_table, same_bits, to_device, w4
+from test_gpu_step_paths import attn
 
 pytestmark = pytest.mark.gpu
 
@@ -169,5 +170,21 @@ def test_queries_of_any_size(dim, inter, rot, weight):
             keep = np.ones((T, h), dtype=bool)
             keep[1, 2:4] = keep[2] = keep[4, ::2] = False
             assert same_bits(host.bits_of(q)[keep], plain[keep])
+
+
+# --------------------------------------------------------------- attention
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 3), (2 ** 31 - 20, 0), (2 ** 31 - 64, 2 ** 31 - 1)])
+@pytest.mark.parametrize("dim,B,rows,block", [(256, 56, 64, 64), (128, 56, 128, 16), (64, 128, 128, 32), (256, 3, 40, 16), (64, 2, 5, 16)])
+def test_window_of_everything_with_more_rows_than_tokens(dim, B, rows, block, window, sinks):
+    """Rows before the first token beside a window near 2^31: what the others see is not passed over."""
+    heads, tokens = 8, max(rows - 10, rows // 2)
+    lens, news = [tokens] * B, [rows] * B
+    cache, table, q_start, q = attn_case(84, lens, news, heads, heads, dim, block)
+    got = attn(to_device(cache), q, table, lens, q_start, rows, window=window, sinks=sinks, scale=0.1)
+    hidden = rows - tokens
+    for b in sorted({0, B // 2, B - 1}):
+        at = slice(b * rows, (b + 1) * rows)
+        assert np.all(got[at][:hidden] == 0)
+        check_attn(got[at], *ref.attention(q[at], cache, table[b:b + 1], [tokens], [0, rows], 0.1), f"request {b}")
 
 
