@@ -9,7 +9,7 @@
 //   outputs  O[d][r] = sum_t p s_t (q_td - 8) + sum_t p (m_t + 8 s_t)
 //
 // 128 + q is exact in BF16 and is one shift and one and-or per two codes.
-// (p s is rounded to BF16, in one part or two: see two_parts.)
+// (p s is rounded to BF16, in two parts: see two_parts.)
 // In the outputs the 136 = 128 + 8 comes off as 136 times the sum of the
 // rounded weights, which one more product per group (with ones) keeps, every
 // few tiles: left in until the end, the sums of a long context would be
@@ -65,9 +65,10 @@ __device__ __forceinline__ f32x4_t mfma(const u32x4_t& a, const u32x4_t& b, cons
 // up to 2^-8 of itself, which moves an output by about as much as its own
 // rounding to BF16 (error against 64 bits 2.3e-3 instead of 1.7e-3); the second
 // part costs one more product a block of values.  Memory bounds the decode
-// kernels, which take it (32 requests up to 8192 tokens: 77 us either way); for
-// long prompts, bound by instructions, it would cost a sixth (190 -> 216 us for
-// 2048 tokens after 2048, heads of 256), so kv4_attn_many_kernel does without.
+// kernels (32 requests up to 8192 tokens: 77 us either way); long prompts, bound by
+// instructions, pay a seventh (2048 tokens after 2048, heads of 256: 181 us with
+// one part, 206 with two; eight prompts of 1000, heads of 64: 94 and 107), so that a
+// request's answer does not depend on the kernel that its company picks.
 struct Pair {
     uint32_t high, low;
 };
@@ -272,8 +273,7 @@ __device__ __forceinline__ void pages_of(const AttnArgs& a, const Entries& x, in
 // What a wave holds of its 16 * kNB rows: queries, running softmax and outputs.
 // A lane's rows are those of its column (lane % 16) of each block of 16; of
 // the tokens and of the outputs it has the share of its lane / 16.
-// kParts: how many BF16 parts a weight of the second product has (see two_parts).
-template <int D, int kNB, int kParts>
+template <int D, int kNB>
 struct Rows {
     static constexpr int kG = Frag<D>::kG, kW = Frag<D>::kW;
     static constexpr int kJ = D == 64 ? 4 : 8;  // blocks of 16 d per group
@@ -285,7 +285,7 @@ struct Rows {
     f32x4_t o[kNB][kG][kJ], ones_sum[kNB][kG];  // of ones_sum only element 0 counts
     float extra[kNB][kG], m[kNB], l[kNB];
     float means[kNB][kG], scales[kNB][kG];  // sums of p m and p s since the last settling
-    u32x4_t pop[kParts][kNB][kG];  // p s of the tile and what its rounding left, the second product's operands
+    u32x4_t pop[2][kNB][kG];  // p s of the tile and what its rounding left, the second product's operands
 
     // Sends for the queries of rows r0 ..; past the last row that one again, unseen.
     __device__ __forceinline__ void fetch(const AttnArgs& a, const Request& req, int head, int r0, int rows, int lane) {
@@ -440,7 +440,7 @@ struct Rows {
                         for (int r = 0; r < 4; r += 2) {
                             const Pair w = two_parts(ps[h][r], ps[h][r + 1]);
                             pop[0][n][q][2 * h + r / 2] = w.high;
-                            if constexpr (kParts == 2) pop[1][n][q][2 * h + r / 2] = w.low;
+                            pop[1][n][q][2 * h + r / 2] = w.low;
                         }
                 }
             };
@@ -467,20 +467,18 @@ struct Rows {
 #pragma unroll
                 for (int n = 0; n < kNB; ++n) {
                     o[n][q][j] = mfma(vop, pop[0][n][q], o[n][q][j]);
-                    if (kParts == 2 && j > 0) o[n][q][j - 1] = mfma(last, pop[kParts - 1][n][q], o[n][q][j - 1]);
+                    if (j > 0) o[n][q][j - 1] = mfma(last, pop[1][n][q], o[n][q][j - 1]);
                 }
                 last = vop;
             }
 #pragma unroll
             for (int n = 0; n < kNB; ++n) {
                 ones_sum[n][q] = mfma(ones, pop[0][n][q], ones_sum[n][q]);
-                if constexpr (kParts == 2) {
-                    o[n][q][kJ - 1] = mfma(last, pop[1][n][q], o[n][q][kJ - 1]);
-                    ones_sum[n][q] = mfma(ones, pop[1][n][q], ones_sum[n][q]);
-                }
+                o[n][q][kJ - 1] = mfma(last, pop[1][n][q], o[n][q][kJ - 1]);
+                ones_sum[n][q] = mfma(ones, pop[1][n][q], ones_sum[n][q]);
             }
         }
-        if constexpr (kAhead > 0) in_order<kG * kJ, kAhead, kParts * kNB>();
+        if constexpr (kAhead > 0) in_order<kG * kJ, kAhead, 2 * kNB>();
     }
 
     // Asks the scheduler for kAhead reads from LDS, then a read after each
@@ -623,7 +621,7 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a) {
 // Few rows: the waves take a row tile's token tiles in turn.
 template <int D, int kNB, int kWaves, bool kWide>
 __global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
-    typedef Rows<D, kNB, 2> R;
+    typedef Rows<D, kNB> R;
     constexpr int kG = R::kG, kJ = R::kJ, kCols = 16 * kNB;
     __shared__ float so[kWaves / 2][kCols][D + 4];
     __shared__ float sm[kWaves][kCols], sl[kWaves][kCols];
@@ -1140,7 +1138,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void kv4_attn_sets_kernel(AttnAr
         for (int w = 0; w < kWaves; ++w) end[i] = fmaf(by[w], so[w][wave * kEnd + i][lane], end[i]);
     }
     const int at = set * kMine + wave * kEnd;  // (q, r, j) as one number
-    const int d = Rows<D, 1, 2>::place(at / kJ / 4, at / kJ % 4, g) + at % kJ;
+    const int d = Rows<D, 1>::place(at / kJ / 4, at / kJ % 4, g) + at % kJ;
     const int t = req.first + row / a.g, h = head * a.g + row % a.g;
     if (a.splits == 1) {
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -1176,13 +1174,16 @@ __device__ __forceinline__ void lds_barrier() {
 // a register's 64 lanes together (16 bytes a lane, no conflicts either way).
 // Two buffers: while a tile is worked on, the next one is unpacked and the
 // one after is on its way from memory.
+// Heads of 64 fit three waves a SIMD, with two operands of the values read ahead
+// in place of four where a tile is one page (eight prompts of 1000 tokens, 32 query
+// and 8 key/value heads: 107 us, 125 with 173 registers and two waves).
 template <int D, int kNB, bool kWide>
-__global__ __launch_bounds__(256, 2) void kv4_attn_many_kernel(AttnArgs a) {
-    typedef Rows<D, kNB, 1> R;
+__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv4_attn_many_kernel(AttnArgs a) {
+    typedef Rows<D, kNB> R;
     constexpr int kWaves = 4, kG = R::kG, kW = R::kW, kJ = R::kJ, kCols = 16 * kNB;
     constexpr int kKeys = 2 * kG * kW, kValues = kG * kJ;  // operands of a tile
     constexpr int kMyKeys = kKeys / kWaves, kMyValues = kValues / kWaves;
-    constexpr int kAheadKeys = kKeys < 6 ? kKeys : 6, kAheadValues = kValues < 8 ? kValues : 8;
+    constexpr int kAheadKeys = kKeys < 6 ? kKeys : 6, kAheadValues = D == 64 ? (kWide ? 2 : 4) : 8;
     __shared__ u32x4_t ops[2][kKeys + kValues][kWave];
 
     const int lane = threadIdx.x & (kWave - 1), wave = (int)sgpr(threadIdx.x / kWave);
@@ -1411,14 +1412,25 @@ Cut cut_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     // of its rows' tokens a tile at a time, where kv4_attn_kernel's four waves
     // share them: it pays where nearly every compute unit has two workgroups (heads
     // of 64, whose tiles are the least work, four), for then the shortest can go with
-    // the longest.  us of both kernels, shared tiles first: heads of 256, 256
-    // workgroups 89 and 69 (1024 tokens after 1024), 512 189 and 207 (2048 after
-    // 2048), 1024 137 and 187 (4096 in two prompts); heads of 128, 352 workgroups 111
-    // and 98, 456 84 and 106, 512 318 and 382; heads of 64, 512 57 and 40 (four
-    // prompts of 1000), 1024 119 and 123, 2048 203 and 250.
+    // the longest.  us of both kernels, shared tiles first, prompts with nothing
+    // before them unless said: heads of 256, 256 workgroups 104 and 78 (1024 tokens
+    // after 1024), 448 198 and 198 (1792 after 2048), 512 204 and 225 (2048 after
+    // 2048) and 22 and 42 (eight prompts of 250), 1024 155 and 185 (two of 2048); heads
+    // of 128, 384 196 and 152 (1536 after 2048), 464 53 and 55 (two of 912), 576 26
+    // and 47 (nine of 250), 1008 156 and 171 (two of 2000); heads of 64, 512 49 and
+    // 40 (1024 tokens), 1024 59 and 77 (four of 1000), 2048 106 and 142 (eight).
+    // One prompt of heads of 128, whose workgroups differ most: 456 96 and 78 (1824),
+    // 576 303 and 248 (2304 after 2048), 1024 302 and 295 (4096), 531 and 538 (4096
+    // after 2048).  A few workgroups past 512 run on their own when the first end,
+    // which counts where each has far to go: 576 180 and 164 (two of 1152 after 1000,
+    // heads of 256), 323 and 260 (2304 after 2048), 128 and 108 at 640 (16 of 144 after
+    // 1000, heads of 128), but 72 and 85 (two of 1152), and 768 155 and 176 (four of
+    // 768 after 1000).
     const int64_t many_rows = 64 * many_blocks(c.head_dim);
     const int64_t shared = (int64_t)a.B * c.kv_heads * ((rows + many_rows - 1) / many_rows);
-    k.many = rows >= many_rows && shared >= (c.head_dim == 64 ? 1024 : 448);
+    const bool few_left = shared > 512 && shared < 704 && (int64_t)a.max_kv >= (int64_t)a.max_q + 800;
+    k.many = rows >= many_rows && !few_left &&
+             shared >= (c.head_dim == 64 || (c.head_dim == 128 && a.B == 1) ? 1024 : 448);
     // Sets: four with up to 4 rows, but two with heads of 256, for the registers
     // of a group's codes (32 requests of 4096 tokens, 8 key/value heads: heads
     // of 128 32 us with four and 35 with two, heads of 256 with pages of 64 58

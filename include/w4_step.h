@@ -162,8 +162,7 @@ W4_API w4_status w4_kv4_read(const w4_kv4_cache* cache, const int32_t* slots, in
  * The tokens are already in the cache (their own included).  Query head h
  * reads key/value head h / (q_heads / kv_heads).  A row that sees nothing is 0.
  * Scores, softmax statistics and sums are FP32; a weight times a value's
- * scale is rounded to two BF16 parts (to one in calls for long prompts: with
- * max_q and B of 448 workgroups' rows and more), the result once to BF16.
+ * scale is rounded to two BF16 parts (2^-16 of it), the result once to BF16.
  * How the work is cut goes by max_q, B and max_kv alone: requests of one new
  * token beside long prompts are faster in a call of their own.
  *   q            device bf16 [T][q_heads][head_dim], 16-byte aligned, rows

@@ -13,7 +13,7 @@ import oracle
 import seeded_inputs as si
 from oracle import step as ref
 from test_gpu_step import DEV, attn_case, bf16, check_attn, check_queries, host, ints, rope_table, same_bits, to_device, w4
-from test_gpu_step_paths import attn
+from test_gpu_step_paths import MANY, TWO_PARTS, attn, many
 
 pytestmark = pytest.mark.gpu
 
@@ -186,5 +186,13 @@ def test_window_of_everything_with_more_rows_than_tokens(dim, B, rows, block, wi
         at = slice(b * rows, (b + 1) * rows)
         assert np.all(got[at][:hidden] == 0)
         check_attn(got[at], *ref.attention(q[at], cache, table[b:b + 1], [tokens], [0, rows], 0.1), f"request {b}")
+
+
+@pytest.mark.parametrize("lens,news,hq,hkv,dim,block,window,sinks", MANY)
+def test_prompts_are_as_exact_as_few_rows(lens, news, hq, hkv, dim, block, window, sinks):
+    """Weights keep 16 bits in calls for long prompts too: a request's rounding does not go by the company it is in."""
+    cache, table, q_start, q = attn_case(61, lens, news, hq, hkv, dim, block)
+    got = attn(to_device(cache), q, table, lens, q_start, many(hq, hkv), window=window, sinks=sinks)
+    check_attn(got, *ref.attention(q, cache, table, lens, q_start, float(np.float32(dim ** -0.5)), window, sinks, TWO_PARTS))
 
 
