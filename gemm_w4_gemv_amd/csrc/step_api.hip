@@ -1,5 +1,6 @@
 // C ABI of the decode step's operators (w4_step.h): host-side validation and
-// dispatch.  As in w4_api.hip, every check runs before the first HIP call.
+// dispatch.  As in w4_api.hip, every check runs before the first HIP call.  An
+// array without elements may have no address.
 #include <math.h>
 
 #include <initializer_list>
@@ -139,13 +140,14 @@ W4_API w4_status w4_qk_norm_rope(const w4_qk_args* args, const w4_kv4_cache* cac
         if (cache->kv_heads != a.kv_heads || cache->head_dim != a.head_dim)
             return fail(W4_ERR_SHAPE, "%s: the cache has %d heads of %d, the call %d of %d", fn, cache->kv_heads,
                         cache->head_dim, a.kv_heads, a.head_dim);
-        if (!a.v || !a.slots) return fail(W4_ERR_NULL, "%s: v and slots must not be NULL with a cache", fn);
-    } else if (!a.k_out) {
+        if (a.T > 0 && (!a.v || !a.slots)) return fail(W4_ERR_NULL, "%s: v and slots must not be NULL with a cache", fn);
+    } else if (a.T > 0 && !a.k_out) {
         return fail(W4_ERR_NULL, "%s: k_out must not be NULL without a cache", fn);
     }
-    if (!a.k || (a.q_heads > 0 && (!a.q || !a.q_out))) return fail(W4_ERR_NULL, "%s: q, k and q_out must not be NULL", fn);
+    if (a.T > 0 && (!a.k || (a.q_heads > 0 && (!a.q || !a.q_out))))
+        return fail(W4_ERR_NULL, "%s: q, k and q_out must not be NULL", fn);
     if (a.rot_dim > 0) {
-        if (!a.cos_sin || !a.positions) return fail(W4_ERR_NULL, "%s: cos_sin and positions must not be NULL", fn);
+        if (!a.cos_sin || (a.T > 0 && !a.positions)) return fail(W4_ERR_NULL, "%s: cos_sin and positions must not be NULL", fn);
         if (a.max_pos < 1) return fail(W4_ERR_SHAPE, "%s: max_pos = %d must be at least 1", fn, a.max_pos);
     }
     if ((int64_t)a.T * ((a.q_heads + 2ll * a.kv_heads + 6) / 4) > kMaxGrid)
@@ -208,7 +210,7 @@ W4_API w4_status w4_kv4_read(const w4_kv4_cache* cache, const int32_t* slots, in
     const w4_status st = check_cache(fn, cache);
     if (st != W4_OK) return st;
     if (n < 0) return fail(W4_ERR_SHAPE, "%s: n = %d is negative", fn, n);
-    if (!slots || (!k_out && !v_out)) return fail(W4_ERR_NULL, "%s: slots and one output must not be NULL", fn);
+    if (n > 0 && (!slots || (!k_out && !v_out))) return fail(W4_ERR_NULL, "%s: slots and one output must not be NULL", fn);
     if (!aligned(slots, 4) || !aligned(k_out, 16) || !aligned(v_out, 16))
         return fail(W4_ERR_ALIGN, "%s: slots must be 4-byte, outputs 16-byte aligned", fn);
     if ((int64_t)n * cache->kv_heads > kMaxGrid) return fail(W4_ERR_SHAPE, "%s: n = %d is too many rows for one call", fn, n);
@@ -237,9 +239,10 @@ W4_API w4_status w4_kv4_attn(const w4_attn_args* args, const w4_kv4_cache* cache
     st = check_attn_shape(fn, args, cache);
     if (st != W4_OK) return st;
     const w4_attn_args& a = *args;
-    if (!a.q || !a.out || !a.kv_lens) return fail(W4_ERR_NULL, "%s: q, out and kv_lens must not be NULL", fn);
+    if ((a.T > 0 && (!a.q || !a.out)) || (a.B > 0 && !a.kv_lens))
+        return fail(W4_ERR_NULL, "%s: q, out and kv_lens must not be NULL", fn);
     if (a.max_blocks < 0) return fail(W4_ERR_SHAPE, "%s: max_blocks = %d is negative", fn, a.max_blocks);
-    if (a.max_blocks > 0 && !a.block_table) return fail(W4_ERR_NULL, "%s: block_table must not be NULL", fn);
+    if (a.B > 0 && a.max_blocks > 0 && !a.block_table) return fail(W4_ERR_NULL, "%s: block_table must not be NULL", fn);
     if (!a.q_start && a.T != a.B) return fail(W4_ERR_SHAPE, "%s: without q_start T = %d must be B = %d", fn, a.T, a.B);
     if (!(a.scale > 0.0f) || !isfinite(a.scale)) return fail(W4_ERR_ARG, "%s: scale must be positive and finite", fn);
     const int64_t wide = (int64_t)a.q_heads * cache->head_dim;
@@ -276,7 +279,8 @@ W4_API w4_status w4_sample(const void* logits, int64_t row_stride, const double*
                            const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens, int rows,
                            int vocab, void* workspace, size_t workspace_bytes, void* stream) {
     const char* fn = "w4_sample";
-    if (!logits || !uniform || !tokens) return fail(W4_ERR_NULL, "%s: logits, uniform and tokens must not be NULL", fn);
+    if (rows != 0 && (!logits || !uniform || !tokens))
+        return fail(W4_ERR_NULL, "%s: logits, uniform and tokens must not be NULL", fn);
     if (rows < 0 || rows > 65535) return fail(W4_ERR_SHAPE, "%s: rows = %d must lie in [0, 65535]", fn, rows);
     if (vocab < 1 || vocab > W4_SAMPLE_MAX_VOCAB)
         return fail(W4_ERR_SHAPE, "%s: vocab = %d must lie in [1, %d]", fn, vocab, W4_SAMPLE_MAX_VOCAB);

@@ -6,8 +6,8 @@
  * the caller owns every buffer, arguments are validated on the host before
  * any HIP call, calls are asynchronous on ``stream``, never allocate, never
  * synchronise and can be captured into a HIP graph; an empty problem is
- * W4_OK with nothing launched; the same call on the same inputs returns the
- * same bits.  Outputs must not overlap any input unless said otherwise.
+ * W4_OK with nothing launched, and an array without elements may be NULL; the
+ * same call on the same inputs returns the same bits.  Outputs must not overlap any input unless said otherwise.
  *
  * The cache.  Pages of ``block_size`` tokens, each with every key/value head;
  * a slot is page * block_size + offset.  A token's vector of one head is cut

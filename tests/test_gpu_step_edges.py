@@ -196,3 +196,24 @@ def test_prompts_are_as_exact_as_few_rows(lens, news, hq, hkv, dim, block, windo
     check_attn(got, *ref.attention(q, cache, table, lens, q_start, float(np.float32(dim ** -0.5)), window, sinks, TWO_PARTS))
 
 
+# ----------------------------------------------------------- empty problems
+def test_a_step_without_rows():
+    """What w4_kv4_plan gives when every request rests, through the binding: no rows, nothing written, no error."""
+    cache = w4.Kv4Cache.empty(2, 16, 2, 128)
+    empty = lambda *shape: torch.zeros(*shape, dtype=bf16, device=DEV)  # noqa: E731
+    none = ints([])
+    q, k, out = empty(0, 4, 128), empty(0, 2, 128), empty(0, 4, 128)
+    table, lens = ints([[0, 1]]), ints([20])
+    q_start, kv_lens, counts = ints([7, 7]), ints([7]), ints([7, 7])
+    w4.w4_kv4_plan(lens, ints([0]), table, none, ints([0]), 16, q_start, kv_lens, none, none, counts)
+    w4.w4_qk_norm_rope(q, k, none, torch.from_numpy(rope_table(128)).to(DEV), q_out=q, v=k, cache=cache, slots=none)
+    w4.w4_qk_norm_rope(q, k, q_out=q, k_out=k)
+    w4.w4_kv4_read(cache, none, k, k.clone())
+    assert w4.w4_kv4_attn(q, cache, table, lens, out, q_start=q_start) is out
+    w4.w4_kv4_attn(q, cache, table[:0], lens[:0], out)
+    tokens = ints([])
+    assert w4.w4_sample(empty(0, 50000), torch.zeros(0, dtype=torch.float64, device=DEV), tokens) is tokens
+    torch.cuda.synchronize()
+    assert q_start.tolist() == [0, 0] and kv_lens.tolist() == [20] and counts.tolist() == [0, 0]
+
+
