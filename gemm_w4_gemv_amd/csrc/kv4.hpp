@@ -35,6 +35,9 @@ struct PlanArgs {
 };
 hipError_t launch_kv4_plan(const PlanArgs& a, hipStream_t stream);
 
+// Workgroups of 256 threads that these two launch (T and n at least 1).
+int64_t qk_norm_rope_groups(const w4_qk_args& a, bool cached);
+int64_t kv4_read_groups(const w4_kv4_cache& c, int n);
 hipError_t launch_qk_norm_rope(const w4_qk_args& a, const w4_kv4_cache* cache, hipStream_t stream);
 hipError_t launch_kv4_read(const w4_kv4_cache& c, const int32_t* slots, int n, void* k_out, void* v_out,
                            hipStream_t stream);

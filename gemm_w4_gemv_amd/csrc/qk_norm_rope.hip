@@ -376,16 +376,19 @@ __global__ __launch_bounds__(kThreads) void kv4_read_kernel(Kv4 cache, const int
     if (v_out) put(v_out, cache.vc[((ph * (bs / 4) + off / 4) * kLanes + li) * 4 + off % 4], cache.vm[mi]);
 }
 
+// Waves that share a token: few tokens, one run of heads each, all in flight at
+// once; many, one wave, which then loads its cosines and sines once.
+int64_t parts_of(const w4_qk_args& a, bool cached) {
+    const int64_t heads = kWave / (a.head_dim / 8);
+    const int64_t runs = (a.q_heads + heads - 1) / heads + (cached ? 2 : 1) * ((a.kv_heads + heads - 1) / heads);
+    const int64_t parts = (8192 + (int64_t)a.T - 1) / a.T;
+    return parts > runs ? runs : parts;
+}
+
 template <int D>
 hipError_t launch_d(const w4_qk_args& a, const w4_kv4_cache* c, hipStream_t stream) {
-    constexpr int kHeads = kWave / (D / 8);
-    const int runs = (a.q_heads + kHeads - 1) / kHeads + (c ? 2 : 1) * ((a.kv_heads + kHeads - 1) / kHeads);
-    // Few tokens: one run a wave, all in flight at once; many: a token's runs
-    // in one wave, which then loads its cosines and sines once.
-    int parts = (8192 + a.T - 1) / a.T;
-    parts = parts < 1 ? 1 : parts > runs ? runs : parts;
-    const int64_t waves = (int64_t)a.T * parts, per = kThreads / kWave;
-    const dim3 grid((unsigned)((waves + per - 1) / per)), block(kThreads);
+    const int parts = (int)parts_of(a, c != nullptr);
+    const dim3 grid((unsigned)qk_norm_rope_groups(a, c != nullptr)), block(kThreads);
     const Kv4 cache = c ? kv4_of(*c) : Kv4{};
     if (c) {
         if (a.interleaved) {
@@ -403,6 +406,14 @@ hipError_t launch_d(const w4_qk_args& a, const w4_kv4_cache* c, hipStream_t stre
 
 }  // namespace
 
+int64_t qk_norm_rope_groups(const w4_qk_args& a, bool cached) {
+    const int64_t per = kThreads / kWave;
+    return ((int64_t)a.T * parts_of(a, cached) + per - 1) / per;
+}
+int64_t kv4_read_groups(const w4_kv4_cache& c, int n) {
+    return ((int64_t)n * c.kv_heads * (c.head_dim / 8) + kThreads - 1) / kThreads;
+}
+
 hipError_t launch_qk_norm_rope(const w4_qk_args& a, const w4_kv4_cache* c, hipStream_t stream) {
     switch (a.head_dim) {
         case 64: return launch_d<64>(a, c, stream);
@@ -414,8 +425,7 @@ hipError_t launch_qk_norm_rope(const w4_qk_args& a, const w4_kv4_cache* c, hipSt
 hipError_t launch_kv4_read(const w4_kv4_cache& c, const int32_t* slots, int n, void* k_out, void* v_out,
                            hipStream_t stream) {
     const Kv4 cache = kv4_of(c);
-    const int64_t lanes = (int64_t)n * c.kv_heads * (c.head_dim / 8);
-    const dim3 grid((unsigned)((lanes + kThreads - 1) / kThreads)), block(kThreads);
+    const dim3 grid((unsigned)kv4_read_groups(c, n)), block(kThreads);
     uint16_t *k = static_cast<uint16_t*>(k_out), *v = static_cast<uint16_t*>(v_out);
     switch (c.head_dim) {
         case 64: kv4_read_kernel<64><<<grid, block, 0, stream>>>(cache, slots, n, k, v); break;

@@ -66,8 +66,9 @@ w4_status check_cache(const char* fn, const w4_kv4_cache* c) {
     return W4_OK;
 }
 
-// A kernel launch counts its workgroups in 32 bits.
+// A kernel launch counts its workgroups in 32 bits, and its work-items too.
 constexpr int64_t kMaxGrid = 0x7FFFFFFFll;
+constexpr int64_t kMaxItems = 0xFFFFFFFFll;
 
 // Shared by w4_kv4_attn and its workspace size: the arguments that decide the split.
 w4_status check_attn_shape(const char* fn, const w4_attn_args* a, const w4_kv4_cache* c) {
@@ -150,7 +151,7 @@ W4_API w4_status w4_qk_norm_rope(const w4_qk_args* args, const w4_kv4_cache* cac
         if (!a.cos_sin || (a.T > 0 && !a.positions)) return fail(W4_ERR_NULL, "%s: cos_sin and positions must not be NULL", fn);
         if (a.max_pos < 1) return fail(W4_ERR_SHAPE, "%s: max_pos = %d must be at least 1", fn, a.max_pos);
     }
-    if ((int64_t)a.T * ((a.q_heads + 2ll * a.kv_heads + 6) / 4) > kMaxGrid)
+    if (a.T > 0 && w4::qk_norm_rope_groups(a, cache != nullptr) > kMaxItems / 256)
         return fail(W4_ERR_SHAPE, "%s: T = %d is too many rows for one call", fn, a.T);
     const int64_t qw = (int64_t)a.q_heads * a.head_dim, kw = (int64_t)a.kv_heads * a.head_dim;
     const auto stride_bad = [](int64_t s, int64_t wide) { return s < wide || s % 8 || s > (1ll << 40); };
@@ -213,7 +214,7 @@ W4_API w4_status w4_kv4_read(const w4_kv4_cache* cache, const int32_t* slots, in
     if (n > 0 && (!slots || (!k_out && !v_out))) return fail(W4_ERR_NULL, "%s: slots and one output must not be NULL", fn);
     if (!aligned(slots, 4) || !aligned(k_out, 16) || !aligned(v_out, 16))
         return fail(W4_ERR_ALIGN, "%s: slots must be 4-byte, outputs 16-byte aligned", fn);
-    if ((int64_t)n * cache->kv_heads > kMaxGrid) return fail(W4_ERR_SHAPE, "%s: n = %d is too many rows for one call", fn, n);
+    if (w4::kv4_read_groups(*cache, n) > kMaxItems / 256) return fail(W4_ERR_SHAPE, "%s: n = %d is too many rows for one call", fn, n);
     const size_t bytes = (size_t)n * cache->kv_heads * cache->head_dim * 2;
     const Range ko = range(k_out, k_out ? bytes : 0), vo = range(v_out, v_out ? bytes : 0);
     const CacheRanges c = ranges_of(*cache);

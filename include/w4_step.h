@@ -118,6 +118,7 @@ W4_API w4_status w4_kv4_plan(const int32_t* cached, const int32_t* new_tokens, i
  *                Each may be exactly its input (same pointer and stride).
  *                k_out may be NULL with a cache
  *   rot_dim      a multiple of 16 in [0, head_dim]
+ *   T            at most 2^26 - 4
  *   cache        NULL, or the cache (its kv_heads and head_dim are used)
  * Errors: W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_UNSUPPORTED (head_dim, block
  * size), W4_ERR_ALIGN, W4_ERR_ALIAS, W4_ERR_ARG (strides, rot_dim, eps), W4_ERR_HIP.
@@ -146,7 +147,8 @@ W4_API w4_status w4_qk_norm_rope(const w4_qk_args* args, const w4_kv4_cache* cac
  *   slots         device int32 [n]; a row whose slot lies outside the cache is
  *                 not written
  *   k_out, v_out  device bf16 [n][kv_heads][head_dim], 16-byte aligned:
- *                 bf16(q * s + m); either may be NULL, not both
+ *                 bf16(q * s + m); either may be NULL, not both; at most 2^35 - 2^11
+ *                 values in each
  * Errors: W4_ERR_NULL, W4_ERR_SHAPE, W4_ERR_UNSUPPORTED, W4_ERR_ALIGN, W4_ERR_ALIAS, W4_ERR_HIP.
  */
 W4_API w4_status w4_kv4_read(const w4_kv4_cache* cache, const int32_t* slots, int n, void* k_out, void* v_out,

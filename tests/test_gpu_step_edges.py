@@ -217,3 +217,21 @@ def test_a_step_without_rows():
     assert q_start.tolist() == [0, 0] and kv_lens.tolist() == [20] and counts.tolist() == [0, 0]
 
 
+# ------------------------------------------------------------- launch sizes
+def test_the_largest_call():
+    """As many tokens as a launch counts work-items for: the first and the last are done like any others."""
+    T, dim = 2 ** 26 - 4, 64
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("less than 24 GiB of memory is free")
+    x = si.bf16_normal(85, (1,), (8, 1, dim))
+    w = si.bf16_normal(85, (2,), (dim,))
+    k = torch.zeros(T, 1, dim, dtype=bf16, device=DEV)
+    k[:4], k[-4:] = host.bf16_tensor(x[:4]), host.bf16_tensor(x[4:])
+    out = torch.full_like(k, 7.0)
+    w4.w4_qk_norm_rope(None, k, k_out=out, k_weight=host.bf16_tensor(w))
+    torch.cuda.synchronize()
+    want = ref.round_to_bf16(ref.norm_rope(x, w, None, None, 0, False, 1e-6, 0.0))
+    assert same_bits(host.bits_of(out[:4]), want[:4]) and same_bits(host.bits_of(out[-4:]), want[4:])
+    assert int(torch.count_nonzero(out[4:-4])) == 0
+
+

@@ -29,3 +29,15 @@ def test_empty_problems_are_checked_for_the_rest(call, kwargs, status):
     assert call(**kwargs) == status
 
 
+# ---------------------------------------------------------------- launch sizes
+@pytest.mark.parametrize("call,kwargs", [
+    (qk, dict(T=1 << 26)), (qk, dict(T=(1 << 26) - 3, cache=False)), (qk, dict(T=2 ** 31 - 1, hq=1, hkv=1, dim=64, rot=64)),
+    (read, dict(n=1 << 27, hkv=2)), (read, dict(n=(1 << 28) - 15, hkv=1)), (read, dict(n=1 << 29, hkv=1, dim=64)),
+    (read, dict(n=1 << 22, hkv=32, dim=256)),
+])
+def test_launches_past_2_32_work_items_are_refused(call, kwargs):
+    """A launch counts its work-items in 32 bits: 64 for each token from 8192 tokens on, one for 8 values read back."""
+    assert call(**kwargs) == SHAPE
+    assert "too many rows" in w4.w4_last_error()
+
+
