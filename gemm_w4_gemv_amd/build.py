@@ -3,7 +3,8 @@
 Each ``.hip`` file is compiled to an object under ``_build/`` in parallel,
 then linked into ``gemm_w4_gemv_amd/libw4.so``, next to this file.  No GPU is
 needed: hipcc cross-compiles for gfx950.  The binding's compiled checks
-(``csrc/marshal.cpp``, host code against torch) become ``_marshal.so`` beside it.
+(``csrc/marshal.cpp``, host code against torch) become the module ``_marshal``
+beside it, where they compile: nothing needs them.
 
     python gemm_w4_gemv_amd/build.py            # build
     python gemm_w4_gemv_amd/build.py --asm      # also write device assembly (.s)
@@ -17,6 +18,7 @@ import concurrent.futures as cf
 import importlib.util
 import os
 import pathlib
+import re
 import shutil
 import subprocess
 import sys
@@ -27,7 +29,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 BUILD = ROOT / "_build"
 LIB = PKG / "libw4.so"
-MARSHAL = PKG / "_marshal.so"
+MARSHAL = PKG / f"_marshal{sysconfig.get_config_var('EXT_SUFFIX')}"
 ARCH = "gfx950"
 
 
@@ -95,23 +97,36 @@ def build(verbose: bool = False, asm: bool = False, defines=(), lib: pathlib.Pat
     return lib
 
 
-def build_marshal() -> None:
-    """Compile the binding's tensor checks (csrc/marshal.cpp) against the installed torch.
+def build_marshal(to: pathlib.Path = MARSHAL) -> bool:
+    """Compile the binding's tensor checks (csrc/marshal.cpp) against the installed torch; False where that fails.
 
-    The same checks are in step.py; without these a call only takes some 2 us longer."""
+    The same checks are in step.py; without these a call only takes some 2 us longer.  They read torch's
+    own structures, so the module carries the torch and the Python that it was built for, step.py takes it
+    with these alone, and copies of other builds are removed whether this one succeeds or not."""
+    for old in to.parent.glob("_marshal*.so*"):
+        old.unlink()
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.origin:
-        raise RuntimeError("torch not found")
+        print("the binding's checks are not compiled: torch not found", file=sys.stderr)
+        return False
     torch = pathlib.Path(spec.origin).parent
-    tmp = MARSHAL.with_suffix(".so.tmp")
-    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-I{torch / 'include'}", f"-I{torch / 'include/torch/csrc/api/include'}",
-           f"-I{sysconfig.get_paths()['include']}", str(CSRC / "marshal.cpp"), "-o", str(tmp), f"-L{torch / 'lib'}",
-           "-lc10", "-ltorch_cpu", "-ltorch_python"]
-    rc, out = _run(cmd)
+    tmp = to.with_name(to.name + ".tmp")
+    try:
+        version = dict(re.findall(r"^(__version__|git_version) = '([^']*)'", (torch / "version.py").read_text(), re.M))
+        built_for = f"{version['__version__']} {version['git_version']}"
+        cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+               f'-DW4_BUILT_FOR="{built_for}"', f"-I{torch / 'include'}", f"-I{torch / 'include/torch/csrc/api/include'}",
+               f"-I{sysconfig.get_paths()['include']}", str(CSRC / "marshal.cpp"), "-o", str(tmp), f"-L{torch / 'lib'}",
+               "-lc10", "-ltorch_cpu", "-ltorch_python"]
+        rc, out = _run(cmd)
+    except (OSError, KeyError) as e:
+        rc, out = 1, repr(e)
     if rc:
-        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{out}")
-    os.replace(tmp, MARSHAL)
+        tmp.unlink(missing_ok=True)
+        print(f"the binding's checks are not compiled, the ones in Python take their place:\n{out}", file=sys.stderr)
+        return False
+    os.replace(tmp, to)
+    return True
 
 
 if __name__ == "__main__":

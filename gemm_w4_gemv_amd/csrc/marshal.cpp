@@ -5,7 +5,8 @@
 //
 // Each function takes what the Python function of the same name in step.py
 // takes and gives what that gives; where a tensor is not as it should be it
-// calls that function, which says what is wrong.
+// calls that function, which says what is wrong.  The module's ``built_for``
+// names the torch (W4_BUILT_FOR, from the build) and the Python that it fits.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <torch/csrc/Dtype.h>
@@ -123,4 +124,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__marshal(void) {
+    PyObject* m = PyModule_Create(&module);
+    PyObject* built_for = m ? Py_BuildValue("(si)", W4_BUILT_FOR, (int)(PY_VERSION_HEX >> 16)) : nullptr;
+    if (!built_for || PyModule_AddObject(m, "built_for", built_for)) {
+        Py_XDECREF(built_for);
+        Py_XDECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import sys
 
 import torch
 
@@ -146,13 +147,21 @@ def _optional_addresses(device, *spec):
 
 
 # The same checks compiled (csrc/marshal.cpp), for host time alone: where a
-# tensor fails one, they call these, which say what is wrong.
+# tensor fails one, they call these, which say what is wrong.  They know how this
+# torch lays out a tensor, so a module built for another one is not taken.
 _in_python = (_addresses, _optional_addresses, _heads)
+
+
+def _fits(module) -> bool:
+    here = (f"{torch.version.__version__} {torch.version.git_version}", sys.hexversion >> 16)
+    return getattr(module, "built_for", None) == here
+
+
 try:
     from . import _marshal
-except ImportError:  # built for another torch, or not at all
-    pass
-else:
+except ImportError:  # not built, or for another torch
+    _marshal = None
+if _marshal is not None and _fits(_marshal):
     _marshal.begin(*_in_python)
     _addresses, _optional_addresses, _heads = _marshal.addresses, _marshal.optional_addresses, _marshal.heads
 

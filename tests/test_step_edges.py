@@ -1,9 +1,17 @@
 """CPU tests of the decode step's operators: calls at the edge of what the header allows, answered before any HIP call."""
 from __future__ import annotations
 
+import importlib.util
+import pathlib
+import sys
+import types
+
 import pytest
+import torch
 
 from test_step import NULL, OK, SHAPE, attn, qk, read, sample, w4
+
+ROOT = pathlib.Path(__file__).resolve().parents[1]
 
 
 # ------------------------------------------------------------ empty problems
@@ -39,5 +47,53 @@ def test_launches_past_2_32_work_items_are_refused(call, kwargs):
     """A launch counts its work-items in 32 bits: 64 for each token from 8192 tokens on, one for 8 values read back."""
     assert call(**kwargs) == SHAPE
     assert "too many rows" in w4.w4_last_error()
+
+
+# -------------------------------------------------- the binding's compiled checks
+def build_module():
+    spec = importlib.util.spec_from_file_location("w4_build", ROOT / "gemm_w4_gemv_amd" / "build.py")
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+def test_compiled_checks_are_optional(tmp_path, monkeypatch, capfd):
+    """Without a compiler, torch's headers or its version the build goes on, says so and leaves no older copy behind."""
+    build = build_module()
+    to = tmp_path / build.MARSHAL.name
+    for way in ("compiler", "source", "version"):
+        stale = [tmp_path / "_marshal.so", to]
+        for f in stale:
+            f.write_bytes(b"of another build")
+        with monkeypatch.context() as m:
+            if way == "compiler":
+                m.setenv("CXX", str(tmp_path / "no such compiler"))
+            elif way == "source":
+                m.setattr(build, "CSRC", tmp_path)
+            else:
+                m.setattr(build.importlib.util, "find_spec", lambda name: None)
+            assert build.build_marshal(to) is False
+        assert "not compiled" in capfd.readouterr().err
+        assert not list(tmp_path.glob("_marshal*"))
+
+
+def test_compiled_checks_are_taken_for_this_torch_alone():
+    from gemm_w4_gemv_amd import step
+    built_for = (f"{torch.version.__version__} {torch.version.git_version}", sys.hexversion >> 16)
+    assert step._fits(types.SimpleNamespace(built_for=built_for))
+    for other in ((built_for[0] + "0", built_for[1]), (built_for[0], built_for[1] + 1), None):
+        assert not step._fits(types.SimpleNamespace(built_for=other))
+    assert not step._fits(types.SimpleNamespace())  # one that does not say
+
+
+def test_compiled_checks_are_in_use_where_they_can_be_built(tmp_path):
+    from gemm_w4_gemv_amd import step
+    build = build_module()
+    if not build.build_marshal(tmp_path / build.MARSHAL.name):
+        pytest.skip("the checks do not compile here")
+    assert build.MARSHAL.exists(), "the library was built without them"
+    assert step._marshal is not None and step._marshal.__file__ == str(build.MARSHAL)
+    assert step._addresses is step._marshal.addresses and step._heads is step._marshal.heads
+    assert step._optional_addresses is step._marshal.optional_addresses
 
 
