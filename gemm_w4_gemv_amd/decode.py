@@ -194,8 +194,8 @@ class DecodeStep:
     ``y`` (bfloat16 [N]).  The tensors must stay alive while the graph does.
 
     With ``attention`` (and then ``name`` and ``layer`` in the dicts, see
-    ``link_decoder_inputs``) every layer's q, k and v go through its cache
-    before its o; with ``sampler`` the step ends in a token from the output of
+    ``link_decoder_inputs``) every layer's q, k and v, in any order, go through its
+    cache before its o; with ``sampler`` the step ends in a token from the output of
     the linear named "logits".  Both are launches of their own, not stages of the chain.
     """
 
@@ -207,6 +207,10 @@ class DecodeStep:
             raise ValueError("the chain runs linears alone: attention and sampler go with mode 'launches'")
         self.attention, self.sampler = attention, sampler
         self.linears = list(linears)
+        if attention is not None:
+            self._check_layers()
+        if sampler is not None and [lin["name"] for lin in self.linears].count("logits") != 1:
+            raise ValueError("a sampler needs one linear named 'logits'")
         self.stream = stream if stream is not None else torch.cuda.Stream()
         if attention is not None or sampler is not None:  # their buffers are filled on the current stream
             self.stream.wait_stream(torch.cuda.current_stream(self.stream.device))
@@ -219,6 +223,26 @@ class DecodeStep:
             off = (-self.workspace.data_ptr()) % 256
             self.chain = w4_chain_create(self.linears, self.workspace[off:off + nbytes])
 
+    def _check_layers(self) -> None:
+        """Each layer is one of the attention's and has q, k and v once, and its o after them."""
+        seen = {}
+        for lin in self.linears:
+            name, layer = lin["name"], lin["layer"]
+            if name not in ("q", "k", "v", "o"):
+                continue
+            if not 0 <= layer < len(self.attention.caches):
+                raise ValueError(f"layer {layer}: the attention has {len(self.attention.caches)} layers")
+            names = seen.setdefault(layer, [])
+            if name in names:
+                raise ValueError(f"layer {layer} has two linears named '{name}'")
+            if "o" in names:
+                raise ValueError(f"layer {layer}: o comes before {name}, which its attention reads")
+            names.append(name)
+        for layer, names in seen.items():
+            for name in ("q", "k", "v"):
+                if name not in names:
+                    raise ValueError(f"layer {layer} has no linear named '{name}'")
+
     def run_eager(self) -> None:
         """Run the step directly on the step's stream (no graph)."""
         if self.mode == "chain":
@@ -226,15 +250,17 @@ class DecodeStep:
             return
         if self.attention is not None:
             self.attention.begin(self.stream)
-        made = {}
+        made = {}  # of each layer: its q, k and v
         for lin in self.linears:
             w4_gemv(lin["x"], lin["qw"], lin["s"], lin["z"], lin["y"], stream=self.stream)
             if self.attention is None and self.sampler is None:
                 continue
-            name = lin["name"]
-            made[name] = lin["y"]
-            if self.attention is not None and name == "v":
-                self.attention.run(lin["layer"], made["q"], made["k"], made["v"], self.stream)
+            name, layer = lin["name"], lin["layer"]
+            if self.attention is not None and name in ("q", "k", "v"):
+                got = made.setdefault(layer, {})
+                got[name] = lin["y"]
+                if len(got) == 3:
+                    self.attention.run(layer, got["q"], got["k"], got["v"], self.stream)
             if self.sampler is not None and name == "logits":
                 self.sampler.run(lin["y"], self.stream)
         if self.attention is not None:

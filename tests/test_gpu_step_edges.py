@@ -11,8 +11,10 @@ import torch
 
 import oracle
 import seeded_inputs as si
+from gemm_w4_gemv_amd.decode import DecodeStep
 from oracle import step as ref
 from test_gpu_step import DEV, attn_case, bf16, check_attn, check_queries, host, ints, rope_table, same_bits, to_device, w4
+from test_gpu_decode_attention import build, feed
 from test_gpu_step_paths import MANY, TWO_PARTS, attn, many
 
 pytestmark = pytest.mark.gpu
@@ -233,5 +235,29 @@ def test_the_largest_call():
     want = ref.round_to_bf16(ref.norm_rope(x, w, None, None, 0, False, 1e-6, 0.0))
     assert same_bits(host.bits_of(out[:4]), want[:4]) and same_bits(host.bits_of(out[-4:]), want[4:])
     assert int(torch.count_nonzero(out[4:-4])) == 0
+
+
+# --------------------------------------------------------------- decode step
+@pytest.mark.parametrize("order", [("v", "k", "q"), ("k", "v", "q"), ("q", "v", "k")])
+def test_decode_step_in_any_order_of_q_k_and_v(order):
+    """The attention of a layer runs when its three outputs are there, whichever comes last: same bits, also captured."""
+    a, b = build(32)[0], build(32)[0]
+    first = {"q": order[0], "k": order[1], "v": order[2]}
+    by = {(lin["layer"], lin["name"]): lin for lin in b.linears}
+    b.linears = [by[lin["layer"], first.get(lin["name"], lin["name"])] for lin in b.linears]
+    c = DecodeStep(b.linears, attention=b.attention, sampler=b.sampler)
+    assert len({lin["x"].data_ptr() for lin in b.linears[:3]}) == 1
+    for t in range(6):
+        for s in (a, b):
+            feed(s, t)  # into the input that layer 0's three share
+        a.run_eager()
+        c.replay() if t % 2 else c.run_eager()
+        torch.cuda.synchronize()
+        for lin in a.linears:
+            other = by[lin["layer"], lin["name"]]
+            assert torch.equal(lin["y"].view(torch.int16), other["y"].view(torch.int16)), (t, lin["layer"], lin["name"])
+        assert torch.equal(a.attention.out.view(torch.int16), b.attention.out.view(torch.int16))
+        assert int(a.sampler.tokens) == int(b.sampler.tokens)
+    c.destroy()
 
 

@@ -97,3 +97,27 @@ def test_compiled_checks_are_in_use_where_they_can_be_built(tmp_path):
     assert step._optional_addresses is step._marshal.optional_addresses
 
 
+# ------------------------------------------------------------- the decode step
+def linears(*names, layer=0):
+    return [{"name": n, "layer": layer} for n in names]
+
+
+ATTENTION = types.SimpleNamespace(caches=[None, None])
+
+
+@pytest.mark.parametrize("lins,attention,sampler,what", [
+    (linears("q", "k", "o", "v"), True, False, "o"), (linears("o", "q", "k", "v"), True, False, "o"),
+    (linears("q", "v", "o"), True, False, "k"), (linears("q", "k", "v", "o") + linears("v", "o", layer=1), True, False, "q"),
+    (linears("q", "k", "v", "q", "o"), True, False, "q"), (linears("q", "k", "v", "o", "o"), True, False, "o"),
+    (linears("q", "k", "v", "o", layer=2), True, False, "layer 2"), (linears("q", "k", "v", "o", layer=-1), True, False, "layer -1"),
+    (linears("q", "k", "v", "o"), True, True, "logits"), (linears("logits", "logits"), False, True, "logits"),
+    ([], False, True, "logits"),
+])
+def test_decode_step_refuses_linears_out_of_order(lins, attention, sampler, what):
+    """Before anything runs: an o that would read what its attention has not written, a layer without its three,
+    one that the attention does not have, a sampler without logits."""
+    from gemm_w4_gemv_amd.decode import DecodeStep
+    with pytest.raises(ValueError, match=what):
+        DecodeStep(lins, stream=object(), attention=ATTENTION if attention else None, sampler=object() if sampler else None)
+
+
