@@ -21,7 +21,7 @@ __all__ = ["Kv4Cache", "w4_kv4_plan", "w4_qk_norm_rope", "w4_kv4_read", "w4_kv4_
 KV4_GROUP = 128
 KV4_PLAN_MAX_BATCH = 4096
 SAMPLE_MAX_VOCAB = 1048576
-_INT_MAX = 2 ** 31 - 1  # ctypes would cut a larger length to 32 bits without a word
+_INT_MAX = 2 ** 31 - 1
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int
@@ -87,6 +87,16 @@ def _refuse(t, name, dtype, device):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     raise ValueError(f"{name} lies on {t.device}, other tensors of this call on cuda:{device}")
+
+
+# ctypes cuts a number to 32 bits without a word.
+def _too_large(where, size):
+    raise ValueError(f"{where}: a size of {size} does not fit 32 bits")
+
+
+def _near(value):
+    """A bound of which any value past the largest means the same; one below 0 is refused by the library."""
+    return value if -1 <= value <= _INT_MAX else max(min(value, _INT_MAX), -1)
 
 
 def _device_of(t, name, dtype):
@@ -236,7 +246,10 @@ def w4_kv4_plan(cached, new_tokens, block_table, free_blocks, free_count, block_
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     B, width = block_table.shape
-    rows, pages, i, v = positions.numel(), free_blocks.numel(), _device_of(block_table, "block_table", _int32), _int32
+    rows, pages = positions.numel(), free_blocks.numel()
+    if max(B, width, rows, pages, abs(block_size)) > _INT_MAX:
+        _too_large("w4_kv4_plan", max(B, width, rows, pages, abs(block_size)))
+    i, v = _device_of(block_table, "block_table", _int32), _int32
     p = _addresses(i, cached, "cached", v, B, new_tokens, "new_tokens", v, B, block_table, "block_table", v, None,
                    free_blocks, "free_blocks", v, pages, free_count, "free_count", v, 1, q_start, "q_start", v, B + 1,
                    kv_lens, "kv_lens", v, B, positions, "positions", v, rows, slots, "slots", v, rows,
@@ -299,8 +312,8 @@ def w4_kv4_read(cache, slots, k_out=None, v_out=None, stream=None) -> None:
 
 def w4_kv4_attn_workspace_bytes(cache, T: int, B: int, q_heads: int, max_q: int, max_kv: int, window: int = 0,
                                 sinks: int = 0) -> int:
-    a = _AttnArgs(T=T, B=B, q_heads=q_heads, max_q=min(max_q, _INT_MAX), max_kv=min(max_kv, _INT_MAX), window=min(window, _INT_MAX),
-                  sinks=min(sinks, _INT_MAX))
+    a = _AttnArgs(T=_near(T), B=_near(B), q_heads=_near(q_heads), max_q=_near(max_q), max_kv=_near(max_kv),
+                  window=_near(window), sinks=_near(sinks))
     return lib.w4_kv4_attn_workspace_bytes(ctypes.byref(a), cache.ref)
 
 
@@ -316,19 +329,20 @@ def w4_kv4_attn(q, cache, block_table, kv_lens, out, q_start=None, max_q: int = 
     if not isinstance(cache, Kv4Cache):
         raise TypeError("cache must be a Kv4Cache")
     i, d = cache.device_index, cache.head_dim
-    qp, qs = _heads(q, "q", i, None, None, d)
-    T, q_heads, _ = q.shape
-    op, os = _heads(out, "out", i, T, q_heads, d)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     B, width = block_table.shape
+    if B > _INT_MAX or width > _INT_MAX:
+        _too_large("w4_kv4_attn", max(B, width))
+    qp, qs = _heads(q, "q", i, None, None, d)
+    T, q_heads, _ = q.shape
+    op, os = _heads(out, "out", i, T, q_heads, d)
     if max_kv is None:
         max_kv = width * cache.block_size
     tp, lp = _addresses(i, block_table, "block_table", _int32, None, kv_lens, "kv_lens", _int32, B)
     sp, = _optional_addresses(i, q_start, "q_start", _int32, B + 1)
-    a = _AttnArgs(qp, op, qs, os, tp, lp, sp, T, B, q_heads, width, min(max_q, _INT_MAX),
-                  min(max_kv, _INT_MAX), min(window, _INT_MAX), min(sinks, _INT_MAX),
-                  1.0 / math.sqrt(d) if scale is None else scale)
+    a = _AttnArgs(qp, op, qs, os, tp, lp, sp, T, B, q_heads, width, _near(max_q), _near(max_kv), _near(window),
+                  _near(sinks), 1.0 / math.sqrt(d) if scale is None else scale)
     pw, nbytes = None, 0
     if workspace is not None:
         pw, nbytes = _ptr(workspace, "workspace", workspace.dtype, i), workspace.numel() * workspace.element_size()
@@ -337,7 +351,7 @@ def w4_kv4_attn(q, cache, block_table, kv_lens, out, q_start=None, max_q: int = 
 
 
 def w4_sample_workspace_bytes(rows: int, vocab: int) -> int:
-    return lib.w4_sample_workspace_bytes(rows, vocab)
+    return lib.w4_sample_workspace_bytes(_near(rows), _near(vocab))
 
 
 def w4_sample(logits, uniform, tokens, temperature=None, top_k=None, top_p=None, min_p=None, workspace=None,
@@ -349,6 +363,8 @@ def w4_sample(logits, uniform, tokens, temperature=None, top_k=None, top_p=None,
     if logits.dim() != 2:
         raise ValueError("logits must be [rows, vocab]")
     rows, vocab = logits.shape
+    if rows > _INT_MAX or vocab > _INT_MAX:
+        _too_large("w4_sample", max(rows, vocab))
     if vocab > 1 and logits.stride(1) != 1:
         raise ValueError("logits: the values of a row must lie together")
     stride = logits.stride(0) if rows > 1 else vocab

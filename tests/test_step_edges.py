@@ -121,3 +121,46 @@ def test_decode_step_refuses_linears_out_of_order(lins, attention, sampler, what
         DecodeStep(lins, stream=object(), attention=ATTENTION if attention else None, sampler=object() if sampler else None)
 
 
+# ----------------------------------------------------- sizes past 32 bits
+FAR = 2 ** 32  # ctypes would take its lowest 32 bits: 0
+
+
+def meta(*shape, dtype=torch.int32):
+    return torch.empty(*shape, dtype=dtype, device="meta")
+
+
+@pytest.mark.parametrize("what", ["block_size", "rows", "pages", "requests", "width"])
+def test_plan_refuses_sizes_past_32_bits(what):
+    more = {k: FAR + 16 if k == what else 16 for k in ("block_size", "rows", "pages", "requests", "width")}
+    B = more["requests"]
+    table, lens, rows = meta(B, more["width"]), meta(B), meta(more["rows"])
+    with pytest.raises(ValueError, match="32 bits"):
+        w4.w4_kv4_plan(lens, lens, table, meta(more["pages"]), meta(1), more["block_size"], meta(B + 1), lens, rows, rows, meta(2))
+
+
+def test_attn_and_sample_refuse_sizes_past_32_bits():
+    from gemm_w4_gemv_amd import step
+    cache = object.__new__(step.Kv4Cache)
+    cache.head_dim, cache.device_index, cache.block_size, cache.ref = 64, 0, 16, None
+    with pytest.raises(ValueError, match="32 bits"):
+        w4.w4_sample(meta(1, FAR + 100, dtype=torch.bfloat16), None, None)
+    with pytest.raises(ValueError, match="32 bits"):
+        w4.w4_sample(meta(FAR + 1, 100, dtype=torch.bfloat16), None, None)
+    q = meta(3, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="32 bits"):
+        w4.w4_kv4_attn(q, cache, meta(FAR + 3, 0), meta(FAR + 3), q)
+    assert w4.w4_sample_workspace_bytes(1, FAR + 40000) == 0
+
+
+@pytest.mark.parametrize("name", ["max_q", "max_kv", "window", "sinks"])
+def test_attn_far_negative_sizes_are_negative(name):
+    """-2^32 is refused like -1, not taken for 0; and what is past the other end counts as the largest."""
+    import ctypes
+    from gemm_w4_gemv_amd import step
+    cache = types.SimpleNamespace(ref=ctypes.byref(step._CacheStruct(1, 1, 1, 1, 100000, 64, 1, 128)))
+    size = lambda **k: step.w4_kv4_attn_workspace_bytes(cache, **{**dict(T=4, B=4, q_heads=1, max_q=1, max_kv=100000), **k})  # noqa: E731
+    assert size() > 0
+    assert size(**{name: -1}) == 0 and size(**{name: -FAR}) == 0 and size(**{name: 1 - FAR}) == 0
+    assert size(**{name: FAR}) == size(**{name: 2 ** 31 - 1})
+
+
