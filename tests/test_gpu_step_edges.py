@@ -174,6 +174,36 @@ def test_queries_of_any_size(dim, inter, rot, weight):
             assert same_bits(host.bits_of(q)[keep], plain[keep])
 
 
+# -------------------------------------------------- queries of any size, again
+@pytest.mark.parametrize("T,h,dim,inter", [(9, 21, 256, False), (8200, 21, 256, True), (8200, 9, 128, False), (3, 40, 64, True)])
+def test_far_queries_in_place(T, h, dim, inter):
+    """Outputs over their inputs, with few and with many tokens (runs of heads in waves of their own, and in turn in one):
+    the same bits as with outputs apart; infinities and NaN as the definition has them."""
+    x = oracle.bf16_to_f64(si.bf16_normal(86, (1, T, h), (T, h + 1, dim))).copy()
+    x[1, ::3] *= 1e25
+    x[T - 1, 1::2] *= 1e-30
+    x[2, h - 1] *= 1e38 / 8
+    x[0, 2, 5], x[0, 4, 7], x[0, 4, 8] = np.inf, np.nan, -np.inf
+    bits = ref.round_to_bf16(x)
+    w = si.bf16_normal(86, (2, dim), (dim,))
+    cs, pos = rope_table(dim, 500), np.arange(T) % 500
+    args = (ints(pos), torch.from_numpy(cs).to(DEV))
+    kw = dict(q_weight=host.bf16_tensor(w), k_weight=host.bf16_tensor(w), interleaved=inter)
+    both = host.bf16_tensor(bits)
+    apart, k_out = torch.zeros(T, h, dim, dtype=bf16, device=DEV), torch.zeros(T, 1, dim, dtype=bf16, device=DEV)
+    w4.w4_qk_norm_rope(both[:, :h], both[:, h:], *args, q_out=apart, k_out=k_out, **kw)
+    w4.w4_qk_norm_rope(both[:, :h], both[:, h:], *args, q_out=both[:, :h], k_out=both[:, h:], **kw)
+    torch.cuda.synchronize()
+    assert same_bits(host.bits_of(both[:, :h]), host.bits_of(apart)) and same_bits(host.bits_of(both[:, h:]), host.bits_of(k_out))
+    at = [0, 1, 2, T - 1]
+    with np.errstate(all="ignore"):
+        want = ref.norm_rope(bits[at], w, cs, pos[at], dim, inter, 1e-6, 0.0)[:, :h]
+    got = host.bf16_values(apart[at])
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    sound = ~np.isnan(want)
+    check_queries(np.where(sound, got, 0.0), np.where(sound, want, 0.0), "q")
+
+
 # --------------------------------------------------------------- attention
 @pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 3), (2 ** 31 - 20, 0), (2 ** 31 - 64, 2 ** 31 - 1)])
 @pytest.mark.parametrize("dim,B,rows,block", [(256, 56, 64, 64), (128, 56, 128, 16), (64, 128, 128, 32), (256, 3, 40, 16), (64, 2, 5, 16)])
