@@ -27,10 +27,10 @@
 // and a second kernel joins those.
 //
 // Measured: 32 requests of up to 8192 tokens, 16 query and 8 key/value heads of
-// 256: 77 us, 4.7 TB/s of codes and pairs (with exclusive-ors for the products and
-// the same loads: 76); one of 131071 tokens, 32 and 8 heads of 128: 31 us, 4.6
-// TB/s; a prompt's 2048 tokens after 2048 others, 16 and 8 heads of 256: 179 us, 576
-// TFLOP/s.
+// 256: 77 us, 4.7 TB/s of codes and pairs (requests of equal length with as many
+// tokens 69, the longest first 70); one of 131071 tokens, 32 and 8 heads of 128: 31
+// us, 4.6 TB/s; a prompt's 2048 tokens after 2048 others, 16 and 8 heads of 256: 204
+// us, 505 TFLOP/s.
 #include <type_traits>
 
 #include "kv4.hpp"
@@ -66,8 +66,8 @@ __device__ __forceinline__ f32x4_t mfma(const u32x4_t& a, const u32x4_t& b, cons
 // rounding to BF16 (error against 64 bits 2.3e-3 instead of 1.7e-3); the second
 // part costs one more product a block of values.  Memory bounds the decode
 // kernels (32 requests up to 8192 tokens: 77 us either way); long prompts, bound by
-// instructions, pay a seventh (2048 tokens after 2048, heads of 256: 181 us with
-// one part, 206 with two; eight prompts of 1000, heads of 64: 94 and 107), so that a
+// instructions, pay a seventh (2048 tokens after 2048, heads of 256: 179 us with
+// one part, 204 with two; eight prompts of 1000, heads of 64: 92 and 106), so that a
 // request's answer does not depend on the kernel that its company picks.
 struct Pair {
     uint32_t high, low;
@@ -1176,7 +1176,7 @@ __device__ __forceinline__ void lds_barrier() {
 // one after is on its way from memory.
 // Heads of 64 fit three waves a SIMD, with two operands of the values read ahead
 // in place of four where a tile is one page (eight prompts of 1000 tokens, 32 query
-// and 8 key/value heads: 107 us, 125 with 173 registers and two waves).
+// and 8 key/value heads: 106 us, 124 with 173 registers and two waves).
 template <int D, int kNB, bool kWide>
 __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv4_attn_many_kernel(AttnArgs a) {
     typedef Rows<D, kNB> R;

@@ -11,9 +11,11 @@
 // lane's eight 4-bit codes are one word of the cache.
 // Memory bounds it for prompts, as long as enough of it is asked for at once
 // (four heads' loads ahead): 8192 tokens of 40 heads of 128 without a cache 39 us,
-// 4.4 TB/s; 4099 tokens of 32 heads of 256 into the cache 40 us, where the keys'
-// FP64 and the codes cost about as much as the memory; launch and latency for a decode step, where the
-// token's heads are spread over waves instead.
+// 4.3 TB/s.  4099 tokens of 32 heads of 256 into the cache take 38 us, half of the
+// waves' cycles waits: 72 MB are read as they must be, but 58 MB written where 43
+// are due, for the cache is written four bytes at a time (values' words at a stride
+// of 16).  Launch and latency bound a decode step, where the token's heads are
+// spread over waves instead.
 #include <type_traits>
 
 #include "kv4.hpp"

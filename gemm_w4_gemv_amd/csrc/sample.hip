@@ -19,7 +19,7 @@
 // one launch and without lists (one row of 32000: 15 us instead of 21, 300 rows
 // 30 instead of 44).
 // What bounds it: the count by the turns that LDS atomics take (64 rows of
-// 262144: 16.5 us, 2 TB/s of logits), the pick by the length of its chain of
+// 262144: 16.5 us, 2 TB/s of logits; bank conflicts are 40 % of the LDS cycles), the pick by the length of its chain of
 // dependent steps (14 us for one row, 21 for 64, a compute unit each).
 // Counts are whole numbers and masses are summed in a fixed order, so a
 // result depends on no order in which anything finishes.
@@ -55,7 +55,9 @@ __device__ __forceinline__ uint32_t bins_of_pair(uint32_t w) {  // two logits ->
 // 2^y for y <= 0: the power of the nearest whole number, and the Taylor
 // series of 2^f to the 13th term for the rest (|f| <= 1/2, so the next term is
 // under 2^-53).  A weight costs 15 operations instead of some 60 with a
-// division and the library's exp; it is off by a few 2^-53.
+// division and the library's exp.  The series is off by a few 2^-53; its argument
+// has the roundings of a difference times a rate, so a weight 2^y is off by some
+// |y| 2^-53 besides.
 __device__ __forceinline__ double exp2_series(double y) {
     y = fmax(y, -2000.0);  // 0 far above that
     const double n = rint(y), f = y - n;

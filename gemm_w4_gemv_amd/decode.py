@@ -121,7 +121,9 @@ class DecodeAttention:
     bfloat16 [1, q_heads, head_dim], what its o linear reads.  ``cached`` (int32 [1]) counts the
     tokens held; a step adds one.  A prompt is stored by the same calls with more rows: its
     tokens' slots are what ``w4_kv4_plan`` gives on ``table``, ``free`` and ``free_count``.
-    A token past ``max_kv`` has no slot, and its outputs are NaN."""
+    A token past the last page (``max_kv`` in whole pages) has no slot, and its outputs are NaN.
+    All layers have the same heads, window and rotation; weights are taken as they are and a
+    rotation's pairs are (i, i + rot_dim / 2)."""
 
     def __init__(self, layers: int, q_heads: int, kv_heads: int, head_dim: int, max_kv: int, cos_sin=None,
                  q_weight=None, k_weight=None, block_size: int = 64, window: int = 0, sinks: int = 0,
