@@ -1439,8 +1439,9 @@ Cut cut_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     k.sets = rows > 8 ? 1 : rows > 4 || c.head_dim == 256 ? 2 : 4;
     // Heads of 128: 32 rows a wave unpack half as often, where that still makes
     // enough workgroups (2000 tokens after 3000, 16 query and 4 key/value heads, 1000
-    // workgroups of 32 rows: 139 us, 168 with 16; half as many 88 and 87; heads of
-    // 64, with half the work in a tile, 106 either way).
+    // workgroups of 32 rows: 139 us, 168 with 16; half as many 88 and 87; 768, 1536
+    // after 2000, 82 and 94; 600, 1200 after 2000, 76 and 80, which says that fewer
+    // would do; heads of 64, with half the work in a tile, 106 either way).
     k.two = !k.many && c.head_dim == 128 && rows > 16 && (int64_t)a.B * c.kv_heads * ((rows + 31) / 32) >= 768;
     const int64_t tile = k.many ? many_rows : k.two ? 32 : 16;
     k.row_tiles = (int)((rows + tile - 1) / tile);
@@ -1472,6 +1473,13 @@ Cut cut_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     // place of splits (200 tokens after 500, 16 query and 8 key/value heads of 128:
     // 11.2 us, split 17.8; joining eight waves there costs 1 to 2 us, which
     // 30 tokens after 200 do not win back: 8.5, four waves 7.7).
+    // On both sides of the bounds, eight waves first, 16 query and 8 key/value heads:
+    // heads of 256, 8 requests of 640 tokens 12.4 and 13.8 us, of 800 14.5 and 13.9;
+    // heads of 128, one of 1050 10.5 and 11.7, of 1300 11.7 and 11.8; heads of 64, one
+    // of 1600 10.1 and 10.5, of 1900 11.3 and 10.8; ten rows a request, heads of
+    // 128, 800 tokens 11.5 and 12.9, 1000 12.8 and 11.6; heads of 64, 1100 11.0 and
+    // 11.9, 1250 11.9 and 10.5.  144 workgroups of heads of 256, 2000 tokens 26.4 and
+    // 25.5, 160 25.5 and 25.1, 192 26.2 and 30.5; 256 with 4300 tokens 53 and 62.
     k.waves = 4;
     if (!k.many && !k.two && (k.sets > 1 || k.splits > 1) && groups <= (c.head_dim == 64 ? 512 : 256) &&
         (tiles * (c.head_dim + 64) <= (k.sets > 1 ? 6800 : 5120) || (groups >= 160 && tiles <= 128))) {
