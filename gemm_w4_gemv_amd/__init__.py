@@ -555,3 +555,9 @@ from .step import *  # noqa: E402,F401,F403
 from .step import __all__ as _step_all  # noqa: E402
 
 __all__ += _step_all
+
+# The operators around a block's products (include/w4_block.h), with step.py's checks.
+from .block import *  # noqa: E402,F401,F403
+from .block import __all__ as _block_all  # noqa: E402
+
+__all__ += _block_all

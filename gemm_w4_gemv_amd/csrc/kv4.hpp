@@ -44,6 +44,9 @@ hipError_t launch_kv4_read(const w4_kv4_cache& c, const int32_t* slots, int n, v
 
 size_t kv4_attn_workspace_bytes(const w4_attn_args& a, const w4_kv4_cache& c);
 hipError_t launch_kv4_attn(const w4_attn_args& a, const w4_kv4_cache& c, void* workspace, hipStream_t stream);
+size_t kv4_attn_shared_workspace_bytes(const w4_attn_args& a, int prefix, const w4_kv4_cache& c);
+hipError_t launch_kv4_attn_shared(const w4_attn_args& a, const int32_t* prefix_table, int prefix, const w4_kv4_cache& c,
+                                  void* workspace, hipStream_t stream);
 
 size_t sample_workspace_bytes(int rows, int vocab);
 struct SampleArgs {

@@ -52,8 +52,15 @@ struct AttnArgs {
     bool in_turn;
     int window, sinks;
     float scale2;  // scale * log2(e)
-    float* part_o;   // [T * q_heads][splits][D]
-    float* part_ml;  // [T * q_heads][splits][2]
+    // A row's results from this launch go to parts part0 .. part0 + splits - 1 of
+    // its ``parts`` (1: they are the output).
+    int parts, part0;
+    float* part_o;   // [T * q_heads][parts][D]
+    float* part_ml;  // [T * q_heads][parts][2]
+    // Tiles below this one are shared by all requests and worked on once, by a
+    // launch of its own (kShared: all rows of the call are one request's, each
+    // at its own request's position; ``requests`` of them).
+    int shared_tiles, requests;
 };
 
 __device__ __forceinline__ f32x4_t mfma(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c) {
@@ -121,24 +128,62 @@ __device__ __forceinline__ Request request_of(const AttnArgs& a, int b) {
     return {q0, max(q1 - q0, 0), max(as_table(a.kv_lens)[b], 0)};
 }
 
+// The position of token t of a call in its own request; -1 if it is in none.
+__device__ __forceinline__ int position_of(const AttnArgs& a, int t) {
+    int b = t, q0 = t, q1 = t + 1;
+    if (a.q_start) {
+        const auto start = [&](int i) { return min(max(a.q_start[i], 0), a.T); };
+        int lo = 0, hi = a.requests;  // the last request that begins at t or before
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (start(mid) <= t) lo = mid; else hi = mid;
+        }
+        b = lo;
+        q0 = start(b);
+        q1 = start(b + 1);
+    }
+    if (t < q0 || t >= q1) return -1;
+    return max(max(a.kv_lens[b], 0) - (q1 - q0) + (t - q0), -1);
+}
+
 // The tiles that some of a run of rows (positions low .. high) see: those of
-// the first tokens, then those of the window.  A row that sees any token past
+// the first tokens, then those of the window; of a shared prefix only its
+// tiles, else only those behind it.  A row that sees any token past
 // the table is NaN, so of those only as far as every such row sees one: a
 // length of no sense takes no longer than the table is.
 struct Tiles {
-    int head, from, count;  // tile v of 0 .. count - 1 is v < head ? v : v - head + from
-    __device__ __forceinline__ int at(int v) const { return v < head ? v : v - head + from; }
+    int lead, head, from, count;  // tile v of 0 .. count - 1 is v < head ? v + lead : v - head + from
+    __device__ __forceinline__ int at(int v) const { return v < head ? v + lead : v - head + from; }
 };
+template <bool kShared>
 __device__ __forceinline__ Tiles tiles_of(const AttnArgs& a, int low, int high) {
-    if (high < 0) return {0, 0, 0};
-    const int past = (int)min((int64_t)a.width << a.c.shift, (int64_t)0x7FFFFFFF);
-    if (a.window == 0) return {0, 0, min(high, past) / kTile + 1};
-    const int end = min(high, max(past, high - a.window + 1)) / kTile + 1;
-    const int from = max(max(low, 0) - a.window + 1, 0) / kTile;
-    // tokens 0 .. last of the first ones (a.sinks = 0: none)
-    const int last = min(min(a.sinks - 1, high), past);
-    const int head = min(last < 0 ? 0 : last / kTile + 1, from);
-    return {head, from, head + end - from};
+    if (high < 0) return {0, 0, 0, 0};
+    const int shared = a.shared_tiles;
+    int past = (int)min((int64_t)a.width << a.c.shift, (int64_t)0x7FFFFFFF);
+    if (!kShared) past = max(past, shared * kTile);
+    Tiles x = {0, 0, 0, 0};
+    if (a.window == 0) {
+        x.count = min(high, past) / kTile + 1;
+    } else {
+        const int end = min(high, max(past, high - a.window + 1)) / kTile + 1;
+        x.from = max(max(low, 0) - a.window + 1, 0) / kTile;
+        // tokens 0 .. last of the first ones (a.sinks = 0: none)
+        const int last = min(min(a.sinks - 1, high), past);
+        x.head = min(last < 0 ? 0 : last / kTile + 1, x.from);
+        x.count = x.head + end - x.from;
+    }
+    // how many of them are below the shared ones' end
+    const int below = min(shared, x.head) + max(min(shared - x.from, x.count - x.head), 0);
+    if (kShared) {
+        x.count = below;
+        x.head = min(x.head, below);
+    } else {
+        x.lead = min(below, x.head);
+        x.from += below - x.lead;
+        x.head -= x.lead;
+        x.count -= below;
+    }
+    return x;
 }
 
 template <int D>
@@ -288,12 +333,17 @@ struct Rows {
     u32x4_t pop[2][kNB][kG];  // p s of the tile and what its rounding left, the second product's operands
 
     // Sends for the queries of rows r0 ..; past the last row that one again, unseen.
+    template <bool kShared>
     __device__ __forceinline__ void fetch(const AttnArgs& a, const Request& req, int head, int r0, int rows, int lane) {
         const int c = lane & 15, g = lane >> 4, first_pos = req.kv - req.rows;
 #pragma unroll
         for (int n = 0; n < kNB; ++n) {
             const int mine = r0 + 16 * n + c, r = min(mine, rows - 1);
-            pos[n] = mine < rows ? max(first_pos + r / a.g, -1) : -1;
+            if constexpr (kShared) {
+                pos[n] = mine < rows ? position_of(a, r / a.g) : -1;
+            } else {
+                pos[n] = mine < rows ? max(first_pos + r / a.g, -1) : -1;
+            }
             const uint16_t* src = a.q + (int64_t)(req.first + r / a.g) * a.q_stride + (size_t)(head * a.g + r % a.g) * D;
 #pragma unroll
             for (int q = 0; q < kG; ++q)
@@ -301,6 +351,23 @@ struct Rows {
                 for (int i = 0; i < kW; ++i)
                     xq[n][q][i] = *reinterpret_cast<const u32x4_t*>(src + q * W4_KV4_GROUP + (kW * g + i) * 8);
         }
+    }
+
+    // The first and last position of the wave's rows (a shared prefix's rows are in no order).
+    __device__ __forceinline__ void reach(int* low, int* high) const {
+        int lo = pos[0], hi = pos[0];
+#pragma unroll
+        for (int n = 1; n < kNB; ++n) {
+            lo = min(lo, pos[n]);
+            hi = max(hi, pos[n]);
+        }
+#pragma unroll
+        for (int x = 1; x < 16; x <<= 1) {
+            lo = min(lo, __shfl_xor(lo, x));
+            hi = max(hi, __shfl_xor(hi, x));
+        }
+        *low = (int)sgpr((uint32_t)lo);
+        *high = (int)sgpr((uint32_t)hi);
     }
 
     // The queries as the score product's operand, their sums; empty outputs.
@@ -518,7 +585,8 @@ struct Rows {
 #pragma unroll
         for (int n = 0; n < kNB; ++n) {
             l[n] = row_sum(l[n]);
-            if (a.width <= 0 && pos[n] >= 0) l[n] = NAN;  // no table: what the row sees lies past it
+            // no table: what the row sees (of its own tokens) lies past it
+            if (a.width <= 0 && pos[n] >= a.shared_tiles * kTile) l[n] = NAN;
 #pragma unroll
             for (int q = 0; q < kG; ++q) {
                 const float e = row_sum(extra[n][q]);
@@ -544,7 +612,7 @@ struct Rows {
             const int row = r0 + 16 * n + c;
             if (row >= rows) continue;
             const int t = req.first + row / a.g, h = head * a.g + row % a.g;
-            if (a.splits == 1) {
+            if (a.parts == 1) {
                 const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
                 uint16_t* dst = a.out + (int64_t)t * a.out_stride + (size_t)h * D;
 #pragma unroll
@@ -562,7 +630,7 @@ struct Rows {
                         }
                     }
             } else {
-                const size_t at = ((size_t)t * a.g * a.c.heads + h) * a.splits + split;
+                const size_t at = ((size_t)t * a.g * a.c.heads + h) * a.parts + a.part0 + split;
                 if (g == 0) {
                     a.part_ml[2 * at] = m[n];
                     a.part_ml[2 * at + 1] = l[n];
@@ -619,7 +687,7 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a) {
 }
 
 // Few rows: the waves take a row tile's token tiles in turn.
-template <int D, int kNB, int kWaves, bool kWide>
+template <int D, int kNB, int kWaves, bool kWide, bool kShared = false>
 __global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
     typedef Rows<D, kNB> R;
     constexpr int kG = R::kG, kJ = R::kJ, kCols = 16 * kNB;
@@ -630,13 +698,16 @@ __global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
     const int c = lane & 15, g = lane >> 4;
     const Share mine = share_of(a);
     const int head = mine.head;
-    const Request req = request_of(a, mine.b);
-    const int rows = min(req.rows, a.max_q) * a.g;  // < 2^31: checked on the host
+    const Request req = kShared ? Request{0, a.T, 0} : request_of(a, mine.b);
+    const int rows = (kShared ? a.T : min(req.rows, a.max_q)) * a.g;  // < 2^31: checked on the host
     const int r0 = mine.row_tile * kCols;
     if (r0 >= rows) return;
     const int first_pos = req.kv - req.rows;
-    const int low = first_pos + r0 / a.g, high = first_pos + (min(r0 + kCols, rows) - 1) / a.g;
-    const Tiles tiles = tiles_of(a, low, high);
+    int low = first_pos + r0 / a.g, high = first_pos + (min(r0 + kCols, rows) - 1) / a.g;
+    R rw;
+    rw.template fetch<kShared>(a, req, head, r0, rows, lane);
+    if constexpr (kShared) rw.reach(&low, &high);
+    const Tiles tiles = tiles_of<kShared>(a, low, high);
     const table_ptr table = as_table(a.table + (size_t)mine.b * a.width);
 
     // this split's tiles, in turn over the waves
@@ -646,8 +717,6 @@ __global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
     const bool any = v < v1 && a.width > 0;
     const auto clamped = [&](int x) { return x < v1 ? x : v1 - 1; };
 
-    R rw;
-    rw.fetch(a, req, head, r0, rows, lane);
     const Offsets offs = offsets_of<D>(lane);
     Frag<D> f;
     int page[2] = {-1, -1};
@@ -829,7 +898,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void kv4_attn_sets_kernel(AttnAr
     if (rows <= 0) return;
     const int first_pos = req.kv - req.rows;
     const int low = first_pos, high = first_pos + (rows - 1) / a.g;
-    const Tiles tiles = tiles_of(a, low, high);
+    const Tiles tiles = tiles_of<false>(a, low, high);
     const table_ptr table = as_table(a.table + (size_t)mine.b * a.width);
 
     // this split's tiles, kT at a time in turn over the waves
@@ -1092,7 +1161,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void kv4_attn_sets_kernel(AttnAr
     // The sets of a wave: common maximum, sums, a part of the outputs for each lane.
     constexpr int kBit = 8;
     l = row_sum(l);
-    if (a.width <= 0 && pos >= 0) l = NAN;  // no table: what the row sees lies past it
+    if (a.width <= 0 && pos >= a.shared_tiles * kTile) l = NAN;  // no table: what the row sees lies past it
     const float top = over_sets<kBit, kCols>(m, [](float x, float y) { return fmaxf(x, y); });
     const float scale = l == 0.0f ? 0.0f : m == -INFINITY ? NAN : __builtin_amdgcn_exp2f((m - top) * a.scale2);
     l = over_sets<kBit, kCols>(l == 0.0f ? 0.0f : l * scale, [](float x, float y) { return x + y; });
@@ -1140,7 +1209,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void kv4_attn_sets_kernel(AttnAr
     const int at = set * kMine + wave * kEnd;  // (q, r, j) as one number
     const int d = Rows<D, 1>::place(at / kJ / 4, at / kJ % 4, g) + at % kJ;
     const int t = req.first + row / a.g, h = head * a.g + row % a.g;
-    if (a.splits == 1) {
+    if (a.parts == 1) {
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         uint16_t* dst = a.out + (int64_t)t * a.out_stride + (size_t)h * D + d;
         if constexpr (kEnd % 2 == 0) {
@@ -1150,7 +1219,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void kv4_attn_sets_kernel(AttnAr
             dst[0] = f32_to_bf16(end[0] * inv);
         }
     } else {
-        const size_t part = ((size_t)t * a.g * a.c.heads + h) * a.splits + mine.split;
+        const size_t part = ((size_t)t * a.g * a.c.heads + h) * a.parts + a.part0 + mine.split;
         if (g == 0 && wave == 0 && set == 0) {
             a.part_ml[2 * part] = now_top;
             a.part_ml[2 * part + 1] = sum;
@@ -1177,7 +1246,8 @@ __device__ __forceinline__ void lds_barrier() {
 // Heads of 64 fit three waves a SIMD, with two operands of the values read ahead
 // in place of four where a tile is one page (eight prompts of 1000 tokens, 32 query
 // and 8 key/value heads: 106 us, 124 with 173 registers and two waves).
-template <int D, int kNB, bool kWide>
+// A shared prefix's tiles may be split over workgroups.
+template <int D, int kNB, bool kWide, bool kShared = false>
 __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv4_attn_many_kernel(AttnArgs a) {
     typedef Rows<D, kNB> R;
     constexpr int kWaves = 4, kG = R::kG, kW = R::kW, kJ = R::kJ, kCols = 16 * kNB;
@@ -1190,24 +1260,43 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv4_attn_many_kernel(Att
     const int c = lane & 15, g = lane >> 4;
     const Share mine = share_of(a);
     const int head = mine.head;
-    const Request req = request_of(a, mine.b);
-    const int rows = min(req.rows, a.max_q) * a.g;
+    const Request req = kShared ? Request{0, a.T, 0} : request_of(a, mine.b);
+    const int rows = (kShared ? a.T : min(req.rows, a.max_q)) * a.g;
     const int base = mine.row_tile * kWaves * kCols;
     if (base >= rows) return;
     const int first_pos = req.kv - req.rows;
-    const int high = first_pos + (min(base + kWaves * kCols, rows) - 1) / a.g;
-    const Tiles tiles = tiles_of(a, first_pos + base / a.g, high);
-    const table_ptr table = as_table(a.table + (size_t)mine.b * a.width);
+    int low = first_pos + base / a.g, high = first_pos + (min(base + kWaves * kCols, rows) - 1) / a.g;
     // this wave's rows; past the last there may be none
     const int r0 = min(base + wave * kCols, rows);
-    const int my_low = first_pos + min(r0, rows - 1) / a.g, my_high = first_pos + (min(r0 + kCols, rows) - 1) / a.g;
+    int my_low = first_pos + min(r0, rows - 1) / a.g, my_high = first_pos + (min(r0 + kCols, rows) - 1) / a.g;
+    R rw;
+    rw.template fetch<kShared>(a, req, head, r0, rows, lane);
+    if constexpr (kShared) {
+        __shared__ int reach[kWaves][2];
+        rw.reach(&my_low, &my_high);
+        if (lane == 0) {
+            reach[wave][0] = r0 < rows ? my_low : 0x7FFFFFFF;
+            reach[wave][1] = my_high;
+        }
+        __syncthreads();
+        low = reach[0][0];
+        high = reach[0][1];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) {
+            low = min(low, reach[w][0]);
+            high = max(high, reach[w][1]);
+        }
+        low = (int)sgpr((uint32_t)low);
+        high = (int)sgpr((uint32_t)high);
+    }
+    const Tiles tiles = tiles_of<kShared>(a, low, high);
+    const table_ptr table = as_table(a.table + (size_t)mine.b * a.width);
 
-    int v = 0;
-    const int v1 = a.width <= 0 ? 0 : tiles.count;
+    const int per = kShared ? (tiles.count + a.splits - 1) / a.splits : tiles.count;
+    int v = kShared ? mine.split * per : 0;
+    const int v1 = a.width <= 0 ? 0 : kShared ? min(tiles.count, v + per) : tiles.count;
     const auto tile_at = [&](int x) { return tiles.at(max(min(x, v1 - 1), 0)) * kTile; };
 
-    R rw;
-    rw.fetch(a, req, head, r0, rows, lane);
     const Offsets offs = offsets_of<D>(lane);
     const uint32_t bias = vgpr_const(kInt4BiasPair);
 
@@ -1327,7 +1416,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv4_attn_many_kernel(Att
         lds_barrier();
     }
     rw.finish(a);
-    if (r0 < rows) rw.store(a, req, head, 0, r0, rows, lane);
+    if (r0 < rows) rw.store(a, req, head, kShared ? mine.split : 0, r0, rows, lane);
 }
 
 // Joins the splits of one row, a workgroup a row: D / 4 lanes hold its values,
@@ -1347,14 +1436,14 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_join_kernel(AttnArgs a) {
     const Request req = request_of(a, b);
     if (i >= req.rows) return;
     const int t = req.first + i;
-    const size_t at = ((size_t)t * heads + h) * a.splits;
+    const size_t at = ((size_t)t * heads + h) * a.parts;
     if (tid < kWave) {
         float ms[kMaxSplits / kWave], ls[kMaxSplits / kWave], now = -INFINITY, sum = 0;
 #pragma unroll
         for (int u = 0; u < kMaxSplits / kWave; ++u) {
             const int s = u * kWave + lane;
-            ms[u] = s < a.splits ? a.part_ml[2 * (at + s)] : -INFINITY;
-            ls[u] = s < a.splits ? a.part_ml[2 * (at + s) + 1] : 0.0f;
+            ms[u] = s < a.parts ? a.part_ml[2 * (at + s)] : -INFINITY;
+            ls[u] = s < a.parts ? a.part_ml[2 * (at + s) + 1] : 0.0f;
             now = fmaxf(now, ms[u]);
         }
 #pragma unroll
@@ -1374,7 +1463,7 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_join_kernel(AttnArgs a) {
     const int li = tid % kLanes;
     f32x4_t v = {0, 0, 0, 0};
 #pragma unroll 8
-    for (int s = tid / kLanes; s < a.splits; s += kAtOnce) {
+    for (int s = tid / kLanes; s < a.parts; s += kAtOnce) {
         const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part_o + (at + s) * D + 4 * li);
         const float w = weight[s];
 #pragma unroll
@@ -1514,7 +1603,7 @@ hipError_t launch_d(const AttnArgs& k, const Cut& cut, int64_t groups, hipStream
         kv4_attn_kernel<D, 1, 4, kWide><<<grid, block, 0, stream>>>(k);
     }
     const hipError_t err = hipGetLastError();
-    if (err != hipSuccess || k.splits == 1) return err;
+    if (err != hipSuccess || k.parts == 1) return err;
     const int64_t units = (int64_t)k.B * k.max_q * k.g * k.c.heads;
     kv4_attn_join_kernel<D><<<dim3((unsigned)units), dim3(kThreads), 0, stream>>>(k);
     return hipGetLastError();
@@ -1525,15 +1614,7 @@ hipError_t launch_w(const AttnArgs& k, const Cut& cut, int64_t groups, hipStream
     return k.c.shift >= 5 ? launch_d<D, true>(k, cut, groups, stream) : launch_d<D, false>(k, cut, groups, stream);
 }
 
-}  // namespace
-
-size_t kv4_attn_workspace_bytes(const w4_attn_args& a, const w4_kv4_cache& c) {
-    const int splits = cut_of(a, c).splits;
-    if (splits == 1) return 0;
-    return (size_t)a.T * a.q_heads * splits * (c.head_dim + 2) * sizeof(float);
-}
-
-hipError_t launch_kv4_attn(const w4_attn_args& a, const w4_kv4_cache& c, void* workspace, hipStream_t stream) {
+AttnArgs args_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     AttnArgs k = {};
     k.q = static_cast<const uint16_t*>(a.q);
     k.out = static_cast<uint16_t*>(a.out);
@@ -1548,23 +1629,131 @@ hipError_t launch_kv4_attn(const w4_attn_args& a, const w4_kv4_cache& c, void* w
     k.g = a.q_heads / c.kv_heads;
     k.width = a.max_blocks;
     k.max_q = a.max_q;
-    const Cut cut = cut_of(a, c);
-    k.row_tiles = cut.row_tiles;
-    k.splits = cut.splits;
-    k.in_turn = cut.many && (int64_t)a.B * c.kv_heads * k.row_tiles * k.splits <= 512;
     k.window = a.window;
     k.sinks = a.sinks;
     k.scale2 = a.scale * 1.4426950408889634f;
-    if (k.splits > 1) {
-        k.part_o = static_cast<float*>(workspace);
-        k.part_ml = k.part_o + (size_t)a.T * a.q_heads * k.splits * c.head_dim;
-    }
+    return k;
+}
+
+size_t part_bytes(const w4_attn_args& a, const w4_kv4_cache& c, int parts) {
+    return (size_t)a.T * a.q_heads * parts * (c.head_dim + 2) * sizeof(float);
+}
+void set_parts(AttnArgs& k, const w4_attn_args& a, const w4_kv4_cache& c, void* workspace, int parts) {
+    k.parts = parts;
+    if (parts == 1) return;
+    k.part_o = static_cast<float*>(workspace);
+    k.part_ml = k.part_o + (size_t)a.T * a.q_heads * parts * c.head_dim;
+}
+
+// The arguments as the cut of each request's own tokens wants them.
+w4_attn_args behind(const w4_attn_args& a, int tiles) {
+    w4_attn_args x = a;
+    x.max_kv = a.max_kv > tiles * kTile ? a.max_kv - tiles * kTile : 0;
+    return x;
+}
+
+// Each request's tokens from tile ``tiles`` on; what is before that has left ``before`` parts.
+hipError_t launch_own(const w4_attn_args& a, const w4_kv4_cache& c, void* workspace, int tiles, int before,
+                      hipStream_t stream) {
+    AttnArgs k = args_of(a, c);
+    const Cut cut = cut_of(behind(a, tiles), c);
+    k.row_tiles = cut.row_tiles;
+    k.splits = cut.splits;
+    k.in_turn = cut.many && (int64_t)a.B * c.kv_heads * k.row_tiles * k.splits <= 512;
+    k.shared_tiles = tiles;
+    k.part0 = before;
+    set_parts(k, a, c, workspace, before + cut.splits);
     const int64_t groups = (int64_t)a.B * c.kv_heads * k.row_tiles * k.splits;
     switch (c.head_dim) {
         case 64: return launch_w<64>(k, cut, groups, stream);
         case 128: return launch_w<128>(k, cut, groups, stream);
         default: return launch_w<256>(k, cut, groups, stream);
     }
+}
+
+// How the tiles that all requests share are cut.
+struct SharedCut {
+    int tiles;   // whole tiles of the prefix; the rest of it is done with each request's own tokens
+    int splits;  // workgroups that share a row tile's tokens; 0: nothing is done apart
+    bool many;   // kv4_attn_many_kernel
+    int row_tiles;
+    Cut own;     // of the tokens behind
+};
+SharedCut shared_cut_of(const w4_attn_args& a, int prefix, const w4_kv4_cache& c) {
+    SharedCut k = {};
+    k.tiles = prefix / kTile;
+    if (k.tiles == 0 || a.T < 2) return k;
+    // a join workgroup a row of every request
+    if ((int64_t)a.B * a.max_q * a.q_heads > (1 << 23) || (int64_t)a.T * a.q_heads > (1 << 23)) return k;
+    k.own = cut_of(behind(a, k.tiles), c);
+    const int64_t rows = (int64_t)a.T * (a.q_heads / c.kv_heads);
+    const int64_t many_rows = 64 * many_blocks(c.head_dim);
+    k.many = rows > many_rows / 2;
+    const int64_t tile = k.many ? many_rows : 16;
+    k.row_tiles = (int)((rows + tile - 1) / tile);
+    const int64_t groups = (int64_t)c.kv_heads * k.row_tiles;
+    int64_t want = 512 / groups;
+    const int64_t most = k.many ? k.tiles / 2 : k.tiles / (2 * kFewWaves);
+    want = want < most ? want : most;
+    if (want > kMaxSplits - k.own.splits) want = kMaxSplits - k.own.splits;
+    k.splits = (int)(want < 1 ? 1 : want);
+    if (k.own.splits + k.splits > kMaxSplits) k.splits = 0;
+    return k;
+}
+
+template <int D>
+hipError_t launch_shared(const AttnArgs& k, const SharedCut& cut, dim3 grid, hipStream_t stream) {
+    const auto launch = [&](auto wide) {
+        constexpr bool kWide = decltype(wide)::value;
+        if (cut.many) {
+            kv4_attn_many_kernel<D, many_blocks(D), kWide, true><<<grid, dim3(256), 0, stream>>>(k);
+        } else {
+            kv4_attn_kernel<D, 1, kFewWaves, kWide, true><<<grid, dim3(256), 0, stream>>>(k);
+        }
+        return hipGetLastError();
+    };
+    return k.c.shift >= 5 ? launch(std::true_type{}) : launch(std::false_type{});
+}
+
+}  // namespace
+
+size_t kv4_attn_workspace_bytes(const w4_attn_args& a, const w4_kv4_cache& c) {
+    const int splits = cut_of(a, c).splits;
+    if (splits == 1) return 0;
+    return part_bytes(a, c, splits);
+}
+
+hipError_t launch_kv4_attn(const w4_attn_args& a, const w4_kv4_cache& c, void* workspace, hipStream_t stream) {
+    return launch_own(a, c, workspace, 0, 0, stream);
+}
+
+size_t kv4_attn_shared_workspace_bytes(const w4_attn_args& a, int prefix, const w4_kv4_cache& c) {
+    const SharedCut cut = shared_cut_of(a, prefix, c);
+    return cut.splits == 0 ? kv4_attn_workspace_bytes(a, c) : part_bytes(a, c, cut.splits + cut.own.splits);
+}
+
+hipError_t launch_kv4_attn_shared(const w4_attn_args& a, const int32_t* prefix_table, int prefix, const w4_kv4_cache& c,
+                                  void* workspace, hipStream_t stream) {
+    const SharedCut cut = shared_cut_of(a, prefix, c);
+    if (cut.splits == 0) return launch_kv4_attn(a, c, workspace, stream);
+    AttnArgs k = args_of(a, c);
+    k.table = prefix_table;
+    k.width = (prefix + c.block_size - 1) / c.block_size;
+    k.requests = a.B;
+    k.B = 1;
+    k.row_tiles = cut.row_tiles;
+    k.splits = cut.splits;
+    k.shared_tiles = cut.tiles;
+    set_parts(k, a, c, workspace, cut.splits + cut.own.splits);
+    const dim3 grid((unsigned)((int64_t)c.kv_heads * cut.row_tiles * cut.splits));
+    hipError_t err;
+    switch (c.head_dim) {
+        case 64: err = launch_shared<64>(k, cut, grid, stream); break;
+        case 128: err = launch_shared<128>(k, cut, grid, stream); break;
+        default: err = launch_shared<256>(k, cut, grid, stream); break;
+    }
+    if (err != hipSuccess) return err;
+    return launch_own(a, c, workspace, cut.tiles, cut.splits, stream);
 }
 
 }  // namespace w4

@@ -1,0 +1,176 @@
+// Tokens sorted by expert.
+//
+//   row(i) = start[e] + #{i' < i : expert(i') = e},  start[e] = sum over e' < e of min(count(e'), capacity)
+//
+// A counting sort: nothing is compared but a workgroup's own few choices.  A
+// workgroup takes a few tokens, finds the rows of their choices and copies the
+// tokens there, reading each once.  What it needs of all other choices are two
+// numbers an expert, how many there are and how many come before; it counts
+// them itself in LDS where they are few, which takes one launch, else from a
+// table of counts per chunk of choices that a first launch makes.  The counts
+// are whole numbers, so LDS atomics do not decide any order.
+#include "block.hpp"
+#include "w4_device.hpp"
+
+namespace w4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxE = W4_MOE_SORT_MAX_EXPERTS;
+constexpr int kOwn = 64;      // choices of a workgroup, at most
+constexpr int kAlone = 4096;  // choices that every workgroup counts itself
+constexpr int kTable = 16384; // counts of the table, at most
+
+struct SortArgs {
+    w4_moe_sort_args a;
+    int n;         // choices
+    int per;       // tokens of a workgroup
+    int chunk;     // choices of a chunk; 0: no table
+    int chunks;
+    int32_t* counts;  // [chunks][num_experts]
+};
+
+__global__ __launch_bounds__(kThreads) void moe_count_kernel(SortArgs k) {
+    __shared__ int hist[kMaxE];
+    const int E = k.a.num_experts;
+    for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
+    __syncthreads();
+    const int first = blockIdx.x * k.chunk, end = min(first + k.chunk, k.n);
+    for (int i = first + threadIdx.x; i < end; i += kThreads) {
+        const int e = k.a.experts[i];
+        if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kThreads) k.counts[blockIdx.x * E + e] = hist[e];
+}
+
+__global__ __launch_bounds__(kThreads) void moe_sort_kernel(SortArgs k) {
+    __shared__ int total[kMaxE + 1], before[kMaxE], sums[kThreads / kWave], rows[kOwn];
+    const w4_moe_sort_args& a = k.a;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, E = a.num_experts;
+    const int t0 = blockIdx.x * k.per, t1 = min(t0 + k.per, a.T);
+    const int i0 = t0 * a.top, i1 = t1 * a.top;
+    for (int e = tid; e < E; e += kThreads) total[e] = before[e] = 0;
+    __syncthreads();
+    int from = 0, to = k.n;  // the choices counted one by one
+    if (k.chunk) {
+        const int mine = i0 / k.chunk;
+        for (int i = tid; i < k.chunks * E; i += kThreads) {
+            const int c = k.counts[i], e = i % E;
+            if (c == 0) continue;
+            atomicAdd(&total[e], c);
+            if (i / E < mine) atomicAdd(&before[e], c);
+        }
+        from = mine * k.chunk;
+        to = i0;
+    }
+    for (int i = from + tid; i < to; i += kThreads) {
+        const int e = a.experts[i];
+        if ((unsigned)e >= (unsigned)E) continue;
+        if (!k.chunk) atomicAdd(&total[e], 1);
+        if (i < i0) atomicAdd(&before[e], 1);
+    }
+    __syncthreads();
+
+    // first rows: a scan over the experts, kMaxE / kThreads of them a thread
+    constexpr int kPer = kMaxE / kThreads;
+    int mine[kPer], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int e = tid * kPer + j;
+        const int c = e < E ? total[e] : 0;
+        mine[j] = a.capacity > 0 ? min(c, a.capacity) : c;
+        sum += mine[j];
+    }
+    int upto = sum;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+        const int x = __shfl_up(upto, off);
+        if (lane >= off) upto += x;
+    }
+    if (lane == kWave - 1) sums[wave] = upto;
+    __syncthreads();
+    int start = upto - sum;
+    for (int w = 0; w < wave; ++w) start += sums[w];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int e = tid * kPer + j;
+        if (e <= E) total[e] = start;
+        start += mine[j];
+    }
+    if (tid == kThreads - 1 && E == kMaxE) total[E] = start;
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int e = tid; e <= E; e += kThreads) a.row_start[e] = total[e];
+
+    // the workgroup's own choices, a lane each
+    if (tid < kOwn) {
+        const int i = i0 + tid;
+        const int e = i < i1 ? a.experts[i] : -1;
+        int rank = 0;
+        for (int l = 0; l < i1 - i0; ++l) rank += l < lane && __builtin_amdgcn_readlane(e, l) == e;
+        int row = -1;
+        if ((unsigned)e < (unsigned)E) {
+            rank += before[e];
+            if (a.capacity == 0 || rank < a.capacity) row = total[e] + rank;
+        }
+        rows[tid] = row;
+        if (i < i1) {
+            a.row_of[i] = row;
+            if (a.source) {
+                if (row >= 0) a.source[row] = i;
+                if (i >= total[E]) a.source[i] = -1;  // no choice has this row
+            }
+        }
+    }
+    if (!a.x) return;
+    __syncthreads();
+    const uint16_t* x = static_cast<const uint16_t*>(a.x);
+    uint16_t* out = static_cast<uint16_t*>(a.rows);
+    const int pieces = a.D / 8;
+    for (int t = t0; t < t1; ++t)
+        for (int p = tid; p < pieces; p += kThreads) {
+            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + (int64_t)t * a.x_stride + 8 * p);
+            for (int j = 0; j < a.top; ++j) {
+                const int row = rows[(t - t0) * a.top + j];
+                if ((unsigned)row < (unsigned)a.R)
+                    *reinterpret_cast<u32x4_t*>(out + (int64_t)row * a.rows_stride + 8 * p) = v;
+            }
+        }
+}
+
+SortArgs cut_of(int T, int top, int E) {
+    SortArgs k = {};
+    k.n = T * top;
+    k.per = k.n <= kAlone ? 1 : kOwn / top;
+    if (k.n > kAlone) {
+        const int most = kTable / E;  // 16 chunks or more
+        k.chunk = (k.n + most - 1) / most;
+        if (k.chunk < 1024) k.chunk = 1024;
+        k.chunk = (k.chunk + k.per * top - 1) / (k.per * top) * (k.per * top);  // a workgroup's choices lie in one
+        k.chunks = (k.n + k.chunk - 1) / k.chunk;
+    }
+    return k;
+}
+
+}  // namespace
+
+size_t moe_sort_workspace_bytes(int T, int top, int num_experts) {
+    return (size_t)cut_of(T, top, num_experts).chunks * num_experts * sizeof(int32_t);
+}
+
+hipError_t launch_moe_sort(const w4_moe_sort_args& a, void* workspace, hipStream_t stream) {
+    SortArgs k = cut_of(a.T, a.top, a.num_experts);
+    k.a = a;
+    k.counts = static_cast<int32_t*>(workspace);
+    if (k.chunk) {
+        moe_count_kernel<<<dim3((unsigned)k.chunks), dim3(kThreads), 0, stream>>>(k);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    const int groups = a.T > 0 ? (a.T + k.per - 1) / k.per : 1;
+    moe_sort_kernel<<<dim3((unsigned)groups), dim3(kThreads), 0, stream>>>(k);
+    return hipGetLastError();
+}
+
+}  // namespace w4

@@ -3,8 +3,6 @@
 // array without elements may have no address.
 #include <math.h>
 
-#include <initializer_list>
-
 #include "kv4.hpp"
 #include "w4_check.hpp"
 #include "w4_step.h"
@@ -12,29 +10,13 @@
 namespace {
 
 using w4::aligned;
+using w4::any_overlap;
 using w4::fail;
 using w4::hip_fail;
 using w4::overlap;
 using w4::Range;
 using w4::range;
-
-bool any_overlap(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
-    for (const Range& o : outs)
-        for (const Range& i : ins)
-            if (overlap(o, i)) return true;
-    return false;
-}
-bool any_overlap(std::initializer_list<Range> outs) {
-    for (const Range& a : outs)
-        for (const Range& b : outs)
-            if (&a != &b && overlap(a, b)) return true;
-    return false;
-}
-
-// Bytes from the first to past the last value of ``rows`` rows of ``wide`` BF16.
-Range rows_range(const void* p, int64_t rows, int64_t stride, int64_t wide) {
-    return range(p, p && rows > 0 ? ((size_t)(rows - 1) * (size_t)stride + (size_t)wide) * 2 : 0);
-}
+using w4::rows_range;
 
 bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
 
@@ -86,6 +68,55 @@ w4_status check_attn_shape(const char* fn, const w4_attn_args* a, const w4_kv4_c
         return fail(W4_ERR_SHAPE, "%s: %d requests of %d rows of %d heads are too many for one call", fn, a->B, a->max_q,
                     a->q_heads);
     return W4_OK;
+}
+
+size_t workspace_for(const char* fn, const w4_attn_args* args, int prefix, const w4_kv4_cache* cache) {
+    if (check_attn_shape(fn, args, cache) != W4_OK) return 0;
+    if (args->T == 0 || args->B == 0 || args->max_q == 0) return 0;
+    return w4::kv4_attn_shared_workspace_bytes(*args, prefix, *cache);
+}
+
+// w4_kv4_attn, and with shared tokens w4_kv4_attn_shared.
+w4_status attend(const char* fn, const w4_attn_args* args, const int32_t* prefix_table, int prefix,
+                 const w4_kv4_cache* cache, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!args) return fail(W4_ERR_NULL, "%s: args must not be NULL", fn);
+    w4_status st = check_cache(fn, cache);
+    if (st != W4_OK) return st;
+    st = check_attn_shape(fn, args, cache);
+    if (st != W4_OK) return st;
+    const w4_attn_args& a = *args;
+    if ((a.T > 0 && (!a.q || !a.out)) || (a.B > 0 && !a.kv_lens))
+        return fail(W4_ERR_NULL, "%s: q, out and kv_lens must not be NULL", fn);
+    if (a.max_blocks < 0) return fail(W4_ERR_SHAPE, "%s: max_blocks = %d is negative", fn, a.max_blocks);
+    if (a.B > 0 && a.max_blocks > 0 && !a.block_table) return fail(W4_ERR_NULL, "%s: block_table must not be NULL", fn);
+    if (prefix < 0) return fail(W4_ERR_SHAPE, "%s: prefix = %d is negative", fn, prefix);
+    if (prefix > 0 && !prefix_table) return fail(W4_ERR_NULL, "%s: prefix_table must not be NULL", fn);
+    if (!a.q_start && a.T != a.B) return fail(W4_ERR_SHAPE, "%s: without q_start T = %d must be B = %d", fn, a.T, a.B);
+    if (!(a.scale > 0.0f) || !isfinite(a.scale)) return fail(W4_ERR_ARG, "%s: scale must be positive and finite", fn);
+    const int64_t wide = (int64_t)a.q_heads * cache->head_dim;
+    for (int64_t s : {a.q_stride, a.out_stride})
+        if (s < wide || s % 8 || s > (1ll << 40))
+            return fail(W4_ERR_ARG, "%s: row strides must be multiples of 8, at least q_heads * head_dim", fn);
+    if (!aligned(a.q, 16) || !aligned(a.out, 16)) return fail(W4_ERR_ALIGN, "%s: q and out must be 16-byte aligned", fn);
+    if (!aligned(a.block_table, 4) || !aligned(a.kv_lens, 4) || !aligned(a.q_start, 4) || !aligned(prefix_table, 4))
+        return fail(W4_ERR_ALIGN, "%s: block tables, kv_lens and q_start must be 4-byte aligned", fn);
+    const size_t need = workspace_for(fn, args, prefix, cache);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return fail(W4_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given%s", fn, need, workspace_bytes,
+                        workspace ? "" : " (NULL)");
+        if (!aligned(workspace, 16)) return fail(W4_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+    }
+    const Range q = rows_range(a.q, a.T, a.q_stride, wide), o = rows_range(a.out, a.T, a.out_stride, wide);
+    const Range w = range(workspace, need), t = range(a.block_table, (size_t)a.B * a.max_blocks * 4),
+                l = range(a.kv_lens, (size_t)a.B * 4), s = range(a.q_start, a.q_start ? ((size_t)a.B + 1) * 4 : 0),
+                p = range(prefix_table, ((size_t)prefix + cache->block_size - 1) / cache->block_size * 4);
+    const CacheRanges c = ranges_of(*cache);
+    if (any_overlap({o, w}, {q, t, l, s, p, c.k, c.km, c.v, c.vm}) || overlap(o, w))
+        return fail(W4_ERR_ALIAS, "%s: out or workspace overlaps an input or each other", fn);
+    if (a.T == 0 || a.B == 0 || a.max_q == 0) return W4_OK;
+    const hipError_t err = w4::launch_kv4_attn_shared(a, prefix_table, prefix, *cache, workspace, static_cast<hipStream_t>(stream));
+    return err == hipSuccess ? W4_OK : hip_fail(err, fn);
 }
 
 }  // namespace
@@ -226,49 +257,22 @@ W4_API w4_status w4_kv4_read(const w4_kv4_cache* cache, const int32_t* slots, in
 }
 
 W4_API size_t w4_kv4_attn_workspace_bytes(const w4_attn_args* args, const w4_kv4_cache* cache) {
-    if (check_attn_shape("w4_kv4_attn_workspace_bytes", args, cache) != W4_OK) return 0;
-    if (args->T == 0 || args->B == 0 || args->max_q == 0) return 0;
-    return w4::kv4_attn_workspace_bytes(*args, *cache);
+    return workspace_for("w4_kv4_attn_workspace_bytes", args, 0, cache);
 }
 
 W4_API w4_status w4_kv4_attn(const w4_attn_args* args, const w4_kv4_cache* cache, void* workspace,
                              size_t workspace_bytes, void* stream) {
-    const char* fn = "w4_kv4_attn";
-    if (!args) return fail(W4_ERR_NULL, "%s: args must not be NULL", fn);
-    w4_status st = check_cache(fn, cache);
-    if (st != W4_OK) return st;
-    st = check_attn_shape(fn, args, cache);
-    if (st != W4_OK) return st;
-    const w4_attn_args& a = *args;
-    if ((a.T > 0 && (!a.q || !a.out)) || (a.B > 0 && !a.kv_lens))
-        return fail(W4_ERR_NULL, "%s: q, out and kv_lens must not be NULL", fn);
-    if (a.max_blocks < 0) return fail(W4_ERR_SHAPE, "%s: max_blocks = %d is negative", fn, a.max_blocks);
-    if (a.B > 0 && a.max_blocks > 0 && !a.block_table) return fail(W4_ERR_NULL, "%s: block_table must not be NULL", fn);
-    if (!a.q_start && a.T != a.B) return fail(W4_ERR_SHAPE, "%s: without q_start T = %d must be B = %d", fn, a.T, a.B);
-    if (!(a.scale > 0.0f) || !isfinite(a.scale)) return fail(W4_ERR_ARG, "%s: scale must be positive and finite", fn);
-    const int64_t wide = (int64_t)a.q_heads * cache->head_dim;
-    for (int64_t s : {a.q_stride, a.out_stride})
-        if (s < wide || s % 8 || s > (1ll << 40))
-            return fail(W4_ERR_ARG, "%s: row strides must be multiples of 8, at least q_heads * head_dim", fn);
-    if (!aligned(a.q, 16) || !aligned(a.out, 16)) return fail(W4_ERR_ALIGN, "%s: q and out must be 16-byte aligned", fn);
-    if (!aligned(a.block_table, 4) || !aligned(a.kv_lens, 4) || !aligned(a.q_start, 4))
-        return fail(W4_ERR_ALIGN, "%s: block_table, kv_lens and q_start must be 4-byte aligned", fn);
-    const size_t need = w4_kv4_attn_workspace_bytes(args, cache);
-    if (need > 0) {
-        if (!workspace || workspace_bytes < need)
-            return fail(W4_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given%s", fn, need, workspace_bytes,
-                        workspace ? "" : " (NULL)");
-        if (!aligned(workspace, 16)) return fail(W4_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
-    }
-    const Range q = rows_range(a.q, a.T, a.q_stride, wide), o = rows_range(a.out, a.T, a.out_stride, wide);
-    const Range w = range(workspace, need), t = range(a.block_table, (size_t)a.B * a.max_blocks * 4),
-                l = range(a.kv_lens, (size_t)a.B * 4), s = range(a.q_start, a.q_start ? ((size_t)a.B + 1) * 4 : 0);
-    const CacheRanges c = ranges_of(*cache);
-    if (any_overlap({o, w}, {q, t, l, s, c.k, c.km, c.v, c.vm}) || overlap(o, w))
-        return fail(W4_ERR_ALIAS, "%s: out or workspace overlaps an input or each other", fn);
-    if (a.T == 0 || a.B == 0 || a.max_q == 0) return W4_OK;
-    const hipError_t err = w4::launch_kv4_attn(a, *cache, workspace, static_cast<hipStream_t>(stream));
-    return err == hipSuccess ? W4_OK : hip_fail(err, fn);
+    return attend("w4_kv4_attn", args, nullptr, 0, cache, workspace, workspace_bytes, stream);
+}
+
+W4_API size_t w4_kv4_attn_shared_workspace_bytes(const w4_attn_args* args, int prefix, const w4_kv4_cache* cache) {
+    if (prefix < 0) return 0;
+    return workspace_for("w4_kv4_attn_shared_workspace_bytes", args, prefix, cache);
+}
+
+W4_API w4_status w4_kv4_attn_shared(const w4_attn_args* args, const int32_t* prefix_table, int prefix,
+                                    const w4_kv4_cache* cache, void* workspace, size_t workspace_bytes, void* stream) {
+    return attend("w4_kv4_attn_shared", args, prefix_table, prefix, cache, workspace, workspace_bytes, stream);
 }
 
 W4_API size_t w4_sample_workspace_bytes(int rows, int vocab) {

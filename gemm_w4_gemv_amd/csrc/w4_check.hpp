@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "w4.h"
 
 namespace w4 {
@@ -26,5 +28,22 @@ inline Range range(const void* p, size_t bytes) {
     return {a, a + bytes};
 }
 inline bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
+inline bool any_overlap(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+    for (const Range& o : outs)
+        for (const Range& i : ins)
+            if (overlap(o, i)) return true;
+    return false;
+}
+inline bool any_overlap(std::initializer_list<Range> outs) {
+    for (const Range& a : outs)
+        for (const Range& b : outs)
+            if (&a != &b && overlap(a, b)) return true;
+    return false;
+}
+
+// Bytes from the first to past the last value of ``rows`` rows of ``wide`` values.
+inline Range rows_range(const void* p, int64_t rows, int64_t stride, int64_t wide, size_t value = 2) {
+    return range(p, p && rows > 0 ? ((size_t)(rows - 1) * (size_t)stride + (size_t)wide) * value : 0);
+}
 
 }  // namespace w4

@@ -16,6 +16,7 @@ import torch
 from . import _check, lib
 
 __all__ = ["Kv4Cache", "w4_kv4_plan", "w4_qk_norm_rope", "w4_kv4_read", "w4_kv4_attn", "w4_kv4_attn_workspace_bytes",
+           "w4_kv4_attn_shared", "w4_kv4_attn_shared_workspace_bytes",
            "w4_sample", "w4_sample_workspace_bytes", "KV4_GROUP", "KV4_PLAN_MAX_BATCH", "SAMPLE_MAX_VOCAB"]
 
 KV4_GROUP = 128
@@ -59,6 +60,8 @@ SIGNATURES = {
     "w4_kv4_read": (_i32, [_cache_p, _vp, _i32, _vp, _vp, _vp]),
     "w4_kv4_attn_workspace_bytes": (_sz, [ctypes.POINTER(_AttnArgs), _cache_p]),
     "w4_kv4_attn": (_i32, [ctypes.POINTER(_AttnArgs), _cache_p, _vp, _sz, _vp]),
+    "w4_kv4_attn_shared_workspace_bytes": (_sz, [ctypes.POINTER(_AttnArgs), _i32, _cache_p]),
+    "w4_kv4_attn_shared": (_i32, [ctypes.POINTER(_AttnArgs), _vp, _i32, _cache_p, _vp, _sz, _vp]),
     "w4_sample_workspace_bytes": (_sz, [_i32, _i32]),
     "w4_sample": (_i32, [_vp, _i64] + [_vp] * 6 + [_i32, _i32, _vp, _sz, _vp]),
 }
@@ -310,11 +313,21 @@ def w4_kv4_read(cache, slots, k_out=None, v_out=None, stream=None) -> None:
     _call("w4_kv4_read", lib.w4_kv4_read, (cache.ref, sp, n, kp, vp), stream, i)
 
 
+def _attn_sizes(T, B, q_heads, max_q, max_kv, window, sinks):
+    return _AttnArgs(T=_near(T), B=_near(B), q_heads=_near(q_heads), max_q=_near(max_q), max_kv=_near(max_kv),
+                     window=_near(window), sinks=_near(sinks))
+
+
 def w4_kv4_attn_workspace_bytes(cache, T: int, B: int, q_heads: int, max_q: int, max_kv: int, window: int = 0,
                                 sinks: int = 0) -> int:
-    a = _AttnArgs(T=_near(T), B=_near(B), q_heads=_near(q_heads), max_q=_near(max_q), max_kv=_near(max_kv),
-                  window=_near(window), sinks=_near(sinks))
+    a = _attn_sizes(T, B, q_heads, max_q, max_kv, window, sinks)
     return lib.w4_kv4_attn_workspace_bytes(ctypes.byref(a), cache.ref)
+
+
+def w4_kv4_attn_shared_workspace_bytes(cache, T: int, B: int, q_heads: int, max_q: int, max_kv: int, prefix: int,
+                                       window: int = 0, sinks: int = 0) -> int:
+    a = _attn_sizes(T, B, q_heads, max_q, max_kv, window, sinks)
+    return lib.w4_kv4_attn_shared_workspace_bytes(ctypes.byref(a), _near(prefix), cache.ref)
 
 
 def w4_kv4_attn(q, cache, block_table, kv_lens, out, q_start=None, max_q: int = 1, max_kv: int | None = None,
@@ -326,6 +339,30 @@ def w4_kv4_attn(q, cache, block_table, kv_lens, out, q_start=None, max_q: int = 
     the last at position ``kv_lens[b] - 1``.  With ``window`` > 0 a row sees the last ``window`` tokens up
     to its own and the first ``sinks``.  ``max_kv`` (default: the block table's reach) and ``max_q`` size
     the split and the workspace (``w4_kv4_attn_workspace_bytes``).  ``scale``: 1 / sqrt(head_dim)."""
+    a, pw, nbytes, i = _attn_args("w4_kv4_attn", q, cache, block_table, kv_lens, out, q_start, max_q, max_kv, scale,
+                                  window, sinks, workspace)
+    _call("w4_kv4_attn", lib.w4_kv4_attn, (ctypes.byref(a), cache.ref, pw, nbytes), stream, i)
+    return out
+
+
+def w4_kv4_attn_shared(q, cache, block_table, kv_lens, out, prefix_table, prefix: int, q_start=None, max_q: int = 1,
+                       max_kv: int | None = None, scale: float | None = None, window: int = 0, sinks: int = 0,
+                       workspace=None, stream=None) -> torch.Tensor:
+    """``w4_kv4_attn`` for requests whose first ``prefix`` tokens are the same and lie in the pages of
+    ``prefix_table`` (int32 [ceil(prefix / block_size)], the first entries of ``block_table``'s rows too): those
+    are worked on once for the rows of all requests (``workspace``: ``w4_kv4_attn_shared_workspace_bytes``)."""
+    a, pw, nbytes, i = _attn_args("w4_kv4_attn_shared", q, cache, block_table, kv_lens, out, q_start, max_q, max_kv,
+                                  scale, window, sinks, workspace)
+    if not -1 <= prefix <= _INT_MAX:
+        _too_large("w4_kv4_attn_shared", prefix)
+    pages = -(-max(prefix, 0) // cache.block_size)
+    tp, = _optional_addresses(i, prefix_table, "prefix_table", _int32, pages)
+    _call("w4_kv4_attn_shared", lib.w4_kv4_attn_shared, (ctypes.byref(a), tp, prefix, cache.ref, pw, nbytes), stream, i)
+    return out
+
+
+def _attn_args(where, q, cache, block_table, kv_lens, out, q_start, max_q, max_kv, scale, window, sinks, workspace):
+    """(struct, workspace's address, its size, device) of an attention's arguments."""
     if not isinstance(cache, Kv4Cache):
         raise TypeError("cache must be a Kv4Cache")
     i, d = cache.device_index, cache.head_dim
@@ -333,7 +370,7 @@ def w4_kv4_attn(q, cache, block_table, kv_lens, out, q_start=None, max_q: int = 
         raise ValueError("block_table must be [B, max_blocks]")
     B, width = block_table.shape
     if B > _INT_MAX or width > _INT_MAX:
-        _too_large("w4_kv4_attn", max(B, width))
+        _too_large(where, max(B, width))
     qp, qs = _heads(q, "q", i, None, None, d)
     T, q_heads, _ = q.shape
     op, os = _heads(out, "out", i, T, q_heads, d)
@@ -346,8 +383,7 @@ def w4_kv4_attn(q, cache, block_table, kv_lens, out, q_start=None, max_q: int = 
     pw, nbytes = None, 0
     if workspace is not None:
         pw, nbytes = _ptr(workspace, "workspace", workspace.dtype, i), workspace.numel() * workspace.element_size()
-    _call("w4_kv4_attn", lib.w4_kv4_attn, (ctypes.byref(a), cache.ref, pw, nbytes), stream, i)
-    return out
+    return a, pw, nbytes, i
 
 
 def w4_sample_workspace_bytes(rows: int, vocab: int) -> int:

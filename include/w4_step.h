@@ -208,6 +208,30 @@ W4_API w4_status w4_kv4_attn(const w4_attn_args* args, const w4_kv4_cache* cache
                              size_t workspace_bytes, void* stream);
 
 /*
+ * w4_kv4_attn_shared -- w4_kv4_attn for requests whose first ``prefix`` tokens
+ * are the same, in the same pages: their scores and sums are formed for the rows
+ * of all requests together, each page read once, and joined with those of each
+ * request's other tokens.  The same function of the same arguments otherwise:
+ * what a row sees, what it is without any, which rows are written.
+ *   prefix_table  device int32 [ceil(prefix / block_size)]: the shared pages.
+ *                 block_table's rows hold them too: a call may read the shared
+ *                 tokens through either, all or in part (precondition, not
+ *                 checked: the entries agree)
+ *   prefix        >= 0; 0 is w4_kv4_attn, and prefix_table may be NULL.  A request
+ *                 may hold fewer tokens
+ *   q_start       does not fall (precondition, not checked)
+ *   workspace     at least w4_kv4_attn_shared_workspace_bytes() bytes for the
+ *                 same arguments, else as for w4_kv4_attn
+ * It pays where the rows of a key/value head, over all requests, far outnumber
+ * those of one; few requests or a short prefix go w4_kv4_attn's way.  Requests
+ * behind different prefixes are calls of their own.
+ * Errors: as w4_kv4_attn; W4_ERR_SHAPE for a negative prefix.
+ */
+W4_API size_t w4_kv4_attn_shared_workspace_bytes(const w4_attn_args* args, int prefix, const w4_kv4_cache* cache);
+W4_API w4_status w4_kv4_attn_shared(const w4_attn_args* args, const int32_t* prefix_table, int prefix,
+                                    const w4_kv4_cache* cache, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * w4_sample -- one token from each row of logits, from a given uniform number.
  * Over a row's tokens in the order (logit falling, index rising):
  *   weight w = exp((logit - largest) / temperature)

@@ -1,0 +1,204 @@
+"""GPU parity of the attention behind a shared prefix against the FP64 oracle of
+the attention itself (each request with all of its tokens), with its bounds: two
+parts of a weight, 2^-16 of it; the parts' join is a few more FP32 roundings,
+within the 64 that the bound has for the sums."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import seeded_inputs as si
+from oracle import step as ref
+from test_gpu_step import check_attn, ints, random_cache, run_attn, to_device
+
+pytestmark = pytest.mark.gpu
+
+w4 = pytest.importorskip("gemm_w4_gemv_amd")
+from gemm_w4_gemv_amd import host  # noqa: E402
+
+DEV = "cuda"
+bf16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+    torch.cuda.synchronize()
+
+
+def case(seed, prefix, lens, news, hq, hkv, dim, block, spare=2):
+    """Requests of lens tokens in all, the first ``prefix`` of each (or all it has) in the same pages."""
+    g = si.rng(seed, 94, hq, dim, block, prefix)
+    shared = -(-prefix // block)
+    need = [max(-(-max(n, 0) // block) - shared, 0) for n in lens]
+    blocks = shared + sum(need) + spare
+    cache = random_cache(seed, blocks, block, hkv, dim)
+    pages = g.permutation(blocks)
+    table = np.full((len(lens), shared + max(need + [0]) + 1), 123456789)
+    table[:, :shared] = pages[:shared]
+    at = shared
+    for b, n in enumerate(need):
+        table[b, shared:shared + n] = pages[at:at + n]
+        at += n
+    q_start = np.concatenate(([0], np.cumsum(news)))
+    T = int(q_start[-1])
+    return cache, pages[:shared], table, q_start, si.bf16_normal(seed, (95, T, hq, dim), (T, hq, dim))
+
+
+def run(cache, q_bits, table, lens, q_start, prefix_table, prefix, pad=0, tail=0, stream=None, **kw):
+    T, hq, d = q_bits.shape
+    space = torch.zeros(T + tail, hq * d + pad, dtype=bf16, device=DEV)
+    q = space[:, :hq * d].unflatten(1, (hq, d))
+    q[:T] = host.bf16_tensor(q_bits)
+    out = torch.full((T + tail, hq * d + 2 * pad), 7.0, dtype=bf16, device=DEV)[:, :hq * d].unflatten(1, (hq, d))
+    max_q = max(int(np.max(np.diff(q_start))), 1) if q_start is not None else 1
+    kw.setdefault("max_kv", max(max(lens), 0))
+    size = w4.w4_kv4_attn_shared_workspace_bytes(cache, T + tail, len(lens), hq, max_q, kw["max_kv"], prefix,
+                                                 kw.get("window", 0), kw.get("sinks", 0))
+    work = torch.full((size // 4,), float("nan"), dtype=torch.float32, device=DEV) if size else None
+    torch.cuda.synchronize()
+    w4.w4_kv4_attn_shared(q, cache, ints(table), ints(lens), out, ints(prefix_table), prefix,
+                          q_start=None if q_start is None else ints(q_start), max_q=max_q, workspace=work, stream=stream,
+                          **kw)
+    torch.cuda.synchronize()
+    return host.bf16_values(out)
+
+
+def expect(cache, q, table, lens, q_start, dim, window=0, sinks=0):
+    table = np.where(table == 123456789, 0, table)
+    return ref.attention(q, cache, table, lens, q_start, float(np.float32(1 / np.sqrt(dim))), window, sinks, 2.0 ** -16)
+
+
+CASES = [  # prefix, lens, news, hq, hkv, dim, block, window, sinks
+    (32, [33, 40], [1, 1], 2, 1, 64, 16, 0, 0), (64, [65, 100, 200], [1] * 3, 8, 2, 128, 16, 0, 0),
+    (48, [60, 49, 300], [1] * 3, 4, 2, 64, 16, 0, 0),                       # half a tile of the prefix is each one's own
+    (1024, [1030, 1100, 1024, 1500], [1] * 4, 16, 8, 256, 64, 0, 0),
+    (640, [700] * 9, [1] * 9, 64, 8, 64, 64, 0, 0), (320, [330, 400] * 20, [1] * 40, 8, 2, 256, 32, 0, 0),
+    (512, [600, 513] * 18, [1] * 36, 20, 1, 128, 128, 0, 0),                # twenty heads to a key head
+    (256, [300, 270, 290], [5, 1, 3], 6, 2, 128, 32, 0, 0), (256, [400] * 4, [33, 1, 70, 2], 4, 2, 256, 64, 0, 0),
+    (2048, [2049] * 12, [1] * 12, 8, 8, 64, 256, 0, 0), (160, [10, 200, 0, 160, 161], [1, 1, 0, 1, 1], 8, 2, 128, 32, 0, 0),
+    (160, [5, 200, 100], [9, 4, 20], 4, 2, 64, 32, 0, 0),                   # rows that see nothing, requests inside the prefix
+    (512, [700, 520, 900], [1] * 3, 8, 2, 128, 64, 300, 0), (512, [700, 520, 900] * 14, [1] * 42, 8, 2, 128, 64, 100, 4),
+    (512, [530, 520, 900], [1, 7, 40], 6, 1, 256, 16, 40, 33), (512, [1000] * 40, [1] * 40, 4, 2, 64, 64, 64, 100),
+    (96, [4000, 100], [1, 1], 4, 1, 128, 32, 0, 0),                         # own tokens far outnumber the shared
+]
+
+
+@pytest.mark.parametrize("prefix,lens,news,hq,hkv,dim,block,window,sinks", CASES)
+def test_attn_shared(prefix, lens, news, hq, hkv, dim, block, window, sinks):
+    cache, shared, table, q_start, q = case(1, prefix, lens, news, hq, hkv, dim, block)
+    got = run(to_device(cache), q, table, lens, q_start, shared, prefix, window=window, sinks=sinks)
+    check_attn(got, *expect(cache, q, table, lens, q_start, dim, window, sinks))
+
+
+@pytest.mark.parametrize("prefix", [0, 1, 31])
+def test_attn_shared_without_a_whole_tile_is_the_attention(prefix):
+    lens, news = [50, 70], [1, 1]
+    cache, shared, table, q_start, q = case(2, prefix, lens, news, 4, 2, 128, 16)
+    dev = to_device(cache)
+    got = run(dev, q, table, lens, q_start, shared, prefix)
+    assert np.array_equal(got, run_attn(dev, q, table, lens, q_start, max_kv=70))
+
+
+@pytest.mark.parametrize("rows", [2, 40])
+def test_attn_shared_without_q_start_strided_and_with_rows_behind(rows):
+    lens = [300 + 3 * i for i in range(rows)]
+    cache, shared, table, q_start, q = case(3, 256, lens, [1] * rows, 8, 2, 128, 64)
+    dev = to_device(cache)
+    want = run(dev, q, table, lens, q_start, shared, 256)
+    check_attn(want, *expect(cache, q, table, lens, q_start, 128))
+    assert np.array_equal(run(dev, q, table, lens, None, shared, 256, pad=24), want)
+    got = run(dev, q, table, lens, q_start, shared, 256, pad=8, tail=3)
+    assert np.all(got[rows:] == 7.0)
+    check_attn(got[:rows], *expect(cache, q, table, lens, q_start, 128))
+
+
+def test_attn_shared_is_right_for_any_max_kv():
+    lens = [700, 650, 1200]
+    cache, shared, table, q_start, q = case(4, 640, lens, [1] * 3, 8, 2, 64, 64)
+    dev = to_device(cache)
+    want = expect(cache, q, table, lens, q_start, 64)
+    for max_kv in (0, 1, 640, 641, 100000, 2 ** 31 - 1):
+        check_attn(run(dev, q, table, lens, q_start, shared, 640, max_kv=max_kv), *want, f"max_kv {max_kv}")
+
+
+@pytest.mark.parametrize("rows", [3, 50])
+def test_attn_shared_bad_pages_and_odd_values(rows):
+    """A page out of range makes NaN of the rows that see it and of no other; what no row sees may hold anything."""
+    lens = [100 + 4 * i for i in range(rows)]
+    lens[0] = 70  # inside the prefix: sees tokens 0 .. 69
+    cache, shared, table, q_start, q = case(5, 96, lens, [1] * rows, 4, 2, 128, 16)
+    want = expect(cache, q, table, lens, q_start, 128)
+    cache.k_meta[shared[5], :, :, 15] = np.nan  # token 95: seen by all but the first
+    cache.v_meta[shared[4], :, :, 7:] = np.inf  # tokens 71 on
+    got = run(to_device(cache), q, table, lens, q_start, shared, 96)
+    check_attn(got[:1], want[0][:1], want[1][:1])
+    assert np.all(np.isnan(got[1:]))
+    cache, shared, table, q_start, q = case(5, 96, lens, [1] * rows, 4, 2, 128, 16)
+    for bad in (-1, 10 ** 6):
+        broken = shared.copy()
+        broken[5] = bad
+        got = run(to_device(cache), q, table, lens, q_start, broken, 96)
+        check_attn(got[:1], want[0][:1], want[1][:1])
+        assert np.all(np.isnan(got[1:]))
+    own = table.copy()
+    own[1, 6] = -1  # a request's own first page
+    got = run(to_device(cache), q, own, lens, q_start, shared, 96)
+    assert np.all(np.isnan(got[1]))
+    rest = [i for i in range(rows) if i != 1]
+    check_attn(got[rest], want[0][rest], want[1][rest])
+
+
+def test_attn_shared_table_that_ends_with_the_prefix():
+    """No page of a request's own in the table: a row past the prefix is NaN, one inside it is not."""
+    lens = [64, 65, 40]
+    cache, shared, table, q_start, q = case(6, 64, lens, [1] * 3, 4, 2, 64, 32)
+    want = expect(cache, q, table, lens, q_start, 64)
+    for width in (2, 0):
+        got = run(to_device(cache), q, table[:, :width], lens, q_start, shared, 64)
+        check_attn(got[[0, 2]], want[0][[0, 2]], want[1][[0, 2]])
+        assert np.all(np.isnan(got[1]))
+
+
+def test_attn_shared_graph_replays_with_growing_requests():
+    """Two captured calls over one workspace, replayed in turn; each request grows between, its table in place."""
+    lens, B, hq, dim, prefix = [321, 330, 350, 400, 322], 5, 8, 128, 320
+    cache, shared, table, q_start, q = case(7, prefix, [n + 40 for n in lens], [1] * B, hq, 2, dim, 32)
+    dev = to_device(cache)
+    stream = torch.cuda.Stream()
+    size = w4.w4_kv4_attn_shared_workspace_bytes(dev, B, B, hq, 1, 500, prefix)
+    work = torch.full((size // 4,), float("nan"), dtype=torch.float32, device=DEV)
+    dev_q = [host.bf16_tensor(q), host.bf16_tensor(q[::-1].copy())]
+    dev_lens, dev_table, dev_shared = ints(lens), ints(table), ints(shared)
+    outs, graphs = [torch.zeros(B, hq, dim, dtype=bf16, device=DEV) for _ in range(2)], []
+    torch.cuda.synchronize()
+    for x, out in zip(dev_q, outs):
+        w4.w4_graph_begin(stream)
+        try:
+            w4.w4_kv4_attn_shared(x, dev, dev_table, dev_lens, out, dev_shared, prefix, max_kv=500, workspace=work, stream=stream)
+        finally:
+            graphs.append(w4.w4_graph_end(stream))
+    for k in range(4):
+        now = [n + 9 * k for n in lens]
+        dev_lens.copy_(ints(now))
+        torch.cuda.synchronize()
+        for graph in graphs:
+            graph.replay(stream)
+        torch.cuda.synchronize()
+        for bits, out in zip((q, q[::-1]), outs):
+            check_attn(host.bf16_values(out), *expect(cache, bits, table, now, q_start, dim), f"replay {k}")
+    for graph in graphs:
+        graph.destroy()
+
+
+def test_attn_shared_repeats_its_bits_on_another_stream():
+    lens = [1100 + i for i in range(30)]
+    cache, shared, table, q_start, q = case(8, 1024, lens, [1] * 30, 16, 4, 64, 64)
+    dev = to_device(cache)
+    want = run(dev, q, table, lens, q_start, shared, 1024)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert np.array_equal(run(dev, q, table, lens, q_start, shared, 1024, stream=side), want)
