@@ -52,14 +52,11 @@ struct AttnArgs {
     bool in_turn;
     int window, sinks;
     float scale2;  // scale * log2(e)
-    // A row's results from this launch go to parts part0 .. part0 + splits - 1 of
-    // its ``parts`` (1: they are the output).
-    int parts, part0;
-    float* part_o;   // [T * q_heads][parts][D]
-    float* part_ml;  // [T * q_heads][parts][2]
-    // Tiles below this one are shared by all requests and worked on once, by a
-    // launch of its own (kShared: all rows of the call are one request's, each
-    // at its own request's position; ``requests`` of them).
+    float* part_o;   // [T * q_heads][splits][D]; NULL: a row's results are the output
+    float* part_ml;  // [T * q_heads][splits][2]
+    // Tiles below this one are shared by all requests and worked on apart, the rows of
+    // all ``requests`` together (kShared), each at its own request's position.  Those
+    // rows' parts lie in blocks of 16 rows as the lanes hold them: see store_block.
     int shared_tiles, requests;
 };
 
@@ -79,9 +76,25 @@ __device__ __forceinline__ f32x4_t mfma(const u32x4_t& a, const u32x4_t& b, cons
 struct Pair {
     uint32_t high, low;
 };
-__device__ __forceinline__ Pair two_parts(float x, float y) {
+// What the rounding left, x - high's half, is exact: as a product of the pair with
+// (-1, 0) or (0, -1) it takes one instruction, where taking the half out first
+// takes two.  (Both in registers: the compiler takes the first, as a literal, for
+// the second.)
+struct Less {
+    uint32_t first = 0x0000BF80u, second = 0xBF800000u;
+    __device__ __forceinline__ Less() { asm volatile("" : "+s"(first), "+s"(second)); }
+};
+__device__ __forceinline__ Pair two_parts(float x, float y, const Less& less) {
     const uint32_t high = pack_bf16x2(x, y);
-    return {high, pack_bf16x2(x - __builtin_bit_cast(float, high << 16), y - __builtin_bit_cast(float, high & 0xFFFF0000u))};
+    return {high, pack_bf16x2(dot2_bf16(high, less.first, x), dot2_bf16(high, less.second, y))};
+}
+
+// max(a, b, c) of scores, which no signalling NaN is among: fmaxf would quiet each
+// of its arguments first, an instruction a score.  A NaN counts for nothing.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float m;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(a), "v"(b), "v"(c));
+    return m;
 }
 
 // Over the four lanes of one row (lane bits 4 and 5).
@@ -90,11 +103,12 @@ __device__ __forceinline__ float row_max(float v) {
     const uint32_t u = __builtin_bit_cast(uint32_t, v);
     const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
     const uint32_t a0 = a[0], a1 = a[1];
-    const float m = fmaxf(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1));
+    const float x0 = __builtin_bit_cast(float, a0), m = max3(x0, x0, __builtin_bit_cast(float, a1));
     const uint32_t w = __builtin_bit_cast(uint32_t, m);
     const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
     const uint32_t b0 = b[0], b1 = b[1];
-    return fmaxf(__builtin_bit_cast(float, b0), __builtin_bit_cast(float, b1));
+    const float y0 = __builtin_bit_cast(float, b0);
+    return max3(y0, y0, __builtin_bit_cast(float, b1));
 }
 
 __device__ __forceinline__ float lo16(uint32_t v) { return f16_to_f32((uint16_t)v); }
@@ -128,22 +142,26 @@ __device__ __forceinline__ Request request_of(const AttnArgs& a, int b) {
     return {q0, max(q1 - q0, 0), max(as_table(a.kv_lens)[b], 0)};
 }
 
-// The position of token t of a call in its own request; -1 if it is in none.
-__device__ __forceinline__ int position_of(const AttnArgs& a, int t) {
-    int b = t, q0 = t, q1 = t + 1;
-    if (a.q_start) {
-        const auto start = [&](int i) { return min(max(a.q_start[i], 0), a.T); };
-        int lo = 0, hi = a.requests;  // the last request that begins at t or before
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (start(mid) <= t) lo = mid; else hi = mid;
-        }
-        b = lo;
-        q0 = start(b);
-        q1 = start(b + 1);
+// A request of a call as the positions of its rows want it.
+struct Span {
+    int q0, q1, kv;
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
+    Span x = {b, b + 1, 0};
+    if (b >= a.requests) return {0, 0, 0};
+    if (a.q_start) x = {min(max(a.q_start[b], 0), a.T), min(max(a.q_start[b + 1], 0), a.T), 0};
+    x.kv = max(a.kv_lens[b], 0);
+    return x;
+}
+// Positions of the call's tokens first .. first + count - 1, each in its own
+// request (-1: sees nothing), into LDS that holds -1: a thread a request, the
+// first of them already loaded, so that one latency is all it takes.
+template <int kThreads>
+__device__ __forceinline__ void put_positions(const AttnArgs& a, Span x, int first, int count, int* pos) {
+    for (int b = threadIdx.x; b < a.requests; b += kThreads) {
+        for (int t = max(x.q0, first); t < min(x.q1, first + count); ++t) pos[t - first] = max(x.kv - x.q1 + t, -1);
+        if (b + kThreads < a.requests) x = span_of(a, b + kThreads);
     }
-    if (t < q0 || t >= q1) return -1;
-    return max(max(a.kv_lens[b], 0) - (q1 - q0) + (t - q0), -1);
 }
 
 // The tiles that some of a run of rows (positions low .. high) see: those of
@@ -330,6 +348,7 @@ struct Rows {
     f32x4_t o[kNB][kG][kJ], ones_sum[kNB][kG];  // of ones_sum only element 0 counts
     float extra[kNB][kG], m[kNB], l[kNB];
     float means[kNB][kG], scales[kNB][kG];  // sums of p m and p s since the last settling
+    Less less;
     u32x4_t pop[2][kNB][kG];  // p s of the tile and what its rounding left, the second product's operands
 
     // Sends for the queries of rows r0 ..; past the last row that one again, unseen.
@@ -339,11 +358,7 @@ struct Rows {
 #pragma unroll
         for (int n = 0; n < kNB; ++n) {
             const int mine = r0 + 16 * n + c, r = min(mine, rows - 1);
-            if constexpr (kShared) {
-                pos[n] = mine < rows ? position_of(a, r / a.g) : -1;
-            } else {
-                pos[n] = mine < rows ? max(first_pos + r / a.g, -1) : -1;
-            }
+            if constexpr (!kShared) pos[n] = mine < rows ? max(first_pos + r / a.g, -1) : -1;
             const uint16_t* src = a.q + (int64_t)(req.first + r / a.g) * a.q_stride + (size_t)(head * a.g + r % a.g) * D;
 #pragma unroll
             for (int q = 0; q < kG; ++q)
@@ -353,8 +368,14 @@ struct Rows {
         }
     }
 
-    // The first and last position of the wave's rows (a shared prefix's rows are in no order).
-    __device__ __forceinline__ void reach(int* low, int* high) const {
+    // The rows' positions, of tokens ``first`` on, and the first and last of them (they are in no order).
+    __device__ __forceinline__ void place(const AttnArgs& a, const int* of, int first, int r0, int rows, int lane, int* low,
+                                          int* high) {
+#pragma unroll
+        for (int n = 0; n < kNB; ++n) {
+            const int mine = r0 + 16 * n + (lane & 15), at = of[min(mine, rows - 1) / a.g - first];
+            pos[n] = mine < rows ? at : -1;
+        }
         int lo = pos[0], hi = pos[0];
 #pragma unroll
         for (int n = 1; n < kNB; ++n) {
@@ -455,9 +476,10 @@ struct Rows {
                                           const uint32_t seen[kNB], float scale2, float slack) {
 #pragma unroll
         for (int n = 0; n < kNB; ++n) {
-            float top = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
-                              fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
-            top = row_max(top);
+            float top = max3(s[n][0][0], s[n][0][1], s[n][0][2]);
+            top = max3(top, s[n][0][3], s[n][1][0]);
+            top = max3(top, s[n][1][1], s[n][1][2]);
+            top = row_max(max3(top, top, s[n][1][3]));
             if (__any(top > m[n] + slack)) {
                 const float now = fmaxf(m[n], top);
                 const float keep = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m[n] - now) * scale2);
@@ -505,7 +527,7 @@ struct Rows {
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int r = 0; r < 4; r += 2) {
-                            const Pair w = two_parts(ps[h][r], ps[h][r + 1]);
+                            const Pair w = two_parts(ps[h][r], ps[h][r + 1], less);
                             pop[0][n][q][2 * h + r / 2] = w.high;
                             pop[1][n][q][2 * h + r / 2] = w.low;
                         }
@@ -612,7 +634,7 @@ struct Rows {
             const int row = r0 + 16 * n + c;
             if (row >= rows) continue;
             const int t = req.first + row / a.g, h = head * a.g + row % a.g;
-            if (a.parts == 1) {
+            if (!a.part_o) {
                 const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
                 uint16_t* dst = a.out + (int64_t)t * a.out_stride + (size_t)h * D;
 #pragma unroll
@@ -630,7 +652,7 @@ struct Rows {
                         }
                     }
             } else {
-                const size_t at = ((size_t)t * a.g * a.c.heads + h) * a.parts + a.part0 + split;
+                const size_t at = ((size_t)t * a.g * a.c.heads + h) * a.splits + split;
                 if (g == 0) {
                     a.part_ml[2 * at] = m[n];
                     a.part_ml[2 * at + 1] = l[n];
@@ -645,6 +667,32 @@ struct Rows {
                             *reinterpret_cast<f32x4_t*>(dst + place(q, r, g) + j) =
                                 f32x4_t{o[n][q][j][r], o[n][q][j + 1][r], o[n][q][j + 2][r], o[n][q][j + 3][r]};
             }
+        }
+    }
+    // A shared prefix's part: the lanes' values as they are, each piece of four a
+    // whole line of the wave (written row by row a lane's 16 bytes are a line's
+    // eighth, and 33 MB of parts took 12 us instead of 4).
+    static constexpr int kPieces = kG * kJ;  // (q * 4 + r) * (kJ / 4) + j / 4
+    __device__ __forceinline__ void store_block(const AttnArgs& a, int head, int split, int r0, int rows, int lane) const {
+        const int blocks = (a.T * a.g + 15) / 16;
+#pragma unroll
+        for (int n = 0; n < kNB; ++n) {
+            const int row = r0 + 16 * n;
+            if (row >= rows) continue;
+            const size_t at = ((size_t)split * a.c.heads + head) * blocks + row / 16;
+            if (lane < 16) {
+                a.part_ml[(at * 16 + lane) * 2] = m[n];
+                a.part_ml[(at * 16 + lane) * 2 + 1] = l[n];
+            }
+            f32x4_t* dst = reinterpret_cast<f32x4_t*>(a.part_o) + at * (4 * D) + lane;
+#pragma unroll
+            for (int q = 0; q < kG; ++q)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int j = 0; j < kJ; j += 4)
+                        dst[((q * 4 + r) * (kJ / 4) + j / 4) * kWave] =
+                            f32x4_t{o[n][q][j][r], o[n][q][j + 1][r], o[n][q][j + 2][r], o[n][q][j + 3][r]};
         }
     }
 };
@@ -668,9 +716,8 @@ __device__ __forceinline__ u32x4_t value_operand(const u32x4_t& first, const u32
 struct Share {
     int head, split, row_tile, b;
 };
-__device__ __forceinline__ Share share_of(const AttnArgs& a) {
+__device__ __forceinline__ Share share_of(const AttnArgs& a, int id) {
     // key/value heads innermost: workgroups that share a head's pages meet on one XCD
-    int id = blockIdx.x;
     Share s;
     s.head = id % a.c.heads;
     id /= a.c.heads;
@@ -687,27 +734,31 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a) {
 }
 
 // Few rows: the waves take a row tile's token tiles in turn.
-template <int D, int kNB, int kWaves, bool kWide, bool kShared = false>
-__global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
+template <int D, int kNB, int kWaves>
+struct FewLds {
+    float so[kWaves / 2][16 * kNB][D + 4];
+    float sm[kWaves][16 * kNB], sl[kWaves][16 * kNB];
+};
+template <int D, int kNB, int kWaves, bool kWide>
+__device__ __forceinline__ void few_rows(const AttnArgs& a, int id, FewLds<D, kNB, kWaves>& lds) {
     typedef Rows<D, kNB> R;
     constexpr int kG = R::kG, kJ = R::kJ, kCols = 16 * kNB;
-    __shared__ float so[kWaves / 2][kCols][D + 4];
-    __shared__ float sm[kWaves][kCols], sl[kWaves][kCols];
+    auto& so = lds.so;
+    auto &sm = lds.sm, &sl = lds.sl;
 
     const int lane = threadIdx.x & (kWave - 1), wave = (int)sgpr(threadIdx.x / kWave);
     const int c = lane & 15, g = lane >> 4;
-    const Share mine = share_of(a);
+    const Share mine = share_of(a, id);
     const int head = mine.head;
-    const Request req = kShared ? Request{0, a.T, 0} : request_of(a, mine.b);
-    const int rows = (kShared ? a.T : min(req.rows, a.max_q)) * a.g;  // < 2^31: checked on the host
+    const Request req = request_of(a, mine.b);
+    const int rows = min(req.rows, a.max_q) * a.g;  // < 2^31: checked on the host
     const int r0 = mine.row_tile * kCols;
     if (r0 >= rows) return;
     const int first_pos = req.kv - req.rows;
-    int low = first_pos + r0 / a.g, high = first_pos + (min(r0 + kCols, rows) - 1) / a.g;
+    const int low = first_pos + r0 / a.g, high = first_pos + (min(r0 + kCols, rows) - 1) / a.g;
     R rw;
-    rw.template fetch<kShared>(a, req, head, r0, rows, lane);
-    if constexpr (kShared) rw.reach(&low, &high);
-    const Tiles tiles = tiles_of<kShared>(a, low, high);
+    rw.template fetch<false>(a, req, head, r0, rows, lane);
+    const Tiles tiles = tiles_of<false>(a, low, high);
     const table_ptr table = as_table(a.table + (size_t)mine.b * a.width);
 
     // this split's tiles, in turn over the waves
@@ -837,6 +888,11 @@ __global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
     }
     if (wave == 0) rw.store(a, req, head, mine.split, r0, rows, lane);
 }
+template <int D, int kNB, int kWaves, bool kWide>
+__global__ __launch_bounds__(kWaves * kWave) void kv4_attn_kernel(AttnArgs a) {
+    __shared__ FewLds<D, kNB, kWaves> lds;
+    few_rows<D, kNB, kWaves, kWide>(a, blockIdx.x, lds);
+}
 
 // Value of lane l ^ kOff within a row of 16, for any set of other lane bits.
 template <int kOff>
@@ -881,17 +937,22 @@ __device__ __forceinline__ float over_sets(float v, F f) {
 // the end as the waves are.
 // Per 32 tokens of D = 128 and 4 rows that is some 160 vector instructions
 // instead of 260.
+template <int D, int kSets, int kWaves>
+struct SetsLds {
+    float so[kWaves][Frag<D>::kG * 4 * (D == 64 ? 4 : 8) / kSets][kWave];
+    float sm[kWaves][16 / kSets], sl[kWaves][16 / kSets];
+};
 template <int D, int kSets, int kWaves, bool kWide>
-__global__ __launch_bounds__(kWaves * kWave, 2) void kv4_attn_sets_kernel(AttnArgs a) {
+__device__ __forceinline__ void sets_of_rows(const AttnArgs& a, int id, SetsLds<D, kSets, kWaves>& lds) {
     constexpr int kT = kSets / 2, kCols = 16 / kSets;  // tiles at a time; rows
     constexpr int kG = Frag<D>::kG, kW = Frag<D>::kW, kJ = D == 64 ? 4 : 8;
     constexpr int kAll = kG * 4 * kJ, kMine = kAll / kSets;  // a lane's outputs, before and after the sets are joined
-    __shared__ float so[kWaves][kMine][kWave];
-    __shared__ float sm[kWaves][kCols], sl[kWaves][kCols];
+    auto& so = lds.so;
+    auto &sm = lds.sm, &sl = lds.sl;
 
     const int lane = threadIdx.x & (kWave - 1), wave = (int)sgpr(threadIdx.x / kWave);
     const int c = lane & 15, g = lane >> 4, set = c / kCols;
-    const Share mine = share_of(a);
+    const Share mine = share_of(a, id);
     const int head = mine.head;
     const Request req = request_of(a, mine.b);
     const int rows = min(min(req.rows, a.max_q) * a.g, kCols);
@@ -1017,6 +1078,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void kv4_attn_sets_kernel(AttnAr
     const float slack = fminf(8.0f / a.scale2, 3e38f);
     const uint32_t bias = vgpr_const(kInt4BiasPair);
     const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    const Less less;
     for (int done = 1; v < v1; v += kWaves * kT, ++done) {
         const Group next = group_at(v + kWaves * kT);
         send_entries(v + 2 * kWaves * kT);
@@ -1079,7 +1141,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void kv4_attn_sets_kernel(AttnAr
         }
 
         // softmax of the lane's four scores
-        const float top = row_max(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])));
+        const float three = max3(s[0], s[1], s[2]), top = row_max(max3(three, three, s[3]));
         if (__any(top > m + slack)) {
             const float top_now = fmaxf(m, top);
             const float keep = top_now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - top_now) * a.scale2);
@@ -1116,8 +1178,8 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void kv4_attn_sets_kernel(AttnAr
             }
             // here, not put off behind the loads that reuse vm's registers
             asm volatile("" : "+v"(means[q]), "+v"(scales[q]));
-            weights[q][0] = two_parts(ps[0], ps[1]);
-            weights[q][1] = two_parts(ps[2], ps[3]);
+            weights[q][0] = two_parts(ps[0], ps[1], less);
+            weights[q][1] = two_parts(ps[2], ps[3], less);
         }
         __builtin_amdgcn_sched_barrier(0);
         fetch_meta(next, a.c.vm, vm);
@@ -1209,7 +1271,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void kv4_attn_sets_kernel(AttnAr
     const int at = set * kMine + wave * kEnd;  // (q, r, j) as one number
     const int d = Rows<D, 1>::place(at / kJ / 4, at / kJ % 4, g) + at % kJ;
     const int t = req.first + row / a.g, h = head * a.g + row % a.g;
-    if (a.parts == 1) {
+    if (!a.part_o) {
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         uint16_t* dst = a.out + (int64_t)t * a.out_stride + (size_t)h * D + d;
         if constexpr (kEnd % 2 == 0) {
@@ -1219,7 +1281,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void kv4_attn_sets_kernel(AttnAr
             dst[0] = f32_to_bf16(end[0] * inv);
         }
     } else {
-        const size_t part = ((size_t)t * a.g * a.c.heads + h) * a.parts + a.part0 + mine.split;
+        const size_t part = ((size_t)t * a.g * a.c.heads + h) * a.splits + mine.split;
         if (g == 0 && wave == 0 && set == 0) {
             a.part_ml[2 * part] = now_top;
             a.part_ml[2 * part + 1] = sum;
@@ -1227,6 +1289,11 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void kv4_attn_sets_kernel(AttnAr
 #pragma unroll
         for (int i = 0; i < kEnd; ++i) a.part_o[part * D + d + i] = end[i];
     }
+}
+template <int D, int kSets, int kWaves, bool kWide>
+__global__ __launch_bounds__(kWaves * kWave, 2) void kv4_attn_sets_kernel(AttnArgs a) {
+    __shared__ SetsLds<D, kSets, kWaves> lds;
+    sets_of_rows<D, kSets, kWaves, kWide>(a, blockIdx.x, lds);
 }
 
 // Waits for a workgroup's LDS accesses and meets the others; loads from
@@ -1247,18 +1314,26 @@ __device__ __forceinline__ void lds_barrier() {
 // in place of four where a tile is one page (eight prompts of 1000 tokens, 32 query
 // and 8 key/value heads: 106 us, 124 with 173 registers and two waves).
 // A shared prefix's tiles may be split over workgroups.
-template <int D, int kNB, bool kWide, bool kShared = false>
-__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv4_attn_many_kernel(AttnArgs a) {
+template <int D, int kNB, bool kShared>
+struct ManyLds {
+    u32x4_t ops[2][2 * Frag<D>::kG * Frag<D>::kW + Frag<D>::kG * (D == 64 ? 4 : 8)][kWave];
+    u32x4_t meta[2][2][Frag<D>::kG][kTile / 4];  // (s, m) pairs of keys and of values
+    int pos[kShared ? 64 * kNB : 1], reach[kShared ? 4 : 1][2];
+};
+template <int D, int kNB, bool kWide, bool kShared>
+__device__ __forceinline__ void many_rows(const AttnArgs& a, int id, ManyLds<D, kNB, kShared>& lds) {
     typedef Rows<D, kNB> R;
     constexpr int kWaves = 4, kG = R::kG, kW = R::kW, kJ = R::kJ, kCols = 16 * kNB;
     constexpr int kKeys = 2 * kG * kW, kValues = kG * kJ;  // operands of a tile
     constexpr int kMyKeys = kKeys / kWaves, kMyValues = kValues / kWaves;
     constexpr int kAheadKeys = kKeys < 6 ? kKeys : 6, kAheadValues = D == 64 ? (kWide ? 2 : 4) : 8;
-    __shared__ u32x4_t ops[2][kKeys + kValues][kWave];
+    auto &ops = lds.ops;
+    auto &pos = lds.pos;
+    auto &reach = lds.reach;
 
     const int lane = threadIdx.x & (kWave - 1), wave = (int)sgpr(threadIdx.x / kWave);
     const int c = lane & 15, g = lane >> 4;
-    const Share mine = share_of(a);
+    const Share mine = share_of(a, id);
     const int head = mine.head;
     const Request req = kShared ? Request{0, a.T, 0} : request_of(a, mine.b);
     const int rows = (kShared ? a.T : min(req.rows, a.max_q)) * a.g;
@@ -1270,24 +1345,40 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv4_attn_many_kernel(Att
     const int r0 = min(base + wave * kCols, rows);
     int my_low = first_pos + min(r0, rows - 1) / a.g, my_high = first_pos + (min(r0 + kCols, rows) - 1) / a.g;
     R rw;
-    rw.template fetch<kShared>(a, req, head, r0, rows, lane);
+    // A shared prefix: the positions of the workgroup's rows.  Only with a window do the
+    // tiles depend on them; without one the first tiles are sent for before they are known.
+    constexpr int kRows = kWaves * kCols;
+    Span span = {};
     if constexpr (kShared) {
-        __shared__ int reach[kWaves][2];
-        rw.reach(&my_low, &my_high);
-        if (lane == 0) {
-            reach[wave][0] = r0 < rows ? my_low : 0x7FFFFFFF;
-            reach[wave][1] = my_high;
-        }
+        span = span_of(a, threadIdx.x);
+        if (threadIdx.x < kRows) pos[threadIdx.x] = -1;
+    }
+    rw.template fetch<kShared>(a, req, head, r0, rows, lane);
+    const auto set_positions = [&]() {  // after a barrier behind the -1s; another has to follow
+        put_positions<kWaves * kWave>(a, span, base / a.g, (min(base + kRows, rows) - 1) / a.g - base / a.g + 1, pos);
+    };
+    if constexpr (kShared) {
         __syncthreads();
-        low = reach[0][0];
-        high = reach[0][1];
+        low = high = a.shared_tiles * kTile - 1;
+        if (a.window != 0) {
+            set_positions();
+            __syncthreads();
+            rw.place(a, pos, base / a.g, r0, rows, lane, &my_low, &my_high);
+            if (lane == 0) {
+                reach[wave][0] = r0 < rows ? my_low : 0x7FFFFFFF;
+                reach[wave][1] = my_high;
+            }
+            __syncthreads();
+            low = reach[0][0];
+            high = reach[0][1];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) {
-            low = min(low, reach[w][0]);
-            high = max(high, reach[w][1]);
+            for (int w = 1; w < kWaves; ++w) {
+                low = min(low, reach[w][0]);
+                high = max(high, reach[w][1]);
+            }
+            low = (int)sgpr((uint32_t)low);
+            high = (int)sgpr((uint32_t)high);
         }
-        low = (int)sgpr((uint32_t)low);
-        high = (int)sgpr((uint32_t)high);
     }
     const Tiles tiles = tiles_of<kShared>(a, low, high);
     const table_ptr table = as_table(a.table + (size_t)mine.b * a.width);
@@ -1304,10 +1395,15 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv4_attn_many_kernel(Att
     // of one group (for which it needs the words of all 32 tokens).
     const int kh = wave * kMyKeys / (kG * kW), kq = wave * kMyKeys / kW % kG, kw = wave * kMyKeys % kW;
     const int vq = wave * kMyValues / kJ, vj = wave * kMyValues % kJ;
-    uint32_t raw_k[kMyKeys];
+    // And a dword of pairs a lane: a token of the keys' (lanes 0 .. 31) or the values', of
+    // group wave % kG (two waves may bring the same).
+    const int mq = wave % kG;
+    const uint32_t* const meta_of = lane < kTile ? a.c.km : a.c.vm;
+    uint32_t raw_k[kMyKeys], raw_m;
     u32x4_t raw_v[2];
     const auto fetch_codes = [&](const Place<kWide>& p) {
-        const uint64_t key = kWide ? p.code[0] + kh * 16 * (D / 2) : p.code[kh % Place<kWide>::kN];
+        // no subscript that is not a constant: it would put the places in memory
+        const uint64_t key = kWide ? p.code[0] + kh * 16 * (D / 2) : kh ? p.code[Place<kWide>::kN - 1] : p.code[0];
         if constexpr (kMyKeys == 4) {
             const u32x4_t w = fetch<u32x4_t>(a.c.kc, key + kq * 64, offs.k);
 #pragma unroll
@@ -1322,6 +1418,8 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv4_attn_many_kernel(Att
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             raw_v[h] = fetch<u32x4_t>(a.c.vc, (kWide ? p.code[0] + h * 16 * (D / 2) : p.code[h % Place<kWide>::kN]) + vq * 256, offs.v);
+        const uint64_t half = kWide ? p.meta[0] + 4 * (lane & 31) : (lane & 16 ? p.meta[Place<kWide>::kN - 1] : p.meta[0]) + 4 * c;
+        raw_m = fetch<uint32_t>(meta_of, half + ((uint64_t)(4u * mq) << a.c.shift), 0);
     };
     const auto unpack = [&](int buffer) {
 #pragma unroll
@@ -1340,32 +1438,39 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv4_attn_many_kernel(Att
             }
             ops[buffer][kKeys + wave * kMyValues + i][lane] = op;
         }
+        reinterpret_cast<uint32_t*>(lds.meta[buffer][lane >> 5][mq])[lane & 31] = raw_m;
     };
-    u32x4_t km[2][kG], vm[2][kG];
-    const auto fetch_meta = [&](const Place<kWide>& p, const uint32_t* from, u32x4_t to[2][kG]) {
-        load_meta<D, kWide>(a, from, to, p, offs);
+    // A tile's pairs as the lanes want them, four tokens each.
+    const auto pairs = [&](int buffer, int of, u32x4_t to[2][kG]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < kG; ++q) to[h][q] = lds.meta[buffer][of][q][4 * h + g];
     };
 
-    int t0 = 0, t1 = 0, page[2] = {-1, -1}, coming[2] = {-1, -1};
+    // Tiles v, v + 1 and v + 2: where they begin, their pages.
+    int from[3], page[3][2];
     Entries next = {};
-    Place<kWide> ahead = {};
+    const auto send = [&](int i, const Entries& e) {  // for the tile v + i
+        pages_of<kWide>(a, e, from[i], high, page[i]);
+        fetch_codes(place_of<D, kWide>(a, from[i], head, page[i]));
+    };
     if (v < v1) {
-        t0 = tile_at(v);
-        t1 = tile_at(v + 1);
-        const Entries now = entries_of<kWide>(a, table, t0), then = entries_of<kWide>(a, table, t1);
-        pages_of<kWide>(a, now, t0, high, page);
-        const Place<kWide> p = place_of<D, kWide>(a, t0, head, page);
-        fetch_codes(p);
-        fetch_meta(p, a.c.km, km);
-        fetch_meta(p, a.c.vm, vm);
+        Entries e[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            from[i] = tile_at(v + i);
+            e[i] = entries_of<kWide>(a, table, from[i]);
+        }
+        send(0, e[0]);
         unpack(0);
-        pages_of<kWide>(a, then, t1, high, coming);
-        ahead = place_of<D, kWide>(a, t1, head, coming);
-        fetch_codes(ahead);
+        send(1, e[1]);
         next = entries_of<kWide>(a, table, tile_at(v + 2));
     }
     rw.start();
+    if (kShared && a.window == 0) set_positions();
     lds_barrier();
+    if (kShared && a.window == 0) rw.place(a, pos, base / a.g, r0, rows, lane, &my_low, &my_high);
 
     const float slack = fminf(8.0f / a.scale2, 3e38f);
     const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
@@ -1375,15 +1480,13 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv4_attn_many_kernel(Att
         // (at the end the last tile again: loads under a condition would be
         // waited for and copied)
         unpack(buffer ^ 1);
-        const int t2 = tile_at(v + 2);
-        int after[2];
-        pages_of<kWide>(a, next, t2, high, after);
-        const Place<kWide> place = ahead;
-        ahead = place_of<D, kWide>(a, t2, head, after);
+        const Entries now = next;
+        from[2] = tile_at(v + 2);
         next = entries_of<kWide>(a, table, tile_at(v + 3));
         __builtin_amdgcn_sched_barrier(0);
-        fetch_codes(ahead);
+        send(2, now);
         __builtin_amdgcn_sched_barrier(0);
+        const int t0 = from[0];
 
         // Rows of a wave that lie before the tile, or before whose window it ends, pass
         // it over.  (Positions below 0 see nothing; less a window they could pass 32 bits.)
@@ -1391,38 +1494,151 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv4_attn_many_kernel(Att
                           (a.window == 0 || t0 + kTile - 1 > max(my_low, 0) - a.window || t0 < a.sinks);
         if (sees) {
             const bool whole = t0 + kTile - 1 <= my_low && (a.window == 0 || t0 > my_high - a.window || t0 + kTile <= a.sinks) &&
-                               page[0] >= 0 && page[1] >= 0 && r0 + kCols <= rows;
+                               page[0][0] >= 0 && page[0][1] >= 0 && r0 + kCols <= rows;
             float s[kNB][2][4];
+            u32x4_t km[2][kG], vm[2][kG];
+            pairs(buffer, 0, km);
             rw.template scores<kAheadKeys>(s, [&](int h, int q, int i) { return ops[buffer][(h * kG + q) * kW + i][lane]; }, km);
             uint32_t seen[kNB];
 #pragma unroll
             for (int n = 0; n < kNB; ++n) seen[n] = 0xFFu;
-            if (!whole) rw.mask(a, s, seen, t0, page, g);
+            if (!whole) rw.mask(a, s, seen, t0, page[0], g);
+            pairs(buffer, 1, vm);
             rw.weigh(s, vm, whole, seen, a.scale2, slack);
             rw.template outputs<kAheadValues>([&](int q, int j) { return ops[buffer][kKeys + q * kJ + j][lane]; }, ones);
         }
-        __builtin_amdgcn_sched_barrier(0);
-        fetch_meta(place, a.c.km, km);
-        fetch_meta(place, a.c.vm, vm);
-        __builtin_amdgcn_sched_barrier(0);
         if (done % 8 == 0) rw.settle();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            page[h] = coming[h];
-            coming[h] = after[h];
+        for (int i = 0; i < 2; ++i) {
+            from[i] = from[i + 1];
+            page[i][0] = page[i + 1][0];
+            page[i][1] = page[i + 1][1];
         }
-        t0 = t1;
-        t1 = t2;
         lds_barrier();
     }
     rw.finish(a);
-    if (r0 < rows) rw.store(a, req, head, kShared ? mine.split : 0, r0, rows, lane);
+    if constexpr (kShared) {
+        rw.store_block(a, head, mine.split, r0, rows, lane);
+    } else {
+        if (r0 < rows) rw.store(a, req, head, 0, r0, rows, lane);
+    }
+}
+template <int D, int kNB, bool kWide>
+__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv4_attn_many_kernel(AttnArgs a) {
+    __shared__ ManyLds<D, kNB, false> lds;
+    many_rows<D, kNB, kWide, false>(a, blockIdx.x, lds);
+}
+
+constexpr int kMaxSplits = 128;
+constexpr int kThreads = 256;
+
+// A shared prefix and each request's own tokens in one launch: the first is
+// bound by arithmetic, the second by memory, and a compute unit that holds a
+// workgroup of each has both at work.
+template <int D, bool kWide, int kSets>
+__global__ __launch_bounds__(kThreads, 2) void kv4_attn_shared_kernel(AttnArgs shared, AttnArgs own, int shared_units) {
+    typedef ManyLds<D, 1, true> Many;
+    typedef std::conditional_t<kSets == 1, FewLds<D, 1, 4>, SetsLds<D, kSets == 1 ? 2 : kSets, 4>> Own;
+    constexpr int kBytes = sizeof(Many) > sizeof(Own) ? sizeof(Many) : sizeof(Own);
+    __shared__ __attribute__((aligned(16))) char lds[kBytes];
+    const int heads = shared.c.heads, unit = blockIdx.x / heads;
+    if (unit < shared_units) {
+        many_rows<D, 1, kWide, true>(shared, blockIdx.x, *reinterpret_cast<Many*>(lds));
+    } else {
+        const int id = blockIdx.x - shared_units * heads;
+        if constexpr (kSets == 1) {
+            few_rows<D, 1, 4, kWide>(own, id, *reinterpret_cast<Own*>(lds));
+        } else {
+            sets_of_rows<D, kSets, 4, kWide>(own, id, *reinterpret_cast<Own*>(lds));
+        }
+    }
+}
+
+// Joins the shared prefix's parts (in blocks of 16 rows) with those of each
+// request's own tokens (row by row): a workgroup a piece of a block, four values
+// of each lane's row, its waves the parts in turn.
+template <int D>
+__global__ __launch_bounds__(kThreads) void kv4_attn_shared_join_kernel(AttnArgs a, const float* own_o, const float* own_ml,
+                                                                        int own_splits) {
+    constexpr int kWaves = kThreads / kWave, kFirst = 8, kJ = D == 64 ? 4 : 8, kPieces = Rows<D, 1>::kPieces;
+    __shared__ float sm[2 * kMaxSplits][16], sl[2 * kMaxSplits][16], sums[kWaves][16];
+    __shared__ f32x4_t part[kWaves][kWave];
+    __shared__ int row_in[16];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = (int)sgpr(tid / kWave);
+    const int c = lane & 15, g = lane >> 4;
+    int id = blockIdx.x;
+    const int head = id % a.c.heads;
+    id /= a.c.heads;
+    const int piece = id % kPieces, block = id / kPieces;
+    const int rows = a.T * a.g, blocks = (rows + 15) / 16, heads = a.g * a.c.heads;
+
+    const f32x4_t* from = reinterpret_cast<const f32x4_t*>(a.part_o) + piece * kWave + lane;
+    const auto at = [&](int s) { return ((size_t)s * a.c.heads + head) * blocks + block; };
+    f32x4_t x[kFirst];
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) {
+        const int s = wave + kWaves * i;
+        x[i] = f32x4_t{0, 0, 0, 0};
+        if (s < a.splits) x[i] = from[at(s) * (4 * D)];
+    }
+    // the lane's row and its place in the output; rows in no request, or past max_q, have none
+    const int row = min(block * 16 + c, rows - 1), t = row / a.g, h = head * a.g + row % a.g;
+    const int first = block * 16 / a.g, count = (min(block * 16 + 15, rows - 1)) / a.g - first + 1;
+    Span span = span_of(a, tid);
+    if (tid < 16) row_in[tid] = -1;
+    for (int i = tid; i < a.splits * 16; i += kThreads) {
+        const float* ml = a.part_ml + (at(i / 16) * 16 + i % 16) * 2;
+        sm[i / 16][i % 16] = ml[0];
+        sl[i / 16][i % 16] = ml[1];
+    }
+    __syncthreads();
+    for (int b = tid; b < a.requests; b += kThreads) {
+        for (int i = max(span.q0, first); i < min(min(span.q1, span.q0 + a.max_q), first + count); ++i) row_in[i - first] = i;
+        if (b + kThreads < a.requests) span = span_of(a, b + kThreads);
+    }
+    __syncthreads();
+    const bool live = block * 16 + c < rows && row_in[t - first] >= 0;
+    const size_t own = ((size_t)t * heads + h) * own_splits;
+    const int d = Rows<D, 1>::place(piece / kJ, piece % kJ / (kJ / 4), g) + piece % (kJ / 4) * 4;
+    float top = -INFINITY;
+    for (int s = 0; s < a.splits; ++s) top = fmaxf(top, sm[s][c]);
+    if (live)
+        for (int s = 0; s < own_splits; ++s) top = fmaxf(top, own_ml[2 * (own + s)]);
+
+    f32x4_t v = {0, 0, 0, 0};
+    float sum = 0;
+    const auto add = [&](float m, float l, const f32x4_t& y) {
+        // a part that saw nothing has l = 0 and counts for nothing; a NaN stays one
+        const float w = l == 0.0f ? 0.0f : m == -INFINITY ? NAN : __builtin_amdgcn_exp2f((m - top) * a.scale2);
+        if (l != 0.0f) sum = fmaf(w, l, sum);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = fmaf(w, y[e], v[e]);
+    };
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) {
+        const int s = wave + kWaves * i;
+        if (s < a.splits) add(sm[s][c], sl[s][c], x[i]);
+    }
+    for (int s = wave + kWaves * kFirst; s < a.splits; s += kWaves) add(sm[s][c], sl[s][c], from[at(s) * (4 * D)]);
+    if (live)
+        for (int s = wave; s < own_splits; s += kWaves)
+            add(own_ml[2 * (own + s)], own_ml[2 * (own + s) + 1], *reinterpret_cast<const f32x4_t*>(own_o + (own + s) * D + d));
+    part[wave][lane] = v;
+    if (g == 0) sums[wave][c] = sum;
+    __syncthreads();
+    if (wave != 0 || !live) return;
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+        v += part[w][lane];
+        sum += sums[w][c];
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    *reinterpret_cast<u32x2_t*>(a.out + (int64_t)t * a.out_stride + (size_t)h * D + d) =
+        u32x2_t{pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv)};
 }
 
 // Joins the splits of one row, a workgroup a row: D / 4 lanes hold its values,
 // so 1024 / D splits are read at once.
-constexpr int kMaxSplits = 128;
-constexpr int kThreads = 256;
 template <int D>
 __global__ __launch_bounds__(kThreads) void kv4_attn_join_kernel(AttnArgs a) {
     constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
@@ -1436,14 +1652,14 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_join_kernel(AttnArgs a) {
     const Request req = request_of(a, b);
     if (i >= req.rows) return;
     const int t = req.first + i;
-    const size_t at = ((size_t)t * heads + h) * a.parts;
+    const size_t at = ((size_t)t * heads + h) * a.splits;
     if (tid < kWave) {
         float ms[kMaxSplits / kWave], ls[kMaxSplits / kWave], now = -INFINITY, sum = 0;
 #pragma unroll
         for (int u = 0; u < kMaxSplits / kWave; ++u) {
             const int s = u * kWave + lane;
-            ms[u] = s < a.parts ? a.part_ml[2 * (at + s)] : -INFINITY;
-            ls[u] = s < a.parts ? a.part_ml[2 * (at + s) + 1] : 0.0f;
+            ms[u] = s < a.splits ? a.part_ml[2 * (at + s)] : -INFINITY;
+            ls[u] = s < a.splits ? a.part_ml[2 * (at + s) + 1] : 0.0f;
             now = fmaxf(now, ms[u]);
         }
 #pragma unroll
@@ -1463,7 +1679,7 @@ __global__ __launch_bounds__(kThreads) void kv4_attn_join_kernel(AttnArgs a) {
     const int li = tid % kLanes;
     f32x4_t v = {0, 0, 0, 0};
 #pragma unroll 8
-    for (int s = tid / kLanes; s < a.parts; s += kAtOnce) {
+    for (int s = tid / kLanes; s < a.splits; s += kAtOnce) {
         const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part_o + (at + s) * D + 4 * li);
         const float w = weight[s];
 #pragma unroll
@@ -1603,7 +1819,7 @@ hipError_t launch_d(const AttnArgs& k, const Cut& cut, int64_t groups, hipStream
         kv4_attn_kernel<D, 1, 4, kWide><<<grid, block, 0, stream>>>(k);
     }
     const hipError_t err = hipGetLastError();
-    if (err != hipSuccess || k.parts == 1) return err;
+    if (err != hipSuccess || !k.part_o) return err;
     const int64_t units = (int64_t)k.B * k.max_q * k.g * k.c.heads;
     kv4_attn_join_kernel<D><<<dim3((unsigned)units), dim3(kThreads), 0, stream>>>(k);
     return hipGetLastError();
@@ -1635,34 +1851,110 @@ AttnArgs args_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     return k;
 }
 
-size_t part_bytes(const w4_attn_args& a, const w4_kv4_cache& c, int parts) {
-    return (size_t)a.T * a.q_heads * parts * (c.head_dim + 2) * sizeof(float);
-}
-void set_parts(AttnArgs& k, const w4_attn_args& a, const w4_kv4_cache& c, void* workspace, int parts) {
-    k.parts = parts;
-    if (parts == 1) return;
-    k.part_o = static_cast<float*>(workspace);
-    k.part_ml = k.part_o + (size_t)a.T * a.q_heads * parts * c.head_dim;
+// How a call whose requests begin with the same tokens is cut.
+struct SharedCut {
+    int tiles;      // whole tiles of the prefix; the rest of it is done with each request's own tokens
+    int splits;     // workgroups that share a row tile's tokens of the prefix; 0: all is done request by request
+    int row_tiles;  // of all requests' rows
+    int blocks;     // of 16 rows of a key/value head
+    int sets, own_row_tiles, own_splits;  // each request's own tokens
+};
+SharedCut shared_cut_of(const w4_attn_args& a, int prefix, const w4_kv4_cache& c) {
+    SharedCut k = {};
+    const int64_t B = a.B, g = a.q_heads / c.kv_heads, rows = a.T * g, own_rows = a.max_q * g;
+    const int64_t tiles = prefix / kTile, own_row_tiles = (own_rows + 15) / 16;
+    // Request by request the prefix's tiles are unpacked and scored for each (later
+    // requests find them in the caches): that costs by tiles times requests, here in
+    // units of a tile against 16 rows.  Together they cost by the rows, and the parts'
+    // way through memory and a join.  us request by request, then together, by units
+    // over rows a request: heads of 128, 2048 (4 requests behind 8192 tokens, 32 and 8 heads)
+    // 15.9 and 17.7, 2048 (64, 8192, 8 and 1 heads) 22.8 and 24.2, 4096 (16, 4096) 23.4 and
+    // 15.9, 4096 (64, 1024) 17.0 and 16.5, 65536 (64, 16384) 150 and 60; heads of 256, 2048
+    // (4, 4096, 16 and 8 heads) 17.7 and 18.4, 4096 (16, 2048) 22.0 and 16.2, 32768 (32, 8192) 99 and
+    // 34; heads of 64, 4096 (64, 2048, 64 and 8 heads) 18.6 and 20.9, 16384 (64, 8192) 61 and 41.  A
+    // request of more than 8 rows has products of its own full enough (24 requests of up to
+    // 5 rows of 8 heads, heads of 64, behind 4112: 54 and 38).
+    // Long prompts, with rows enough of their own, are done request by request.
+    const int64_t units = B * own_row_tiles * c.kv_heads * tiles, each = (rows + B - 1) / B;
+    if (a.T < 2 || own_rows > 64 || rows > (1 << 20) || units <= (each < 8 ? each : 8) * (c.head_dim == 64 ? 6144 : 2048)) return k;
+    const int64_t own_groups = B * c.kv_heads * own_row_tiles, groups = c.kv_heads * ((rows + 63) / 64);
+    if (own_groups > (1 << 20)) return k;
+    k.tiles = (int)tiles;
+    k.row_tiles = (int)((rows + 63) / 64);
+    k.blocks = (int)((rows + 15) / 16);
+    k.sets = own_rows > 8 ? 1 : own_rows > 4 || c.head_dim == 256 ? 2 : 4;
+    k.own_row_tiles = (int)own_row_tiles;
+    const auto bounded = [](int64_t x, int64_t most) {
+        x = x < most ? x : most;
+        return (int)(x < 1 ? 1 : x < kMaxSplits ? x : kMaxSplits);
+    };
+    const int64_t own_tokens = (int64_t)a.max_kv - tiles * kTile;
+    k.own_splits = bounded(own_tokens / (32 * kTile), 1024 / own_groups);
+    // The prefix: two workgroups a compute unit (four with heads of 64, of half the
+    // registers), each with eight tiles or more; short prefixes up to 16 of four.  A
+    // part more is a write and a read of its rows.  32 requests behind 8192 tokens, 16 and
+    // 8 heads of 256: 16 splits 38.5 us, 24 33.2, 32 34.4, 48 46; 64 behind 16384, 32 and 8
+    // heads of 128: 12 70 us, 16 60, 20 64; 64 of 1024, 16 and 8 heads of 256: 4 23.8, 8 22.1, 16
+    // 26.8; 64 of 8192, 64 and 8 heads of 64: 8 48, 12 43.4, 16 40.6, 20 46.
+    const int64_t few = tiles / 4 < 16 ? tiles / 4 : 16;
+    k.splits = bounded((c.head_dim == 64 ? 1024 : 512) / groups, few > tiles / 8 ? few : tiles / 8);
+    return k;
 }
 
-// The arguments as the cut of each request's own tokens wants them.
-w4_attn_args behind(const w4_attn_args& a, int tiles) {
-    w4_attn_args x = a;
-    x.max_kv = a.max_kv > tiles * kTile ? a.max_kv - tiles * kTile : 0;
-    return x;
+// The workspace of such a call: floats before each of its four arrays, and of all.
+struct SharedSpace {
+    size_t own_o, ml, own_ml, all;
+};
+SharedSpace shared_space_of(const w4_attn_args& a, const w4_kv4_cache& c, const SharedCut& k) {
+    const size_t rows = (size_t)k.splits * c.kv_heads * k.blocks * 16, own = (size_t)a.T * a.q_heads * k.own_splits;
+    SharedSpace s;
+    s.own_o = rows * c.head_dim;
+    s.ml = s.own_o + own * c.head_dim;
+    s.own_ml = s.ml + rows * 2;
+    s.all = s.own_ml + own * 2;
+    return s;
 }
 
-// Each request's tokens from tile ``tiles`` on; what is before that has left ``before`` parts.
-hipError_t launch_own(const w4_attn_args& a, const w4_kv4_cache& c, void* workspace, int tiles, int before,
-                      hipStream_t stream) {
+template <int D, bool kWide>
+hipError_t launch_shared_w(const AttnArgs& shared, const AttnArgs& own, const SharedCut& cut, hipStream_t stream) {
+    const int shared_units = cut.row_tiles * cut.splits, units = shared_units + own.B * cut.own_row_tiles * cut.own_splits;
+    const dim3 grid((unsigned)(units * shared.c.heads)), block(kThreads);
+    if (cut.sets == 1) {
+        kv4_attn_shared_kernel<D, kWide, 1><<<grid, block, 0, stream>>>(shared, own, shared_units);
+    } else if (cut.sets == 2) {
+        kv4_attn_shared_kernel<D, kWide, 2><<<grid, block, 0, stream>>>(shared, own, shared_units);
+    } else {
+        if constexpr (D < 256) kv4_attn_shared_kernel<D, kWide, 4><<<grid, block, 0, stream>>>(shared, own, shared_units);
+    }
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    const dim3 join((unsigned)(cut.blocks * Rows<D, 1>::kPieces * shared.c.heads));
+    kv4_attn_shared_join_kernel<D><<<join, block, 0, stream>>>(shared, own.part_o, own.part_ml, own.splits);
+    return hipGetLastError();
+}
+template <int D>
+hipError_t launch_shared(const AttnArgs& shared, const AttnArgs& own, const SharedCut& cut, hipStream_t stream) {
+    return own.c.shift >= 5 ? launch_shared_w<D, true>(shared, own, cut, stream) : launch_shared_w<D, false>(shared, own, cut, stream);
+}
+
+}  // namespace
+
+size_t kv4_attn_workspace_bytes(const w4_attn_args& a, const w4_kv4_cache& c) {
+    const int splits = cut_of(a, c).splits;
+    if (splits == 1) return 0;
+    return (size_t)a.T * a.q_heads * splits * (c.head_dim + 2) * sizeof(float);
+}
+
+hipError_t launch_kv4_attn(const w4_attn_args& a, const w4_kv4_cache& c, void* workspace, hipStream_t stream) {
     AttnArgs k = args_of(a, c);
-    const Cut cut = cut_of(behind(a, tiles), c);
+    const Cut cut = cut_of(a, c);
     k.row_tiles = cut.row_tiles;
     k.splits = cut.splits;
     k.in_turn = cut.many && (int64_t)a.B * c.kv_heads * k.row_tiles * k.splits <= 512;
-    k.shared_tiles = tiles;
-    k.part0 = before;
-    set_parts(k, a, c, workspace, before + cut.splits);
+    if (k.splits > 1) {
+        k.part_o = static_cast<float*>(workspace);
+        k.part_ml = k.part_o + (size_t)a.T * a.q_heads * k.splits * c.head_dim;
+    }
     const int64_t groups = (int64_t)a.B * c.kv_heads * k.row_tiles * k.splits;
     switch (c.head_dim) {
         case 64: return launch_w<64>(k, cut, groups, stream);
@@ -1671,89 +1963,37 @@ hipError_t launch_own(const w4_attn_args& a, const w4_kv4_cache& c, void* worksp
     }
 }
 
-// How the tiles that all requests share are cut.
-struct SharedCut {
-    int tiles;   // whole tiles of the prefix; the rest of it is done with each request's own tokens
-    int splits;  // workgroups that share a row tile's tokens; 0: nothing is done apart
-    bool many;   // kv4_attn_many_kernel
-    int row_tiles;
-    Cut own;     // of the tokens behind
-};
-SharedCut shared_cut_of(const w4_attn_args& a, int prefix, const w4_kv4_cache& c) {
-    SharedCut k = {};
-    k.tiles = prefix / kTile;
-    if (k.tiles == 0 || a.T < 2) return k;
-    // a join workgroup a row of every request
-    if ((int64_t)a.B * a.max_q * a.q_heads > (1 << 23) || (int64_t)a.T * a.q_heads > (1 << 23)) return k;
-    k.own = cut_of(behind(a, k.tiles), c);
-    const int64_t rows = (int64_t)a.T * (a.q_heads / c.kv_heads);
-    const int64_t many_rows = 64 * many_blocks(c.head_dim);
-    k.many = rows > many_rows / 2;
-    const int64_t tile = k.many ? many_rows : 16;
-    k.row_tiles = (int)((rows + tile - 1) / tile);
-    const int64_t groups = (int64_t)c.kv_heads * k.row_tiles;
-    int64_t want = 512 / groups;
-    const int64_t most = k.many ? k.tiles / 2 : k.tiles / (2 * kFewWaves);
-    want = want < most ? want : most;
-    if (want > kMaxSplits - k.own.splits) want = kMaxSplits - k.own.splits;
-    k.splits = (int)(want < 1 ? 1 : want);
-    if (k.own.splits + k.splits > kMaxSplits) k.splits = 0;
-    return k;
-}
-
-template <int D>
-hipError_t launch_shared(const AttnArgs& k, const SharedCut& cut, dim3 grid, hipStream_t stream) {
-    const auto launch = [&](auto wide) {
-        constexpr bool kWide = decltype(wide)::value;
-        if (cut.many) {
-            kv4_attn_many_kernel<D, many_blocks(D), kWide, true><<<grid, dim3(256), 0, stream>>>(k);
-        } else {
-            kv4_attn_kernel<D, 1, kFewWaves, kWide, true><<<grid, dim3(256), 0, stream>>>(k);
-        }
-        return hipGetLastError();
-    };
-    return k.c.shift >= 5 ? launch(std::true_type{}) : launch(std::false_type{});
-}
-
-}  // namespace
-
-size_t kv4_attn_workspace_bytes(const w4_attn_args& a, const w4_kv4_cache& c) {
-    const int splits = cut_of(a, c).splits;
-    if (splits == 1) return 0;
-    return part_bytes(a, c, splits);
-}
-
-hipError_t launch_kv4_attn(const w4_attn_args& a, const w4_kv4_cache& c, void* workspace, hipStream_t stream) {
-    return launch_own(a, c, workspace, 0, 0, stream);
-}
-
 size_t kv4_attn_shared_workspace_bytes(const w4_attn_args& a, int prefix, const w4_kv4_cache& c) {
     const SharedCut cut = shared_cut_of(a, prefix, c);
-    return cut.splits == 0 ? kv4_attn_workspace_bytes(a, c) : part_bytes(a, c, cut.splits + cut.own.splits);
+    return cut.splits == 0 ? kv4_attn_workspace_bytes(a, c) : shared_space_of(a, c, cut).all * sizeof(float);
 }
 
 hipError_t launch_kv4_attn_shared(const w4_attn_args& a, const int32_t* prefix_table, int prefix, const w4_kv4_cache& c,
                                   void* workspace, hipStream_t stream) {
     const SharedCut cut = shared_cut_of(a, prefix, c);
     if (cut.splits == 0) return launch_kv4_attn(a, c, workspace, stream);
-    AttnArgs k = args_of(a, c);
-    k.table = prefix_table;
-    k.width = (prefix + c.block_size - 1) / c.block_size;
-    k.requests = a.B;
-    k.B = 1;
-    k.row_tiles = cut.row_tiles;
-    k.splits = cut.splits;
-    k.shared_tiles = cut.tiles;
-    set_parts(k, a, c, workspace, cut.splits + cut.own.splits);
-    const dim3 grid((unsigned)((int64_t)c.kv_heads * cut.row_tiles * cut.splits));
-    hipError_t err;
+    const SharedSpace space = shared_space_of(a, c, cut);
+    float* const base = static_cast<float*>(workspace);
+    AttnArgs own = args_of(a, c);
+    own.shared_tiles = cut.tiles;
+    own.requests = a.B;
+    AttnArgs shared = own;
+    own.row_tiles = cut.own_row_tiles;
+    own.splits = cut.own_splits;
+    own.part_o = base + space.own_o;
+    own.part_ml = base + space.own_ml;
+    shared.table = prefix_table;
+    shared.width = (prefix + c.block_size - 1) / c.block_size;
+    shared.B = 1;
+    shared.row_tiles = cut.row_tiles;
+    shared.splits = cut.splits;
+    shared.part_o = base;
+    shared.part_ml = base + space.ml;
     switch (c.head_dim) {
-        case 64: err = launch_shared<64>(k, cut, grid, stream); break;
-        case 128: err = launch_shared<128>(k, cut, grid, stream); break;
-        default: err = launch_shared<256>(k, cut, grid, stream); break;
+        case 64: return launch_shared<64>(shared, own, cut, stream);
+        case 128: return launch_shared<128>(shared, own, cut, stream);
+        default: return launch_shared<256>(shared, own, cut, stream);
     }
-    if (err != hipSuccess) return err;
-    return launch_own(a, c, workspace, cut.tiles, cut.splits, stream);
 }
 
 }  // namespace w4

@@ -72,26 +72,53 @@ def expect(cache, q, table, lens, q_start, dim, window=0, sinks=0):
     return ref.attention(q, cache, table, lens, q_start, float(np.float32(1 / np.sqrt(dim))), window, sinks, 2.0 ** -16)
 
 
-CASES = [  # prefix, lens, news, hq, hkv, dim, block, window, sinks
-    (32, [33, 40], [1, 1], 2, 1, 64, 16, 0, 0), (64, [65, 100, 200], [1] * 3, 8, 2, 128, 16, 0, 0),
-    (48, [60, 49, 300], [1] * 3, 4, 2, 64, 16, 0, 0),                       # half a tile of the prefix is each one's own
-    (1024, [1030, 1100, 1024, 1500], [1] * 4, 16, 8, 256, 64, 0, 0),
-    (640, [700] * 9, [1] * 9, 64, 8, 64, 64, 0, 0), (320, [330, 400] * 20, [1] * 40, 8, 2, 256, 32, 0, 0),
-    (512, [600, 513] * 18, [1] * 36, 20, 1, 128, 128, 0, 0),                # twenty heads to a key head
-    (256, [300, 270, 290], [5, 1, 3], 6, 2, 128, 32, 0, 0), (256, [400] * 4, [33, 1, 70, 2], 4, 2, 256, 64, 0, 0),
-    (2048, [2049] * 12, [1] * 12, 8, 8, 64, 256, 0, 0), (160, [10, 200, 0, 160, 161], [1, 1, 0, 1, 1], 8, 2, 128, 32, 0, 0),
-    (160, [5, 200, 100], [9, 4, 20], 4, 2, 64, 32, 0, 0),                   # rows that see nothing, requests inside the prefix
-    (512, [700, 520, 900], [1] * 3, 8, 2, 128, 64, 300, 0), (512, [700, 520, 900] * 14, [1] * 42, 8, 2, 128, 64, 100, 4),
-    (512, [530, 520, 900], [1, 7, 40], 6, 1, 256, 16, 40, 33), (512, [1000] * 40, [1] * 40, 4, 2, 64, 64, 64, 100),
-    (96, [4000, 100], [1, 1], 4, 1, 128, 32, 0, 0),                         # own tokens far outnumber the shared
+def apart(prefix, lens, news, hq, hkv, dim, block, window=0, sinks=0):
+    """Whether a call does the shared tokens apart: its workspace then differs from the attention's."""
+    c = w4.step._CacheStruct(16, 16, 16, 16, 1 << 15, block, hkv, dim)
+    fake = type("Cache", (), {"ref": w4.step.ctypes.byref(c)})()
+    args = (sum(news), len(lens), hq, max(news), max(lens))
+    return (w4.w4_kv4_attn_shared_workspace_bytes(fake, *args, prefix, window, sinks) !=
+            w4.w4_kv4_attn_workspace_bytes(fake, *args, window, sinks))
+
+
+TOGETHER = [  # prefix, lens, news, hq, hkv, dim, block, window, sinks
+    (560, [561, 600, 575] * 16, [1] * 48, 8, 8, 64, 16, 0, 0),               # half a tile of the prefix is each one's own
+    (1024, [1025] * 50, [1] * 50, 16, 8, 64, 32, 0, 0), (3904, [3950, 3905, 4100] * 17, [1] * 51, 64, 8, 64, 64, 0, 0),
+    (896, [900, 1000] * 20, [1] * 40, 8, 4, 128, 64, 0, 0), (848, [850, 900, 1400] * 14, [1] * 42, 8, 4, 128, 16, 0, 0),
+    (1024, [1030, 2000, 1024, 1500] * 6, [1] * 24, 16, 8, 256, 64, 0, 0), (720, [721, 800] * 12, [1] * 24, 16, 8, 256, 16, 0, 0),
+    (4096, [4200] * 9, [1] * 9, 8, 8, 256, 256, 0, 0), (2112, [2150, 2113] * 16, [1] * 32, 128, 8, 128, 128, 0, 0),  # 16 rows a request
+    (1888, [1900] * 18, [1] * 18, 160, 8, 128, 64, 0, 0),                    # 20
+    (4160, [4200, 4170, 4300] * 4, [5, 1, 3] * 4, 16, 8, 128, 32, 0, 0), (2080, [2200] * 18, [8, 1, 7, 2, 8, 3] * 3, 24, 8, 256, 16, 0, 0),
+    (1024, [10, 1200, 0, 1024, 1025, 31] * 7, [1, 1, 0, 1, 1, 1] * 7, 8, 4, 128, 32, 0, 0),  # requests inside the prefix, empty ones
+    (1760, [5, 1900, 1800] * 8, [9, 4, 1] * 8, 8, 8, 128, 32, 0, 0),         # rows that see nothing
+    (1024, [1100, 1030, 1500] * 12, [1] * 36, 8, 4, 128, 64, 300, 0), (1024, [1100, 1030, 1500] * 12, [1] * 36, 8, 4, 128, 16, 100, 4),
+    (1024, [1100, 1030, 1500] * 8, [1] * 24, 16, 8, 256, 64, 1050, 33), (2048, [2050, 2300] * 16, [1, 2] * 16, 8, 8, 64, 64, 2100, 700),
+    (1024, [1040, 5000] * 10, [1] * 20, 8, 8, 128, 64, 0, 0),                # own tokens in splits of their own
 ]
 
 
-@pytest.mark.parametrize("prefix,lens,news,hq,hkv,dim,block,window,sinks", CASES)
+@pytest.mark.parametrize("prefix,lens,news,hq,hkv,dim,block,window,sinks", TOGETHER)
 def test_attn_shared(prefix, lens, news, hq, hkv, dim, block, window, sinks):
+    assert apart(prefix, lens, news, hq, hkv, dim, block, window, sinks)
     cache, shared, table, q_start, q = case(1, prefix, lens, news, hq, hkv, dim, block)
     got = run(to_device(cache), q, table, lens, q_start, shared, prefix, window=window, sinks=sinks)
     check_attn(got, *expect(cache, q, table, lens, q_start, dim, window, sinks))
+
+
+@pytest.mark.parametrize("prefix,lens,news,hq,hkv,dim,block,window,sinks", [
+    (32, [33, 40], [1, 1], 2, 1, 64, 16, 0, 0), (48, [60, 49, 300], [1] * 3, 4, 2, 64, 16, 0, 0),
+    (1024, [1030, 1100, 1024, 1500], [1] * 4, 16, 8, 256, 64, 0, 0), (256, [400] * 4, [33, 1, 70, 2], 4, 2, 256, 64, 0, 0),
+    (160, [10, 200, 0, 160, 161], [1, 1, 0, 1, 1], 8, 2, 128, 32, 0, 0), (512, [700, 520, 900], [1] * 3, 8, 2, 128, 64, 300, 4),
+])
+def test_attn_shared_of_few_requests(prefix, lens, news, hq, hkv, dim, block, window, sinks):
+    """Where it does not pay, the tokens are read through each request's table as ever."""
+    assert not apart(prefix, lens, news, hq, hkv, dim, block, window, sinks)
+    cache, shared, table, q_start, q = case(1, prefix, lens, news, hq, hkv, dim, block)
+    dev = to_device(cache)
+    got = run(dev, q, table, lens, q_start, shared, prefix, window=window, sinks=sinks)
+    check_attn(got, *expect(cache, q, table, lens, q_start, dim, window, sinks))
+    table = np.where(table == 123456789, 0, table)
+    assert np.array_equal(got, run_attn(dev, q, table, lens, q_start, window=window, sinks=sinks))
 
 
 @pytest.mark.parametrize("prefix", [0, 1, 31])
@@ -105,20 +132,22 @@ def test_attn_shared_without_a_whole_tile_is_the_attention(prefix):
 
 @pytest.mark.parametrize("rows", [2, 40])
 def test_attn_shared_without_q_start_strided_and_with_rows_behind(rows):
-    lens = [300 + 3 * i for i in range(rows)]
-    cache, shared, table, q_start, q = case(3, 256, lens, [1] * rows, 8, 2, 128, 64)
+    lens = [930 + 3 * i for i in range(rows)]
+    assert apart(900, lens, [1] * rows, 8, 4, 128, 64) == (rows == 40)
+    cache, shared, table, q_start, q = case(3, 900, lens, [1] * rows, 8, 4, 128, 64)
     dev = to_device(cache)
-    want = run(dev, q, table, lens, q_start, shared, 256)
+    want = run(dev, q, table, lens, q_start, shared, 900)
     check_attn(want, *expect(cache, q, table, lens, q_start, 128))
-    assert np.array_equal(run(dev, q, table, lens, None, shared, 256, pad=24), want)
-    got = run(dev, q, table, lens, q_start, shared, 256, pad=8, tail=3)
+    assert np.array_equal(run(dev, q, table, lens, None, shared, 900, pad=24), want)
+    got = run(dev, q, table, lens, q_start, shared, 900, pad=8, tail=3)
     assert np.all(got[rows:] == 7.0)
     check_attn(got[:rows], *expect(cache, q, table, lens, q_start, 128))
 
 
 def test_attn_shared_is_right_for_any_max_kv():
-    lens = [700, 650, 1200]
-    cache, shared, table, q_start, q = case(4, 640, lens, [1] * 3, 8, 2, 64, 64)
+    lens = [700, 650, 1200] * 20
+    assert apart(640, lens, [1] * 60, 8, 8, 64, 64)
+    cache, shared, table, q_start, q = case(4, 640, lens, [1] * 60, 8, 8, 64, 64)
     dev = to_device(cache)
     want = expect(cache, q, table, lens, q_start, 64)
     for max_kv in (0, 1, 640, 641, 100000, 2 ** 31 - 1):
@@ -128,25 +157,30 @@ def test_attn_shared_is_right_for_any_max_kv():
 @pytest.mark.parametrize("rows", [3, 50])
 def test_attn_shared_bad_pages_and_odd_values(rows):
     """A page out of range makes NaN of the rows that see it and of no other; what no row sees may hold anything."""
-    lens = [100 + 4 * i for i in range(rows)]
-    lens[0] = 70  # inside the prefix: sees tokens 0 .. 69
-    cache, shared, table, q_start, q = case(5, 96, lens, [1] * rows, 4, 2, 128, 16)
+    prefix, last = 704, 43  # pages of 16, 22 tiles
+    lens = [708 + 4 * i for i in range(rows)]
+    lens[0] = 678  # inside the prefix: sees tokens 0 .. 677
+    make = lambda: case(5, prefix, lens, [1] * rows, 8, 4, 128, 16)  # noqa: E731
+    assert apart(prefix, lens, [1] * rows, 8, 4, 128, 16) == (rows == 50)
+    cache, shared, table, q_start, q = make()
     want = expect(cache, q, table, lens, q_start, 128)
-    cache.k_meta[shared[5], :, :, 15] = np.nan  # token 95: seen by all but the first
-    cache.v_meta[shared[4], :, :, 7:] = np.inf  # tokens 71 on
-    got = run(to_device(cache), q, table, lens, q_start, shared, 96)
+    cache.k_meta[shared[last], :, :, 15] = np.nan  # token 703: seen by all but the first
+    cache.v_meta[shared[last - 1], :, :, 6:] = np.inf  # tokens 678 on
+    got = run(to_device(cache), q, table, lens, q_start, shared, prefix)
     check_attn(got[:1], want[0][:1], want[1][:1])
     assert np.all(np.isnan(got[1:]))
-    cache, shared, table, q_start, q = case(5, 96, lens, [1] * rows, 4, 2, 128, 16)
+    cache, shared, table, q_start, q = make()
     for bad in (-1, 10 ** 6):
         broken = shared.copy()
-        broken[5] = bad
-        got = run(to_device(cache), q, table, lens, q_start, broken, 96)
+        broken[last] = bad
+        both = table.copy()
+        both[:, last] = bad  # the rows of the table hold the prefix's pages too
+        got = run(to_device(cache), q, both, lens, q_start, broken, prefix)
         check_attn(got[:1], want[0][:1], want[1][:1])
         assert np.all(np.isnan(got[1:]))
     own = table.copy()
-    own[1, 6] = -1  # a request's own first page
-    got = run(to_device(cache), q, own, lens, q_start, shared, 96)
+    own[1, last + 1] = -1  # a request's own first page
+    got = run(to_device(cache), q, own, lens, q_start, shared, prefix)
     assert np.all(np.isnan(got[1]))
     rest = [i for i in range(rows) if i != 1]
     check_attn(got[rest], want[0][rest], want[1][rest])
@@ -154,22 +188,25 @@ def test_attn_shared_bad_pages_and_odd_values(rows):
 
 def test_attn_shared_table_that_ends_with_the_prefix():
     """No page of a request's own in the table: a row past the prefix is NaN, one inside it is not."""
-    lens = [64, 65, 40]
-    cache, shared, table, q_start, q = case(6, 64, lens, [1] * 3, 4, 2, 64, 32)
-    want = expect(cache, q, table, lens, q_start, 64)
-    for width in (2, 0):
-        got = run(to_device(cache), q, table[:, :width], lens, q_start, shared, 64)
-        check_attn(got[[0, 2]], want[0][[0, 2]], want[1][[0, 2]])
-        assert np.all(np.isnan(got[1]))
+    lens = [1024, 1025, 40] * 10
+    assert apart(1024, lens, [1] * 30, 8, 8, 128, 32)
+    cache, shared, table, q_start, q = case(6, 1024, lens, [1] * 30, 8, 8, 128, 32)
+    want = expect(cache, q, table, lens, q_start, 128)
+    inside = [i for i in range(30) if i % 3 != 1]
+    for width in (32, 0):
+        got = run(to_device(cache), q, table[:, :width], lens, q_start, shared, 1024)
+        check_attn(got[inside], want[0][inside], want[1][inside])
+        assert np.all(np.isnan(got[1::3]))
 
 
 def test_attn_shared_graph_replays_with_growing_requests():
     """Two captured calls over one workspace, replayed in turn; each request grows between, its table in place."""
-    lens, B, hq, dim, prefix = [321, 330, 350, 400, 322], 5, 8, 128, 320
-    cache, shared, table, q_start, q = case(7, prefix, [n + 40 for n in lens], [1] * B, hq, 2, dim, 32)
+    lens, B, hq, dim, prefix = [721, 730, 750, 800, 722] * 10, 50, 8, 128, 704
+    assert apart(prefix, lens, [1] * B, hq, 4, dim, 32)
+    cache, shared, table, q_start, q = case(7, prefix, [n + 40 for n in lens], [1] * B, hq, 4, dim, 32)
     dev = to_device(cache)
     stream = torch.cuda.Stream()
-    size = w4.w4_kv4_attn_shared_workspace_bytes(dev, B, B, hq, 1, 500, prefix)
+    size = w4.w4_kv4_attn_shared_workspace_bytes(dev, B, B, hq, 1, 900, prefix)
     work = torch.full((size // 4,), float("nan"), dtype=torch.float32, device=DEV)
     dev_q = [host.bf16_tensor(q), host.bf16_tensor(q[::-1].copy())]
     dev_lens, dev_table, dev_shared = ints(lens), ints(table), ints(shared)
@@ -178,7 +215,7 @@ def test_attn_shared_graph_replays_with_growing_requests():
     for x, out in zip(dev_q, outs):
         w4.w4_graph_begin(stream)
         try:
-            w4.w4_kv4_attn_shared(x, dev, dev_table, dev_lens, out, dev_shared, prefix, max_kv=500, workspace=work, stream=stream)
+            w4.w4_kv4_attn_shared(x, dev, dev_table, dev_lens, out, dev_shared, prefix, max_kv=900, workspace=work, stream=stream)
         finally:
             graphs.append(w4.w4_graph_end(stream))
     for k in range(4):
@@ -196,7 +233,8 @@ def test_attn_shared_graph_replays_with_growing_requests():
 
 def test_attn_shared_repeats_its_bits_on_another_stream():
     lens = [1100 + i for i in range(30)]
-    cache, shared, table, q_start, q = case(8, 1024, lens, [1] * 30, 16, 4, 64, 64)
+    assert apart(1024, lens, [1] * 30, 8, 8, 64, 64)
+    cache, shared, table, q_start, q = case(8, 1024, lens, [1] * 30, 8, 8, 64, 64)
     dev = to_device(cache)
     want = run(dev, q, table, lens, q_start, shared, 1024)
     side = torch.cuda.Stream()
