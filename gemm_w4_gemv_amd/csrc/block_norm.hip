@@ -22,49 +22,56 @@ namespace {
 __device__ __forceinline__ double of_words(uint32_t lo, uint32_t hi) {
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
+// As swap_pair_sum: a's sum over the lane pair in lanes whose bit kOff is clear, b's in the others.
 template <int kOff>
-__device__ __forceinline__ double pair_sum64(double v) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32);
-    if constexpr (kOff >= 16) {
-        uint32_t l0, l1, h0, h1;
-        if constexpr (kOff == 32) {
-            const auto l = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
-            const auto h = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
-            l0 = l[0], l1 = l[1], h0 = h[0], h1 = h[1];
-        } else {
-            const auto l = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
-            const auto h = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
-            l0 = l[0], l1 = l[1], h0 = h[0], h1 = h[1];
-        }
-        return of_words(l0, h0) + of_words(l1, h1);
+__device__ __forceinline__ double swap_pair_sum64(double a, double b) {
+    const uint64_t x = __builtin_bit_cast(uint64_t, a), y = __builtin_bit_cast(uint64_t, b);
+    uint32_t l0, l1, h0, h1;
+    if constexpr (kOff == 32) {
+        const auto l = __builtin_amdgcn_permlane32_swap((uint32_t)x, (uint32_t)y, false, false);
+        const auto h = __builtin_amdgcn_permlane32_swap((uint32_t)(x >> 32), (uint32_t)(y >> 32), false, false);
+        l0 = l[0], l1 = l[1], h0 = h[0], h1 = h[1];
     } else {
-        const float l = dpp_partner<kOff>(__builtin_bit_cast(float, lo)), h = dpp_partner<kOff>(__builtin_bit_cast(float, hi));
-        return v + of_words(__builtin_bit_cast(uint32_t, l), __builtin_bit_cast(uint32_t, h));
+        const auto l = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)y, false, false);
+        const auto h = __builtin_amdgcn_permlane16_swap((uint32_t)(x >> 32), (uint32_t)(y >> 32), false, false);
+        l0 = l[0], l1 = l[1], h0 = h[0], h1 = h[1];
+    }
+    return of_words(l0, h0) + of_words(l1, h1);
+}
+// Sum over the lanes that differ in bits kFrom, kFrom / 2, .. 1 (kFrom at most 16).
+template <int kFrom>
+__device__ __forceinline__ double low_sum64(double v) {
+    if constexpr (kFrom == 16) {
+        return low_sum64<8>(swap_pair_sum64<16>(v, v));
+    } else if constexpr (kFrom >= 1) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32);
+        const float l = dpp_partner<kFrom>(__builtin_bit_cast(float, lo)), h = dpp_partner<kFrom>(__builtin_bit_cast(float, hi));
+        return low_sum64<kFrom / 2>(v + of_words(__builtin_bit_cast(uint32_t, l), __builtin_bit_cast(uint32_t, h)));
+    } else {
+        return v;
     }
 }
-__device__ __forceinline__ double wave_sum(double v) {
-    v = pair_sum64<32>(v);
-    v = pair_sum64<16>(v);
-    v = pair_sum64<8>(v);
-    v = pair_sum64<4>(v);
-    v = pair_sum64<2>(v);
-    return pair_sum64<1>(v);
+template <int kLane>
+__device__ __forceinline__ double lane_of(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return of_words(__builtin_amdgcn_readlane((uint32_t)b, kLane), __builtin_amdgcn_readlane((uint32_t)(b >> 32), kLane));
 }
 
-// Sum over the kWaves waves of a team, in wave order; ``box`` is LDS of the
-// team's own for this one sum (a second sum before the next barrier needs
-// another).  All teams of a workgroup must come here together.
+// Two sums over the kWaves waves of a team at once: lanes 0 .. 31 take a's, the
+// others b's.  ``box`` is LDS of the team's own for these; its next use must be
+// behind another barrier than this one.  All teams of a workgroup must come here
+// together.
 template <int kWaves>
-__device__ __forceinline__ double team_sum(double v, double* box, int wave) {
-    v = wave_sum(v);
-    if constexpr (kWaves == 1) return v;
-    box[wave] = v;  // every lane holds the sum; one address, one value
-    __syncthreads();
-    v = box[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) v += box[w];
-    return v;
+__device__ __forceinline__ void team_sums(double& a, double& b, double (*box)[2], int wave, int lane) {
+    double v = low_sum64<16>(swap_pair_sum64<32>(a, b));
+    if constexpr (kWaves > 1) {
+        box[wave][lane >> 5] = v;  // 32 lanes hold a sum; one address, one value
+        __syncthreads();
+        v = low_sum64<kWaves / 2>(box[lane & (kWaves - 1)][lane >> 5]);
+    }
+    a = lane_of<0>(v);
+    b = lane_of<32>(v);
 }
 
 // 1 / sqrt(m) as two factors: neither the squares of large values nor those of
@@ -112,21 +119,64 @@ struct Raw {
         }
     }
 };
-template <bool kF32>
+template <bool kApart, typename T>
+__device__ __forceinline__ void put(T* p, const T& v) {
+    if constexpr (kApart) {
+        __builtin_nontemporal_store(v, p);
+    } else {
+        *p = v;
+    }
+}
+template <bool kF32, bool kApart = false>
 __device__ __forceinline__ void store(void* p, int64_t at, const f32x8_t& v) {
     if constexpr (kF32) {
         f32x4_t* q = reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + at);
-        q[0] = f32x4_t{v[0], v[1], v[2], v[3]};
-        q[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+        put<kApart>(q, f32x4_t{v[0], v[1], v[2], v[3]});
+        put<kApart>(q + 1, f32x4_t{v[4], v[5], v[6], v[7]});
     } else {
-        *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p) + at) = narrow(v);
+        put<kApart>(reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p) + at), narrow(v));
     }
 }
 
-__device__ __forceinline__ double squares(const f32x8_t& v, double s) {
+// A lane's sums of x^2 and x y over its values, of a row (there(c): the lane has a
+// chunk c).  In FP32, if the squares of no lane of the wave come near to what FP32
+// holds, which is all but always so, and a third of the time of FP64.
+template <int kChunks, typename X, typename Y, typename F>
+__device__ __forceinline__ void products(double& xx, double& xy, X x, Y y, F there) {
+    float s = 0, m = 0;
+    bool any = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fma((double)v[i], (double)v[i], s);
-    return s;
+    for (int c = 0; c < kChunks; ++c) {
+        if (!there(c)) continue;
+        any = true;
+        const f32x8_t v = x(c), w = y(c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s = fmaf(v[i], v[i], s);
+            m = fmaf(v[i], w[i], m);
+        }
+    }
+    xx = s;
+    xy = m;
+    const bool plain = s > 0x1p-40f && s < 0x1p100f && m < INFINITY && m > -INFINITY;
+    if (!__any(any && !plain)) return;
+    xx = xy = 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        if (!there(c)) continue;
+        const f32x8_t v = x(c), w = y(c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            xx = fma((double)v[i], (double)v[i], xx);
+            xy = fma((double)v[i], (double)w[i], xy);
+        }
+    }
+}
+template <int kChunks, typename X, typename F>
+__device__ __forceinline__ double squares(X x, F there) {
+    double xx, unused;
+    products<kChunks>(xx, unused, x, x, there);
+    return xx;
 }
 
 // A team of kWaves waves holds a row, kChunks times 8 values a lane; small
@@ -137,30 +187,33 @@ constexpr int teams() {
 }
 
 // ------------------------------------------------------------------ forward
-template <int kWaves, int kChunks, bool kF32>
+// kApart: results go past the caches' ways of keeping them.  4099 rows of 3840: 28
+// us without, 21.5 with; a row later read by another norm, 256 rows 9.1 and 8.3, 64
+// rows 7.3 and 7.5.
+template <int kWaves, int kChunks, bool kF32, bool kApart>
 __global__ __launch_bounds__(kWaves* teams<kWaves>() * kWave) void block_norm_kernel(w4_norm_args a) {
     constexpr int kTeams = teams<kWaves>(), kLanes = kWaves * kWave;
-    __shared__ double box[2][kTeams][kWaves];
+    __shared__ double box[2][kTeams][kWaves][2];
     const int team = kTeams == 1 ? 0 : (int)sgpr(threadIdx.x / kLanes);
-    const int tid = threadIdx.x % kLanes, wave = tid / kWave;
+    const int tid = threadIdx.x % kLanes, wave = tid / kWave, lane = tid % kWave;
     const int64_t t = (int64_t)blockIdx.x * kTeams + team;
     // a team of one wave meets no other; larger ones have the workgroup to themselves
     if (t >= a.T) return;
 
-    const int64_t last = a.D;
+    const auto there = [&](int c) { return (c * kLanes + tid) * 8 < a.D; };
     Raw<kF32> h[kChunks];
     Raw<false> y[kChunks], wy[kChunks], wz[kChunks], g[kChunks];
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
         const int64_t d = (c * kLanes + tid) * 8;
-        if (d >= last) continue;
+        if (!there(c)) continue;
         if (a.y) y[c].load(a.y, t * a.y_stride + d);
         h[c].load(a.h, t * a.h_stride + d);
     }
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
         const int64_t d = (c * kLanes + tid) * 8;
-        if (d >= last) continue;
+        if (!there(c)) continue;
         if (a.y_weight) wy[c].load(a.y_weight, d);
         if (a.gate) g[c].load(a.gate, t * a.gate_stride + d);
         if (a.z_weight) wz[c].load(a.z_weight, d);
@@ -169,17 +222,13 @@ __global__ __launch_bounds__(kWaves* teams<kWaves>() * kWave) void block_norm_ke
     f32x8_t x[kChunks];  // h'
     Inverse r1 = {1.0f, 1.0f};
     if (a.y && a.y_weight) {
-        double s = 0;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-            if ((c * kLanes + tid) * 8 < last) s = squares(y[c].values(), s);
-        r1 = inverse_root(team_sum<kWaves>(s, box[0][team], wave) / a.D + (double)a.eps);
+        double s = squares<kChunks>([&](int c) { return y[c].values(); }, there), unused = 0;
+        team_sums<kWaves>(s, unused, box[0][team], wave, lane);
+        r1 = inverse_root(s / a.D + (double)a.eps);
     }
-    double s = 0;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-        const int64_t d = (c * kLanes + tid) * 8;
-        if (d >= last) continue;
+        if (!there(c)) continue;
         x[c] = h[c].values();
         if (a.y) {
             f32x8_t u = y[c].values();
@@ -191,32 +240,43 @@ __global__ __launch_bounds__(kWaves* teams<kWaves>() * kWave) void block_norm_ke
             if (a.gate) u *= g[c].values();
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[c][i] = fmaf(a.residual_scale, x[c][i], a.branch_scale * u[i]);
-            if (a.h_out) store<kF32>(a.h_out, t * a.h_out_stride + d, x[c]);
+            if (a.h_out) store<kF32, kApart>(a.h_out, t * a.h_out_stride + (c * kLanes + tid) * 8, x[c]);
         }
-        if (a.z && a.z_weight) s = squares(x[c], s);
     }
     if (!a.z) return;
     Inverse r2 = {1.0f, 1.0f};
-    if (a.z_weight) r2 = inverse_root(team_sum<kWaves>(s, box[1][team], wave) / a.D + (double)a.eps);
+    if (a.z_weight) {
+        double s = squares<kChunks>([&](int c) { return x[c]; }, there), unused = 0;
+        team_sums<kWaves>(s, unused, box[1][team], wave, lane);
+        r2 = inverse_root(s / a.D + (double)a.eps);
+    }
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-        const int64_t d = (c * kLanes + tid) * 8;
-        if (d >= last) continue;
+        if (!there(c)) continue;
         f32x8_t v = x[c];
         if (a.z_weight) {
             const f32x8_t w = wz[c].values();
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = r2.of(v[i]) * (w[i] + a.weight_add);
         }
-        store<false>(a.z, t * a.z_stride + d, v);
+        store<false, kApart>(a.z, t * a.z_stride + (c * kLanes + tid) * 8, v);
     }
 }
 
 // ----------------------------------------------------------------- gradient
-// Sums over the rows are taken in two steps: a workgroup adds its run of rows
-// in registers, row by row, and a second kernel adds the workgroups' sums, so
-// that no atomic decides their order.
-constexpr int kRuns = 512;
+// A workgroup of eight waves (sixteen for the longest rows), in teams of as many as a
+// row takes, goes over a run of rows.  The next row is on its way while one is worked on: a row is four
+// sums over it, two of which can wait for the others, so a row costs two
+// barriers; the sum of the next row's y^2 goes with the second.
+//
+//   first   sum h'^2 and sum g2 h'   (g2 = dz w2: mean(g2 n2) = r2 mean(g2 h'))
+//   second  sum g1 n1 of this row, sum y^2 of the next
+//
+// Sums over the rows are taken in three steps, none of whose order is left to
+// chance: a lane adds its columns row by row, the teams join in LDS, and a second
+// kernel adds the workgroups' sums in FP64.
+constexpr int kRuns = 256;
+constexpr int kRunWaves = 16;  // of block_norm_runs_kernel
 
 struct GradArgs {
     w4_norm_args a;
@@ -226,179 +286,202 @@ struct GradArgs {
 };
 
 template <int kWaves, int kChunks, bool kF32>
-__global__ __launch_bounds__(kWaves* kWave) void block_norm_grad_kernel(GradArgs k) {
-    constexpr int kLanes = kWaves * kWave;
-    __shared__ double box[4][kWaves];
+__global__ __launch_bounds__((kWaves > 8 ? kWaves : 8) * kWave) void block_norm_grad_kernel(GradArgs k) {
+    constexpr int kLanes = kWaves * kWave, kTeams = kWaves > 8 ? 1 : 8 / kWaves;
+    constexpr f32x8_t kZero = {0, 0, 0, 0, 0, 0, 0, 0};
+    __shared__ double box[2][kTeams][kWaves][2];
+    __shared__ f32x8_t join[kTeams == 1 ? 1 : 4 * kWave][kChunks];
     const w4_norm_args& a = k.a;
     const w4_norm_grad_args& g = k.g;
-    const int tid = threadIdx.x, wave = tid / kWave, run = blockIdx.x;
+    const int team = kTeams == 1 ? 0 : (int)sgpr(threadIdx.x / kLanes);
+    const int tid = threadIdx.x % kLanes, wave = tid / kWave, lane = tid % kWave, run = blockIdx.x;
     const int64_t first = (int64_t)run * a.T / k.runs, end = (int64_t)(run + 1) * a.T / k.runs;
-    const int64_t last = a.D;
-    const bool shared_gate = a.gate && a.gate_stride == 0;
+    const bool shared_gate = a.gate && a.gate_stride == 0, normed_z = g.dz && a.z_weight;
+
+    struct Row {
+        Raw<kF32> h[kChunks], dho[kChunks];
+        Raw<false> y[kChunks], dz[kChunks];
+    };
+    const auto here = [&](int c) { return (c * kLanes + tid) * 8 < a.D; };
+    const auto fetch = [&](Row& r, int64_t t) {
+        if (t >= end) return;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int64_t d = (c * kLanes + tid) * 8;
+            if (!here(c)) continue;
+            if (a.y) r.y[c].load(a.y, t * a.y_stride + d);
+            r.h[c].load(a.h, t * a.h_stride + d);
+            if (g.dz) r.dz[c].load(g.dz, t * g.dz_stride + d);
+            if (g.dh_out) r.dho[c].load(g.dh_out, t * g.dh_out_stride + d);
+        }
+    };
+    const auto squares_of_y = [&](const Row& r, int64_t t) {
+        if (t >= end || !a.y || !a.y_weight) return 0.0;
+        return squares<kChunks>([&](int c) { return r.y[c].values(); }, here);
+    };
 
     f32x8_t sum_y[kChunks], sum_z[kChunks], sum_g[kChunks];
+    Raw<false> wy[kChunks], wz[kChunks], gate[kChunks];
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) sum_y[c] = sum_z[c] = sum_g[c] = f32x8_t{0, 0, 0, 0, 0, 0, 0, 0};
-
-    for (int64_t t = first; t < end; ++t) {
-        Raw<kF32> h[kChunks], dho[kChunks];
-        Raw<false> y[kChunks], dz[kChunks], gate[kChunks];
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int64_t d = (c * kLanes + tid) * 8;
-            if (d >= last) continue;
-            if (a.y) y[c].load(a.y, t * a.y_stride + d);
-            h[c].load(a.h, t * a.h_stride + d);
-            if (g.dz) dz[c].load(g.dz, t * g.dz_stride + d);
-            if (g.dh_out) dho[c].load(g.dh_out, t * g.dh_out_stride + d);
-            if (a.gate) gate[c].load(a.gate, t * a.gate_stride + d);
-        }
-        Inverse r1 = {1.0f, 1.0f}, r2 = {1.0f, 1.0f};
-        if (a.y && a.y_weight) {
-            double s = 0;
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-                if ((c * kLanes + tid) * 8 < last) s = squares(y[c].values(), s);
-            r1 = inverse_root(team_sum<kWaves>(s, box[0], wave) / a.D + (double)a.eps);
-        }
-        // h', and with dz the norm behind it
-        f32x8_t x[kChunks], dx[kChunks];
-        double s = 0;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int64_t d = (c * kLanes + tid) * 8;
-            if (d >= last) continue;
-            x[c] = h[c].values();
-            if (a.y) {
-                f32x8_t u = y[c].values();
-                if (a.y_weight) {
-                    Raw<false> raw;
-                    raw.load(a.y_weight, d);
-                    const f32x8_t w = raw.values();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) u[i] = r1.of(u[i]) * (w[i] + a.weight_add);
-                }
-                if (a.gate) u *= gate[c].values();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[c][i] = fmaf(a.residual_scale, x[c][i], a.branch_scale * u[i]);
-            }
-            s = squares(x[c], s);
-        }
-        if (g.dz && a.z_weight) {
-            r2 = inverse_root(team_sum<kWaves>(s, box[1], wave) / a.D + (double)a.eps);
-            double m = 0;
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                const int64_t d = (c * kLanes + tid) * 8;
-                if (d >= last) continue;
-                Raw<false> raw;
-                raw.load(a.z_weight, d);
-                const f32x8_t w = raw.values(), v = dz[c].values();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[c][i] = r2.of(x[c][i]);  // n2
-                    sum_z[c][i] = fmaf(v[i], x[c][i], sum_z[c][i]);
-                    dx[c][i] = v[i] * (w[i] + a.weight_add);
-                    m = fma((double)dx[c][i], (double)x[c][i], m);
-                }
-            }
-            const float mean = (float)(team_sum<kWaves>(m, box[2], wave) / a.D);
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dx[c][i] = r2.of(fmaf(-mean, x[c][i], dx[c][i]));
-        } else {
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) dx[c] = g.dz ? dz[c].values() : f32x8_t{0, 0, 0, 0, 0, 0, 0, 0};
-        }
-        double m = 0;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int64_t d = (c * kLanes + tid) * 8;
-            if (d >= last) continue;
-            if (g.dh_out) dx[c] += dho[c].values();
-            if (g.dh) {
-                f32x8_t v = dx[c];
-                if (a.y) v *= a.residual_scale;
-                store<kF32>(g.dh, t * g.dh_stride + d, v);
-            }
-            if (!a.y) continue;
-            f32x8_t n = y[c].values(), w, b = dx[c] * a.branch_scale;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = 1.0f;
-            if (a.y_weight) {
-                Raw<false> raw;
-                raw.load(a.y_weight, d);
-                w = raw.values();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    w[i] += a.weight_add;
-                    n[i] = r1.of(n[i]);
-                }
-            }
-            if (a.gate) {
-                f32x8_t dg;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dg[i] = b[i] * (n[i] * w[i]);
-                if (shared_gate) {
-                    sum_g[c] += dg;
-                } else if (g.d_gate) {
-                    store<false>(g.d_gate, t * g.d_gate_stride + d, dg);
-                }
-                b *= gate[c].values();
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                sum_y[c][i] = fmaf(b[i], n[i], sum_y[c][i]);
-                dx[c][i] = b[i] * w[i];
-                x[c][i] = n[i];
-                m = fma((double)dx[c][i], (double)n[i], m);
-            }
-        }
-        if (a.y && g.dy) {
-            float mean = 0;
-            if (a.y_weight) mean = (float)(team_sum<kWaves>(m, box[3], wave) / a.D);
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                const int64_t d = (c * kLanes + tid) * 8;
-                if (d >= last) continue;
-                if (a.y_weight) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) dx[c][i] = r1.of(fmaf(-mean, x[c][i], dx[c][i]));
-                }
-                store<false>(g.dy, t * g.dy_stride + d, dx[c]);
-            }
-        }
-        // the next row's first sum must not reach a box that another wave still reads
-        if constexpr (kWaves > 1) __syncthreads();
+    for (int c = 0; c < kChunks; ++c) {
+        const int64_t d = (c * kLanes + tid) * 8;
+        sum_y[c] = sum_z[c] = sum_g[c] = kZero;
+        if (!here(c)) continue;
+        if (a.y_weight) wy[c].load(a.y_weight, d);
+        if (a.z_weight) wz[c].load(a.z_weight, d);
+        if (shared_gate) gate[c].load(a.gate, d);
     }
-    const auto put = [&](int which, const f32x8_t* v) {
+
+    Row row;
+    fetch(row, first + team);
+    double sy = squares_of_y(row, first + team), unused = 0;
+    team_sums<kWaves>(sy, unused, box[1][team], wave, lane);
+    const double per = 1.0 / a.D;
+    for (int64_t t0 = first; t0 < end; t0 += kTeams) {  // every team as often: the barriers are the workgroup's
+        const int64_t t = t0 + team;
+        const bool live = t < end;
+        Row next;
+        fetch(next, t + kTeams);
+        const Inverse r1 = a.y && a.y_weight ? inverse_root(sy * per + (double)a.eps) : Inverse{1.0f, 1.0f};
+        f32x8_t n1[kChunks], x[kChunks], dx[kChunks];  // y's norm before its weight; h'; dz w2
+        double s = 0, m = 0;
+        if (live) {
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int64_t d = (c * kLanes + tid) * 8;
-            if (d < last) store<true>(k.part, ((int64_t)which * k.runs + run) * a.D + d, v[c]);
+            for (int c = 0; c < kChunks; ++c) {
+                if (!here(c)) continue;
+                x[c] = row.h[c].values();
+                if (a.gate && !shared_gate) gate[c].load(a.gate, t * a.gate_stride + (c * kLanes + tid) * 8);
+                if (a.y) {
+                    n1[c] = row.y[c].values();
+                    if (a.y_weight) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) n1[c][i] = r1.of(n1[c][i]);
+                    }
+                    f32x8_t u = n1[c];
+                    if (a.y_weight) u *= wy[c].values() + a.weight_add;
+                    if (a.gate) u *= gate[c].values();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[c][i] = fmaf(a.residual_scale, x[c][i], a.branch_scale * u[i]);
+                }
+                dx[c] = g.dz ? row.dz[c].values() : kZero;
+                if (normed_z) dx[c] *= wz[c].values() + a.weight_add;
+            }
+            if (normed_z) products<kChunks>(s, m, [&](int c) { return x[c]; }, [&](int c) { return dx[c]; }, here);
         }
+        team_sums<kWaves>(s, m, box[0][team], wave, lane);
+        const Inverse r2 = normed_z ? inverse_root(s * per + (double)a.eps) : Inverse{1.0f, 1.0f};
+        // mean(g2 n2): the sum may leave FP32 where its product with 1 / rms does not
+        const float mean2 = normed_z ? (float)(m * per * r2.power * r2.rest) : 0.0f;
+        float m1 = 0;
+        if (live) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                const int64_t d = (c * kLanes + tid) * 8;
+                if (!here(c)) continue;
+                if (normed_z) {
+                    const f32x8_t v = row.dz[c].values();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float n2 = r2.of(x[c][i]);
+                        sum_z[c][i] = fmaf(v[i], n2, sum_z[c][i]);
+                        dx[c][i] = r2.of(fmaf(-mean2, n2, dx[c][i]));
+                    }
+                }
+                if (g.dh_out) dx[c] += row.dho[c].values();
+                if (g.dh) store<kF32>(g.dh, t * g.dh_stride + d, a.y ? dx[c] * a.residual_scale : dx[c]);
+                if (!a.y) continue;
+                f32x8_t b = dx[c] * a.branch_scale;
+                if (a.gate) {
+                    f32x8_t u = n1[c];
+                    if (a.y_weight) u *= wy[c].values() + a.weight_add;
+                    u *= b;
+                    if (shared_gate) {
+                        sum_g[c] += u;
+                    } else if (g.d_gate) {
+                        store<false>(g.d_gate, t * g.d_gate_stride + d, u);
+                    }
+                    b *= gate[c].values();
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum_y[c][i] = fmaf(b[i], n1[c][i], sum_y[c][i]);
+                if (a.y_weight) b *= wy[c].values() + a.weight_add;
+                dx[c] = b;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m1 = fmaf(b[i], n1[c][i], m1);
+            }
+        }
+        m = m1;
+        sy = squares_of_y(next, t + kTeams);
+        team_sums<kWaves>(m, sy, box[1][team], wave, lane);
+        if (live && a.y && g.dy) {
+            const float mean1 = (float)(m * per);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                if (!here(c)) continue;
+                if (a.y_weight) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dx[c][i] = r1.of(fmaf(-mean1, n1[c][i], dx[c][i]));
+                }
+                store<false>(g.dy, t * g.dy_stride + (c * kLanes + tid) * 8, dx[c]);
+            }
+        }
+        row = next;
+    }
+
+    const auto put = [&](int which, f32x8_t* v) {
+        // the teams' sums, halving their number
+        if constexpr (kTeams > 1) {
+#pragma unroll
+            for (int half = kTeams / 2; half >= 1; half /= 2) {
+                __syncthreads();
+                if (team >= half && team < 2 * half) {
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) join[(team - half) * kLanes + tid][c] = v[c];
+                }
+                __syncthreads();
+                if (team < half) {
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) v[c] += join[team * kLanes + tid][c];
+                }
+            }
+            if (team != 0) return;
+        }
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+            if (here(c)) store<true>(k.part, ((int64_t)which * k.runs + run) * a.D + (c * kLanes + tid) * 8, v[c]);
     };
     if (g.d_y_weight) put(0, sum_y);
     if (g.d_z_weight) put(1, sum_z);
     if (g.d_gate && shared_gate) put(2, sum_g);
 }
 
-// Adds the runs of one column of one of the three sums, four lanes a column.
-__global__ __launch_bounds__(256) void block_norm_runs_kernel(GradArgs k) {
-    __shared__ double box[4][kWave];
+// Adds the runs of one column of one of the three sums: sixteen lanes a column,
+// all their loads at once.
+__global__ __launch_bounds__(kRunWaves * kWave) void block_norm_runs_kernel(GradArgs k) {
+    __shared__ double box[kRunWaves][kWave];
     float* out[3] = {k.g.d_y_weight, k.g.d_z_weight,
                      k.a.gate && k.a.gate_stride == 0 ? static_cast<float*>(k.g.d_gate) : nullptr};
     float* to = out[blockIdx.y];
     if (!to) return;
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int d = blockIdx.x * kWave + lane;
+    const float* from = k.part + (int64_t)blockIdx.y * k.runs * k.a.D + d;
+    float v[kRuns / kRunWaves];
+#pragma unroll
+    for (int i = 0; i < kRuns / kRunWaves; ++i) {
+        const int r = wave + kRunWaves * i;
+        v[i] = r < k.runs && d < k.a.D ? from[(int64_t)r * k.a.D] : 0.0f;
+    }
     double s = 0;
-    if (d < k.a.D)
-        for (int r = wave; r < k.runs; r += 4) s += (double)k.part[((int64_t)blockIdx.y * k.runs + r) * k.a.D + d];
+#pragma unroll
+    for (int i = 0; i < kRuns / kRunWaves; ++i) s += (double)v[i];
     box[wave][lane] = s;
     __syncthreads();
-    if (wave == 0 && d < k.a.D) to[d] = (float)(box[0][lane] + box[1][lane] + box[2][lane] + box[3][lane]);
+    if (wave == 0 && d < k.a.D) {
+#pragma unroll
+        for (int w = 1; w < kRunWaves; ++w) s += box[w][lane];
+        to[d] = (float)s;
+    }
 }
 
 int runs_of(int T) { return T < kRuns ? T : kRuns; }
@@ -421,12 +504,15 @@ hipError_t launch_block_norm(const w4_norm_args& a, hipStream_t stream) {
     return with_team(a.D, [&](auto waves, auto chunks) {
         constexpr int kW = decltype(waves)::value, kC = decltype(chunks)::value, kT = teams<kW>();
         const dim3 grid((unsigned)((a.T + kT - 1) / kT)), block(kW * kT * kWave);
-        if (a.h_f32) {
-            block_norm_kernel<kW, kC, true><<<grid, block, 0, stream>>>(a);
-        } else {
-            block_norm_kernel<kW, kC, false><<<grid, block, 0, stream>>>(a);
-        }
-        return hipGetLastError();
+        const auto launch = [&](auto apart) {
+            if (a.h_f32) {
+                block_norm_kernel<kW, kC, true, decltype(apart)::value><<<grid, block, 0, stream>>>(a);
+            } else {
+                block_norm_kernel<kW, kC, false, decltype(apart)::value><<<grid, block, 0, stream>>>(a);
+            }
+            return hipGetLastError();
+        };
+        return (int64_t)a.T * a.D >= 1 << 19 ? launch(std::true_type{}) : launch(std::false_type{});
     });
 }
 
@@ -435,20 +521,28 @@ size_t block_norm_grad_workspace_bytes(int T, int D) { return (size_t)3 * runs_o
 hipError_t launch_block_norm_grad(const w4_norm_args& a, const w4_norm_grad_args& g, void* workspace, hipStream_t stream) {
     GradArgs k = {a, g, static_cast<float*>(workspace), runs_of(a.T)};
     if (a.T > 0) {
-        const hipError_t err = with_team(a.D, [&](auto waves, auto chunks) {
+        const dim3 grid((unsigned)k.runs), block(a.D <= 8192 ? 8 * kWave : 16 * kWave);
+        const auto launch = [&](auto waves, auto chunks) {
             constexpr int kW = decltype(waves)::value, kC = decltype(chunks)::value;
-            const dim3 grid((unsigned)k.runs), block(kW * kWave);
             if (a.h_f32) {
                 block_norm_grad_kernel<kW, kC, true><<<grid, block, 0, stream>>>(k);
             } else {
                 block_norm_grad_kernel<kW, kC, false><<<grid, block, 0, stream>>>(k);
             }
             return hipGetLastError();
-        });
+        };
+        using std::integral_constant;
+        constexpr integral_constant<int, 1> one{};
+        const hipError_t err = a.D <= 512    ? launch(one, one)
+                               : a.D <= 1024 ? launch(integral_constant<int, 2>{}, one)
+                               : a.D <= 2048 ? launch(integral_constant<int, 4>{}, one)
+                               : a.D <= 4096 ? launch(integral_constant<int, 8>{}, one)
+                               : a.D <= 8192 ? launch(integral_constant<int, 8>{}, integral_constant<int, 2>{})
+                                             : launch(integral_constant<int, 16>{}, integral_constant<int, 2>{});
         if (err != hipSuccess) return err;
     }
     if (!g.d_y_weight && !g.d_z_weight && !(g.d_gate && a.gate_stride == 0)) return hipSuccess;
-    block_norm_runs_kernel<<<dim3((unsigned)((a.D + kWave - 1) / kWave), 3), dim3(256), 0, stream>>>(k);
+    block_norm_runs_kernel<<<dim3((unsigned)((a.D + kWave - 1) / kWave), 3), dim3(kRunWaves * kWave), 0, stream>>>(k);
     return hipGetLastError();
 }
 
