@@ -13,6 +13,7 @@ import ctypes
 import torch
 
 from . import lib
+from . import step as _step
 from .step import _addresses, _bf16, _call, _device_of, _f32, _INT_MAX, _int32, _near, _optional_addresses, _ptr, _refuse, \
     _too_large
 
@@ -81,21 +82,32 @@ for _name, (_res, _args) in SIGNATURES.items():
     _fn.restype, _fn.argtypes = _res, _args
 
 
-def _rows(t, name, dtype, device, shape):
-    """A tensor [rows, values] whose rows lie at any stride: (address, stride); None: (None, 0)."""
-    if t is None:
-        return None, 0
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError(f"{name} must be a tensor [rows, values]")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}; got {list(t.shape)}")
-    if t.dtype is not dtype or t.get_device() != device:
-        _refuse(t, name, dtype, device)
-    step, unit = t.stride()
-    if shape[0] > 0 and shape[1] > 1 and unit != 1:
-        raise ValueError(f"{name}: the values of a row must lie together")
-    # one row or none: whatever stride it has is not used
-    return t.data_ptr(), step if shape[0] > 1 else max(shape[1], 8)
+def _rows(device, n, wide, *spec):
+    """Address and row stride, one behind the other, of each of some tensors [n, wide], given as (tensor, name,
+    dtype), whose rows lie at any stride; (None, 0) for None."""
+    out = []
+    for t, name, dtype in zip(spec[0::3], spec[1::3], spec[2::3]):
+        if t is None:
+            out += (None, 0)
+            continue
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise ValueError(f"{name} must be a tensor [rows, values]")
+        if t.shape != (n, wide):
+            raise ValueError(f"{name} must be {[n, wide]}; got {list(t.shape)}")
+        if t.dtype is not dtype or t.get_device() != device:
+            _refuse(t, name, dtype, device)
+        step, unit = t.stride()
+        if n > 0 and wide > 1 and unit != 1:
+            raise ValueError(f"{name}: the values of a row must lie together")
+        # one row or none: whatever stride it has is not used
+        out += (t.data_ptr(), step if n > 1 else max(wide, 8))
+    return tuple(out)
+
+
+_rows_in_python = _rows
+if _step._marshal is not None and _step._fits(_step._marshal):  # the same check compiled
+    _step._marshal.begin_rows(_rows)
+    _rows = _step._marshal.rows
 
 
 def _space(workspace, device):
@@ -104,37 +116,33 @@ def _space(workspace, device):
     return _ptr(workspace, "workspace", workspace.dtype, device), workspace.numel() * workspace.element_size()
 
 
-def _sized(t, name, dims):
-    """Sizes of a tensor, each within 32 bits."""
-    if not isinstance(t, torch.Tensor) or t.dim() != dims:
-        raise ValueError(f"{name} must be a tensor of {dims} dimensions")
-    if t.numel() and max(t.shape) > _INT_MAX:
-        _too_large(name, max(t.shape))
-    return t.shape
+def _matrix(t, name):
+    """Sizes of a tensor of two dimensions, each within 32 bits."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a tensor of 2 dimensions")
+    n, wide = t.shape
+    if n > _INT_MAX or wide > _INT_MAX:
+        _too_large(name, max(n, wide))
+    return n, wide
 
 
-def _norm_args(h, y, y_weight, z_weight, gate, residual_scale, branch_scale, eps, weight_add):
-    """(struct without outputs, device, shape, h's dtype) of a norm's inputs."""
-    shape = T, D = _sized(h, "h", 2)
+def _stream_of(h):
+    """(rows, values, dtype, device) of the residual stream."""
+    T, D = _matrix(h, "h")
     kind = h.dtype
     if kind is not _bf16 and kind is not _f32:
         raise TypeError(f"h: dtype {kind}, not torch.bfloat16 or torch.float32")
-    i = _device_of(h, "h", kind)
-    hp, hs = _rows(h, "h", kind, i, shape)
-    yp, ys = _rows(y, "y", _bf16, i, shape)
+    return T, D, kind, _device_of(h, "h", kind)
+
+
+def _given(i, T, D, y_weight, z_weight, gate):
+    """Addresses of the weights and the gate, the gate's row stride (0: one for all tokens)."""
     if gate is None or gate.dim() == 1:
-        gs = 0
-        wy, wz, gp = _optional_addresses(i, y_weight, "y_weight", _bf16, D, z_weight, "z_weight", _bf16, D,
-                                         gate, "gate", _bf16, D)
-    else:
-        gp, gs = _rows(gate, "gate", _bf16, i, shape)
-        if gs == 0:
-            raise ValueError("gate: one for all tokens is [D]")
-        wy, wz = _optional_addresses(i, y_weight, "y_weight", _bf16, D, z_weight, "z_weight", _bf16, D)
-    a = _NormArgs(h=hp, y=yp, y_weight=wy, z_weight=wz, gate=gp, h_stride=hs, y_stride=ys, gate_stride=gs, T=T, D=D,
-                  h_f32=kind is _f32, residual_scale=residual_scale, branch_scale=branch_scale, eps=eps,
-                  weight_add=weight_add)
-    return a, i, shape, kind
+        return (*_optional_addresses(i, y_weight, "y_weight", _bf16, D, z_weight, "z_weight", _bf16, D, gate, "gate", _bf16, D), 0)
+    gp, gs = _rows(i, T, D, gate, "gate", _bf16)
+    if gs == 0:
+        raise ValueError("gate: one for all tokens is [D]")
+    return (*_optional_addresses(i, y_weight, "y_weight", _bf16, D, z_weight, "z_weight", _bf16, D), gp, gs)
 
 
 def w4_block_norm(h, y=None, h_out=None, z=None, y_weight=None, z_weight=None, gate=None, residual_scale: float = 1.0,
@@ -144,9 +152,11 @@ def w4_block_norm(h, y=None, h_out=None, z=None, y_weight=None, z_weight=None, g
 
     ``h``, ``h_out`` [T, D] bfloat16 or float32 (``h_out`` may be ``h``), ``y``, ``z`` bfloat16 [T, D] (``z`` may be
     ``y``), weights bfloat16 [D] (None: no norm), ``gate`` bfloat16 [D] or [T, D].  Without ``y`` only ``z`` of ``h``."""
-    a, i, shape, kind = _norm_args(h, y, y_weight, z_weight, gate, residual_scale, branch_scale, eps, weight_add)
-    a.h_out, a.h_out_stride = _rows(h_out, "h_out", kind, i, shape)
-    a.z, a.z_stride = _rows(z, "z", _bf16, i, shape)
+    T, D, kind, i = _stream_of(h)
+    hp, hs, yp, ys, op, os, zp, zs = _rows(i, T, D, h, "h", kind, y, "y", _bf16, h_out, "h_out", kind, z, "z", _bf16)
+    wy, wz, gp, gs = _given(i, T, D, y_weight, z_weight, gate)
+    a = _NormArgs(hp, yp, op, zp, wy, wz, gp, hs, ys, os, zs, gs, T, D, kind is _f32, residual_scale, branch_scale, eps,
+                  weight_add)
     _call("w4_block_norm", lib.w4_block_norm, (ctypes.byref(a),), stream, i)
 
 
@@ -163,18 +173,18 @@ def w4_block_norm_grad(h, y=None, dh_out=None, dz=None, dh=None, dy=None, y_weig
     ``dh`` (may be ``dh_out``) has ``h``'s type, ``dy`` (may be ``dz``) is bfloat16, ``d_y_weight``, ``d_z_weight`` and a
     shared gate's ``d_gate`` are float32 [D], a gate of [T, D] has a bfloat16 ``d_gate`` of that shape; each may be None.
     ``workspace``: ``w4_block_norm_grad_workspace_bytes(T, D)``, for the sums over tokens."""
-    a, i, shape, kind = _norm_args(h, y, y_weight, z_weight, gate, residual_scale, branch_scale, eps, weight_add)
-    g = _NormGradArgs()
-    g.dh_out, g.dh_out_stride = _rows(dh_out, "dh_out", kind, i, shape)
-    g.dz, g.dz_stride = _rows(dz, "dz", _bf16, i, shape)
-    g.dh, g.dh_stride = _rows(dh, "dh", kind, i, shape)
-    g.dy, g.dy_stride = _rows(dy, "dy", _bf16, i, shape)
-    g.d_y_weight, g.d_z_weight = _optional_addresses(i, d_y_weight, "d_y_weight", _f32, shape[1],
-                                                     d_z_weight, "d_z_weight", _f32, shape[1])
-    if gate is not None and gate.dim() == 2:
-        g.d_gate, g.d_gate_stride = _rows(d_gate, "d_gate", _bf16, i, shape)
+    T, D, kind, i = _stream_of(h)
+    hp, hs, yp, ys, hop, hos, zp, zs, dhp, dhs, dyp, dys = _rows(
+        i, T, D, h, "h", kind, y, "y", _bf16, dh_out, "dh_out", kind, dz, "dz", _bf16, dh, "dh", kind, dy, "dy", _bf16)
+    wy, wz, gp, gs = _given(i, T, D, y_weight, z_weight, gate)
+    sy, sz = _optional_addresses(i, d_y_weight, "d_y_weight", _f32, D, d_z_weight, "d_z_weight", _f32, D)
+    if gs:
+        dgp, dgs = _rows(i, T, D, d_gate, "d_gate", _bf16)
     else:
-        g.d_gate, = _optional_addresses(i, d_gate, "d_gate", _f32, shape[1])
+        (dgp,), dgs = _optional_addresses(i, d_gate, "d_gate", _f32, D), 0
+    a = _NormArgs(hp, yp, None, None, wy, wz, gp, hs, ys, 0, 0, gs, T, D, kind is _f32, residual_scale, branch_scale, eps,
+                  weight_add)
+    g = _NormGradArgs(hop, zp, dhp, dyp, hos, zs, dhs, dys, dgs, sy, sz, dgp)
     pw, nbytes = _space(workspace, i)
     _call("w4_block_norm_grad", lib.w4_block_norm_grad, (ctypes.byref(a), ctypes.byref(g), pw, nbytes), stream, i)
 
@@ -191,25 +201,24 @@ def w4_moe_sort(experts, num_experts: int, row_start, row_of, source=None, x=Non
     (-1: none), ``source`` [T * top] (the choice of each row, -1 behind the last; may be None).  With ``x`` bfloat16
     [T, D], ``rows`` [R, D] gets ``x[t]`` at each of token t's rows.  An expert takes its first ``capacity`` choices
     (0: all)."""
-    T, top = _sized(experts, "experts", 2)
-    i = _device_of(experts, "experts", _int32)
+    T, top = _matrix(experts, "experts")
+    i, v = _device_of(experts, "experts", _int32), _int32
     if not -1 <= num_experts <= _INT_MAX:
         _too_large("w4_moe_sort", num_experts)
-    v = _int32
-    ep, rs = _addresses(i, experts, "experts", v, None, row_start, "row_start", v, max(num_experts, 0) + 1)
     if not isinstance(row_of, torch.Tensor) or row_of.shape != experts.shape:
         raise ValueError(f"row_of must be {[T, top]}")
-    ro, so = _optional_addresses(i, row_of, "row_of", v, None, source, "source", v, T * top)
-    a = _SortArgs(experts=ep, row_start=rs, row_of=ro, source=so, T=T, top=top, num_experts=num_experts,
-                  capacity=_near(capacity))
+    ep, sp, rp = _addresses(i, experts, "experts", v, None, row_start, "row_start", v, max(num_experts, 0) + 1,
+                            row_of, "row_of", v, None)
+    so, = _optional_addresses(i, source, "source", v, T * top)
+    R = D = xs = rs = 0
+    xp = op = None
     if x is not None or rows is not None:
         if x is None or rows is None:
             raise ValueError("x and rows go together")
-        D = _sized(x, "x", 2)[1]
-        R = _sized(rows, "rows", 2)[0]
-        a.x, a.x_stride = _rows(x, "x", _bf16, i, (T, D))
-        a.rows, a.rows_stride = _rows(rows, "rows", _bf16, i, (R, D))
-        a.R, a.D = R, D
+        (R, D), _ = _matrix(rows, "rows"), _matrix(x, "x")
+        xp, xs = _rows(i, T, D, x, "x", _bf16)
+        op, rs = _rows(i, R, D, rows, "rows", _bf16)
+    a = _SortArgs(ep, sp, rp, so, xp, op, xs, rs, T, top, num_experts, _near(capacity), R, D)
     pw, nbytes = _space(workspace, i)
     _call("w4_moe_sort", lib.w4_moe_sort, (ctypes.byref(a), pw, nbytes), stream, i)
 
@@ -225,9 +234,9 @@ def _choices(row_of, weights, T, R, device):
         if not isinstance(given, torch.Tensor) or given.dim() != 2 or given.shape[0] != T:
             raise ValueError(f"row_of and weights must be [{T}, top]")
         top = given.shape[1]
-    for name, t in (("row_of", row_of), ("weights", weights)):
-        if t is not None and t.shape != (T, top):
-            raise ValueError(f"{name} must be {[T, top]}; got {list(t.shape)}")
+        for name, t in (("row_of", row_of), ("weights", weights)):
+            if t is not None and t is not given and t.shape != (T, top):
+                raise ValueError(f"{name} must be {[T, top]}; got {list(t.shape)}")
     return (top, *_optional_addresses(device, row_of, "row_of", _int32, None, weights, "weights", _f32, None))
 
 
@@ -236,14 +245,12 @@ def w4_moe_combine(y, out, row_of=None, weights=None, add=None, stream=None) -> 
 
     ``row_of`` int32 [T, top] (``w4_moe_sort``'s; None: row t * top + j), ``weights`` float32 [T, top] (None: 1),
     ``add`` bfloat16 [T, N] (None: 0; may be ``out``).  A row outside ``y`` counts for nothing."""
-    R, N = _sized(y, "y", 2)
-    T = _sized(out, "out", 2)[0]
+    (R, N), (T, _) = _matrix(y, "y"), _matrix(out, "out")
     i = _device_of(out, "out", _bf16)
-    a = _CombineArgs(T=T, R=R, N=N)
-    a.top, a.row_of, a.weights = _choices(row_of, weights, T, R, i)
-    a.y, a.y_stride = _rows(y, "y", _bf16, i, (R, N))
-    a.add, a.add_stride = _rows(add, "add", _bf16, i, (T, N))
-    a.out, a.out_stride = _rows(out, "out", _bf16, i, (T, N))
+    top, rp, wp = _choices(row_of, weights, T, R, i)
+    yp, ys = _rows(i, R, N, y, "y", _bf16)
+    ap, as_, op, os = _rows(i, T, N, add, "add", _bf16, out, "out", _bf16)
+    a = _CombineArgs(yp, rp, wp, ap, op, ys, as_, os, T, top, R, N)
     _call("w4_moe_combine", lib.w4_moe_combine, (ctypes.byref(a),), stream, i)
     return out
 
@@ -251,19 +258,19 @@ def w4_moe_combine(y, out, row_of=None, weights=None, add=None, stream=None) -> 
 def w4_moe_combine_grad(dout, y=None, row_of=None, weights=None, dy=None, dweights=None, stream=None) -> None:
     """Gradients of ``w4_moe_combine``'s rows and weights: ``dy[row_of[t, j]] = weights[t, j] * dout[t]`` (``dy`` may
     be ``y``; rows that no choice has are left) and ``dweights[t, j] = dout[t] . y[row_of[t, j]]`` (0 without a row)."""
-    T, N = _sized(dout, "dout", 2)
+    T, N = _matrix(dout, "dout")
     given = y if y is not None else dy
     if given is None:
         raise ValueError("y or dy must be given")
-    R = _sized(given, "y" if y is not None else "dy", 2)[0]
+    R, _ = _matrix(given, "y" if y is not None else "dy")
     i = _device_of(dout, "dout", _bf16)
-    a = _CombineGradArgs(T=T, R=R, N=N)
-    a.top, a.row_of, a.weights = _choices(row_of, weights, T, R, i)
-    a.dout, a.dout_stride = _rows(dout, "dout", _bf16, i, (T, N))
-    a.y, a.y_stride = _rows(y, "y", _bf16, i, (R, N))
-    a.dy, a.dy_stride = _rows(dy, "dy", _bf16, i, (R, N))
+    top, rp, wp = _choices(row_of, weights, T, R, i)
+    gp, gs = _rows(i, T, N, dout, "dout", _bf16)
+    yp, ys, dp, ds = _rows(i, R, N, y, "y", _bf16, dy, "dy", _bf16)
+    dw = None
     if dweights is not None:
-        if dweights.shape != (T, a.top):
-            raise ValueError(f"dweights must be {[T, a.top]}; got {list(dweights.shape)}")
-        a.dweights, = _addresses(i, dweights, "dweights", _f32, None)
+        if not isinstance(dweights, torch.Tensor) or dweights.shape != (T, top):
+            raise ValueError(f"dweights must be a tensor {[T, top]}")
+        dw, = _addresses(i, dweights, "dweights", _f32, None)
+    a = _CombineGradArgs(gp, yp, rp, wp, dp, dw, gs, ys, ds, T, top, R, N)
     _call("w4_moe_combine_grad", lib.w4_moe_combine_grad, (ctypes.byref(a),), stream, i)

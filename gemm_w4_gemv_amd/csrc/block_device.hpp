@@ -20,4 +20,23 @@ __device__ __forceinline__ u32x4_t narrow(const f32x8_t& v) {
     return u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
 }
 
+// Loads and stores that with kApart go past the caches' ways of keeping what is
+// read or written once.
+template <bool kApart, typename T>
+__device__ __forceinline__ void put(T* p, const T& v) {
+    if constexpr (kApart) {
+        __builtin_nontemporal_store(v, p);
+    } else {
+        *p = v;
+    }
+}
+template <bool kApart, typename T>
+__device__ __forceinline__ T take(const T* p) {
+    if constexpr (kApart) {
+        return __builtin_nontemporal_load(p);
+    } else {
+        return *p;
+    }
+}
+
 }  // namespace w4

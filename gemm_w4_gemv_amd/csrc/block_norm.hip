@@ -119,14 +119,6 @@ struct Raw {
         }
     }
 };
-template <bool kApart, typename T>
-__device__ __forceinline__ void put(T* p, const T& v) {
-    if constexpr (kApart) {
-        __builtin_nontemporal_store(v, p);
-    } else {
-        *p = v;
-    }
-}
 template <bool kF32, bool kApart = false>
 __device__ __forceinline__ void store(void* p, int64_t at, const f32x8_t& v) {
     if constexpr (kF32) {

@@ -3,8 +3,8 @@
 // through Python than its kernel runs (tables of a step 7.6 us of host time
 // with the checks in Python, 5.6 with these).
 //
-// Each function takes what the Python function of the same name in step.py
-// takes and gives what that gives; where a tensor is not as it should be it
+// Each function takes what the Python function of the same name in step.py (rows:
+// in block.py) takes and gives what that gives; where a tensor is not as it should be it
 // calls that function, which says what is wrong.  The module's ``built_for``
 // names the torch (W4_BUILT_FOR, from the build) and the Python that it fits.
 #define PY_SSIZE_T_CLEAN
@@ -17,6 +17,7 @@ namespace {
 PyObject* slow_addresses = nullptr;
 PyObject* slow_optional = nullptr;
 PyObject* slow_heads = nullptr;
+PyObject* slow_rows = nullptr;
 
 // A dense tensor on GPU ``device``, or NULL.
 const at::Tensor* tensor_on(PyObject* o, long device) {
@@ -98,7 +99,54 @@ PyObject* heads(PyObject*, PyObject* const* args, Py_ssize_t count) {
     }
 }
 
-// begin(addresses, optional_addresses, heads): the Python functions to fall back on.
+// rows(device, n, wide, tensor, name, dtype, tensor, name, dtype, ...): address and row
+// stride, one behind the other, of each tensor [n, wide] whose rows' values lie
+// together; (None, 0) for None.
+PyObject* rows(PyObject*, PyObject* const* args, Py_ssize_t count) {
+    const auto slow = [&] { return PyObject_Vectorcall(slow_rows, args, (size_t)count, nullptr); };
+    if (count < 3 || count % 3) return slow();
+    long long size[3];
+    for (int i = 0; i < 3; ++i) {
+        size[i] = PyLong_AsLongLong(args[i]);
+        if (size[i] == -1 && PyErr_Occurred()) PyErr_Clear();
+        if (size[i] < 0) return slow();
+    }
+    const int64_t n = size[1], wide = size[2];
+    const Py_ssize_t tensors = count / 3 - 1;
+    PyObject* out = PyTuple_New(2 * tensors);
+    if (!out) return nullptr;
+    bool good = true;
+    try {
+        for (Py_ssize_t i = 0; good && i < tensors; ++i) {
+            PyObject* const* a = args + 3 + 3 * i;
+            PyObject *address = nullptr, *stride = nullptr;
+            if (a[0] == Py_None) {
+                Py_INCREF(Py_None);
+                address = Py_None;
+                stride = PyLong_FromLong(0);
+            } else {
+                const at::Tensor* t = tensor_on(a[0], (long)size[0]);
+                good = t && THPDtype_Check(a[2]) && t->scalar_type() == reinterpret_cast<THPDtype*>(a[2])->scalar_type &&
+                       t->dim() == 2 && t->size(0) == n && t->size(1) == wide && (n == 0 || wide <= 1 || t->stride(1) == 1);
+                if (!good) break;
+                address = PyLong_FromVoidPtr(t->data_ptr());
+                stride = PyLong_FromLongLong(n > 1 ? (long long)t->stride(0) : std::max<long long>(wide, 8));
+            }
+            good = address && stride;
+            if (address) PyTuple_SET_ITEM(out, 2 * i, address);
+            if (stride) PyTuple_SET_ITEM(out, 2 * i + 1, stride);
+        }
+    } catch (...) {
+        good = false;
+    }
+    if (good) return out;
+    Py_DECREF(out);
+    PyErr_Clear();
+    return slow();
+}
+
+// begin(addresses, optional_addresses, heads), begin_rows(rows): the Python
+// functions to fall back on.
 PyObject* begin(PyObject*, PyObject* const* args, Py_ssize_t count) {
     if (count != 3) {
         PyErr_SetString(PyExc_TypeError, "begin(addresses, optional_addresses, heads)");
@@ -114,12 +162,25 @@ PyObject* begin(PyObject*, PyObject* const* args, Py_ssize_t count) {
     Py_RETURN_NONE;
 }
 
+PyObject* begin_rows(PyObject*, PyObject* const* args, Py_ssize_t count) {
+    if (count != 1) {
+        PyErr_SetString(PyExc_TypeError, "begin_rows(rows)");
+        return nullptr;
+    }
+    PyObject* old = slow_rows;
+    Py_INCREF(args[0]);
+    slow_rows = args[0];
+    Py_XDECREF(old);
+    Py_RETURN_NONE;
+}
+
 template <PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr};
 }
 PyMethodDef methods[] = {method<addresses<false>>("addresses"), method<addresses<true>>("optional_addresses"),
-                         method<heads>("heads"), method<begin>("begin"), {}};
+                         method<heads>("heads"), method<begin>("begin"), method<rows>("rows"),
+                         method<begin_rows>("begin_rows"), {}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
