@@ -19,7 +19,8 @@ buffers, so one replay recomputes every output.
 
 With a ``DecodeAttention`` the step is a whole token's: between a layer's q, k,
 v and its o it stores the token in the layer's 4-bit cache and attends over
-it, and with a ``TokenSampler`` it ends in the next token.
+it, and with a ``TokenSampler`` it ends in the next token.  With
+``DecodeNorms`` the blocks read a normed residual stream and add to it.
 """
 from __future__ import annotations
 
@@ -27,7 +28,7 @@ import torch
 
 from . import w4_gemv, w4_graph_begin, w4_graph_end, W4Graph, w4_chain_create, w4_chain_run, \
     w4_chain_workspace_bytes, Kv4Cache, w4_kv4_plan, w4_qk_norm_rope, w4_kv4_attn, w4_kv4_attn_workspace_bytes, \
-    w4_sample, w4_sample_workspace_bytes
+    w4_sample, w4_sample_workspace_bytes, w4_block_norm
 
 # Stage of each decoder linear within its layer.  Along the decoder's data
 # flow q -> o -> gate -> down -> (next layer's) q each of these waits for the
@@ -53,7 +54,7 @@ def decoder_stages(names, layers_of, grouped: bool = False):
     return [per * layer + table[name] for name, layer in zip(names, layers_of)]
 
 
-def link_decoder_inputs(linears, attention: "DecodeAttention | None" = None) -> None:
+def link_decoder_inputs(linears, attention: "DecodeAttention | None" = None, norms: "DecodeNorms | None" = None) -> None:
     """Make every linear read the output it reads in a decoder layer.
 
     ``linears`` are dicts with ``name``, ``layer``, ``x`` and ``y``, in layer
@@ -62,7 +63,9 @@ def link_decoder_inputs(linears, attention: "DecodeAttention | None" = None) -> 
     reads q's output, or with ``attention`` its layer's output there (the
     gate/up product is outside this path); gate and up read o's, down reads
     gate's, and a layer's q, k and v read the previous layer's down output,
-    as a linear named "logits" does (its layer is one past the last).
+    as a linear named "logits" does (its layer is one past the last).  With
+    ``norms`` q, k, v, gate, up and logits read the normed stream instead, the
+    first layer's too.
     """
     out = {}
     for lin in linears:
@@ -70,6 +73,8 @@ def link_decoder_inputs(linears, attention: "DecodeAttention | None" = None) -> 
         src = DECODER_INPUT[name]
         if attention is not None and name == "o":
             lin["x"] = attention.out[layer].view(-1)
+        elif norms is not None and src in ("h", "o"):
+            lin["x"] = norms.z.view(-1)
         elif src == "h":
             if layer > 0:
                 lin["x"] = out[(layer - 1, "down")]
@@ -171,6 +176,43 @@ class DecodeAttention:
             torch.add(self.counts[:1], 0, out=self.free_count)
 
 
+class DecodeNorms:
+    """The residual stream ``h`` [1, hidden] of a decode step's token (bfloat16, or float32 with ``wide``; the
+    caller puts the token's embedding there) and the norms around the blocks, whose inputs are in ``z``.
+
+    A layer's attention reads norm(h) * ``attn_in[layer]`` and its output linear's result is added to ``h``, normed by
+    ``attn_out[layer]`` first if that is given; so with ``mlp_in`` and ``mlp_out`` around gate, up and down.  ``final`` is the
+    norm before the logits.  Weights are bfloat16 [hidden], ``weight_add`` is added to each; ``branch_scale``
+    multiplies what is added to ``h`` and ``residual_scale`` what it is added to."""
+
+    def __init__(self, attn_in, mlp_in, final, attn_out=None, mlp_out=None, wide: bool = False, eps: float = 1e-6,
+                 weight_add: float = 0.0, residual_scale: float = 1.0, branch_scale: float = 1.0):
+        if len(attn_in) != len(mlp_in) or any(w is not None and len(w) != len(attn_in) for w in (attn_out, mlp_out)):
+            raise ValueError("norms: as many weights before and after each block as layers")
+        self.layers = len(attn_in)
+        none = [None] * self.layers
+        # by layer and block: the weight after it and the one before the next
+        self.after = {}
+        for i in range(self.layers):
+            self.after[i, "o"] = ((attn_out or none)[i], mlp_in[i])
+            self.after[i, "down"] = ((mlp_out or none)[i], attn_in[i + 1] if i + 1 < self.layers else final)
+        self.first = attn_in[0] if self.layers else final
+        self.settings = dict(eps=eps, weight_add=weight_add)
+        self.scales = dict(residual_scale=residual_scale, branch_scale=branch_scale)
+        self.h = torch.zeros(1, final.numel(), dtype=torch.float32 if wide else torch.bfloat16, device=final.device)
+        self.z = torch.zeros(1, final.numel(), dtype=torch.bfloat16, device=final.device)
+
+    def begin(self, stream: torch.cuda.Stream) -> None:
+        """What the first block reads, of the stream as the caller left it."""
+        w4_block_norm(self.h, z=self.z, z_weight=self.first, stream=stream, **self.settings)
+
+    def run(self, layer: int, name: str, y, stream: torch.cuda.Stream) -> None:
+        """Adds a block's output (its linear ``name``, "o" or "down") to the stream; what the next block reads."""
+        y_weight, z_weight = self.after[layer, name]
+        w4_block_norm(self.h, y.view(1, -1), h_out=self.h, z=self.z, y_weight=y_weight, z_weight=z_weight, stream=stream,
+                      **self.settings, **self.scales)
+
+
 class TokenSampler:
     """Draws a token from each row of logits [rows, vocab]: settings are tensors (or None) that
     the caller changes in place, ``uniform`` (float64 [rows], in [0, 1)) anew for every token."""
@@ -197,24 +239,30 @@ class DecodeStep:
 
     With ``attention`` (and then ``name`` and ``layer`` in the dicts, see
     ``link_decoder_inputs``) every layer's q, k and v, in any order, go through its
-    cache before its o; with ``sampler`` the step ends in a token from the output of
-    the linear named "logits".  Both are launches of their own, not stages of the chain.
+    cache before its o; with ``norms`` every o and down is added to the residual stream
+    that the other linears read; with ``sampler`` the step ends in a token from the output of
+    the linear named "logits".  These are launches of their own, not stages of the chain.
     """
 
     def __init__(self, linears, stream: torch.cuda.Stream | None = None, mode: str = "launches",
-                 attention: DecodeAttention | None = None, sampler: TokenSampler | None = None):
+                 attention: DecodeAttention | None = None, sampler: TokenSampler | None = None,
+                 norms: DecodeNorms | None = None):
         if mode not in ("launches", "chain"):
             raise ValueError("mode must be 'launches' or 'chain'")
         if mode == "chain" and (attention is not None or sampler is not None):
             raise ValueError("the chain runs linears alone: attention and sampler go with mode 'launches'")
-        self.attention, self.sampler = attention, sampler
+        if mode == "chain" and norms is not None:
+            raise ValueError("the chain runs linears alone: norms go with mode 'launches'")
+        self.attention, self.sampler, self.norms = attention, sampler, norms
         self.linears = list(linears)
         if attention is not None:
             self._check_layers()
+        if norms is not None:
+            self._check_blocks()
         if sampler is not None and [lin["name"] for lin in self.linears].count("logits") != 1:
             raise ValueError("a sampler needs one linear named 'logits'")
         self.stream = stream if stream is not None else torch.cuda.Stream()
-        if attention is not None or sampler is not None:  # their buffers are filled on the current stream
+        if attention is not None or sampler is not None or norms is not None:  # their buffers are filled on the current stream
             self.stream.wait_stream(torch.cuda.current_stream(self.stream.device))
         self.mode = mode
         self.graph: W4Graph | None = None
@@ -245,6 +293,26 @@ class DecodeStep:
                 if name not in names:
                     raise ValueError(f"layer {layer} has no linear named '{name}'")
 
+    def _check_blocks(self) -> None:
+        """The linears that read the normed stream run while it is theirs: a layer's q, k and v before its o, gate and
+        up between o and down, layer after layer, each o and down once."""
+        turn = {"q": 0, "k": 0, "v": 0, "o": 1, "gate": 2, "up": 2, "down": 3}
+        ends, last = {}, -1
+        for lin in self.linears:
+            name, layer = lin["name"], lin["layer"]
+            at = 4 * self.norms.layers if name == "logits" else 4 * layer + turn[name]
+            if name != "logits" and not 0 <= layer < self.norms.layers:
+                raise ValueError(f"layer {layer}: the norms have {self.norms.layers} layers")
+            if at < last:
+                raise ValueError(f"layer {layer}: {name} comes behind a linear that changes the stream it reads")
+            last = at
+            if name in ("o", "down"):
+                ends[at] = ends.get(at, 0) + 1
+        for layer in range(self.norms.layers):
+            for name in ("o", "down"):
+                if ends.get(4 * layer + turn[name]) != 1:
+                    raise ValueError(f"layer {layer} must have one linear named '{name}'")
+
     def run_eager(self) -> None:
         """Run the step directly on the step's stream (no graph)."""
         if self.mode == "chain":
@@ -252,12 +320,16 @@ class DecodeStep:
             return
         if self.attention is not None:
             self.attention.begin(self.stream)
+        if self.norms is not None:
+            self.norms.begin(self.stream)
         made = {}  # of each layer: its q, k and v
         for lin in self.linears:
             w4_gemv(lin["x"], lin["qw"], lin["s"], lin["z"], lin["y"], stream=self.stream)
-            if self.attention is None and self.sampler is None:
+            if self.attention is None and self.sampler is None and self.norms is None:
                 continue
             name, layer = lin["name"], lin["layer"]
+            if self.norms is not None and name in ("o", "down"):
+                self.norms.run(layer, name, lin["y"], self.stream)
             if self.attention is not None and name in ("q", "k", "v"):
                 got = made.setdefault(layer, {})
                 got[name] = lin["y"]
