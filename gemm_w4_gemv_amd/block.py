@@ -137,7 +137,7 @@ def _stream_of(h):
 
 def _given(i, T, D, y_weight, z_weight, gate):
     """Addresses of the weights and the gate, the gate's row stride (0: one for all tokens)."""
-    if gate is None or gate.dim() == 1:
+    if not isinstance(gate, torch.Tensor) or gate.dim() == 1:
         return (*_optional_addresses(i, y_weight, "y_weight", _bf16, D, z_weight, "z_weight", _bf16, D, gate, "gate", _bf16, D), 0)
     gp, gs = _rows(i, T, D, gate, "gate", _bf16)
     if gs == 0:
