@@ -5,9 +5,9 @@
 //
 // Memory bounds both (a row is read and written once, a few operations a
 // value), so a team of waves holds a row in registers, 16 bytes a load, and
-// the two sums of squares are all that it exchanges.  Those are FP64: the
-// squares of BF16's largest and smallest values leave FP32, and the few FP64
-// instructions hide behind the loads.
+// the two sums of squares are all that it exchanges, in FP64; a lane's own share
+// is FP32 where that holds it, since the squares of BF16's largest and smallest
+// values do not fit.
 #include <math.h>
 
 #include <type_traits>
@@ -256,13 +256,20 @@ __global__ __launch_bounds__(kWaves* teams<kWaves>() * kWave) void block_norm_ke
 }
 
 // ----------------------------------------------------------------- gradient
-// A workgroup of eight waves (sixteen for the longest rows), in teams of as many as a
-// row takes, goes over a run of rows.  The next row is on its way while one is worked on: a row is four
+// A workgroup of eight waves, in teams of as many as a row takes, goes over a run
+// of rows.  The next row is on its way while one is worked on: a row is four
 // sums over it, two of which can wait for the others, so a row costs two
 // barriers; the sum of the next row's y^2 goes with the second.
 //
 //   first   sum h'^2 and sum g2 h'   (g2 = dz w2: mean(g2 n2) = r2 mean(g2 h'))
 //   second  sum g1 n1 of this row, sum y^2 of the next
+//
+// Measured, all gradients, an FP32 stream: 8192 rows of 4096 137 us, 4.4 TB/s; the
+// instructions of one workgroup a compute unit bound it, two waves a SIMD.
+// Rows past 8192 (kLong) would fill the registers: their sums over the rows lie in
+// LDS, weights are read row by row and no row is ahead (4 chunks of eight
+// waves: 2048 rows of 16384 275 us, 2 chunks of sixteen 328, with all in registers, most
+// of which the compiler then moves to memory, 1250; 2730 of 12288 183, 329 and 1217).
 //
 // Sums over the rows are taken in three steps, none of whose order is left to
 // chance: a lane adds its columns row by row, the teams join in LDS, and a second
@@ -278,10 +285,12 @@ struct GradArgs {
 };
 
 template <int kWaves, int kChunks, bool kF32>
-__global__ __launch_bounds__((kWaves > 8 ? kWaves : 8) * kWave) void block_norm_grad_kernel(GradArgs k) {
-    constexpr int kLanes = kWaves * kWave, kTeams = kWaves > 8 ? 1 : 8 / kWaves;
+__global__ __launch_bounds__(8 * kWave) void block_norm_grad_kernel(GradArgs k) {
+    constexpr int kLanes = kWaves * kWave, kTeams = 8 / kWaves;
+    constexpr bool kLong = kChunks > 2;
     constexpr f32x8_t kZero = {0, 0, 0, 0, 0, 0, 0, 0};
-    __shared__ double box[2][kTeams][kWaves][2];
+    __shared__ double box[kLong ? 3 : 2][kTeams][kWaves][2];
+    __shared__ f32x4_t far_sums[kLong ? 2 : 1][kLong ? 2 * kChunks : 1][kLong ? kLanes : 1];
     __shared__ f32x8_t join[kTeams == 1 ? 1 : 4 * kWave][kChunks];
     const w4_norm_args& a = k.a;
     const w4_norm_grad_args& g = k.g;
@@ -314,42 +323,80 @@ __global__ __launch_bounds__((kWaves > 8 ? kWaves : 8) * kWave) void block_norm_
 
     f32x8_t sum_y[kChunks], sum_z[kChunks], sum_g[kChunks];
     Raw<false> wy[kChunks], wz[kChunks], gate[kChunks];
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
+    const auto weights = [&](int c) {
         const int64_t d = (c * kLanes + tid) * 8;
-        sum_y[c] = sum_z[c] = sum_g[c] = kZero;
-        if (!here(c)) continue;
         if (a.y_weight) wy[c].load(a.y_weight, d);
         if (a.z_weight) wz[c].load(a.z_weight, d);
         if (shared_gate) gate[c].load(a.gate, d);
+    };
+    // sum += x * y in the lane's columns
+    const auto grow = [&](int which, int c, f32x8_t* sum, const f32x8_t& x, const f32x8_t& y) {
+        if constexpr (kLong) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                f32x4_t& far = far_sums[which][2 * c + half][tid];
+                f32x4_t v = far;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = fmaf(x[4 * half + i], y[4 * half + i], v[i]);
+                far = v;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[c][i] = fmaf(x[i], y[i], sum[c][i]);
+        }
+    };
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        sum_y[c] = sum_z[c] = sum_g[c] = kZero;
+        if constexpr (kLong) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) far_sums[i / 2][2 * c + i % 2][tid] = f32x4_t{0, 0, 0, 0};
+        } else if (here(c)) {
+            weights(c);
+        }
     }
 
     Row row;
-    fetch(row, first + team);
-    double sy = squares_of_y(row, first + team), unused = 0;
-    team_sums<kWaves>(sy, unused, box[1][team], wave, lane);
+    double sy = 0, unused = 0;
+    if constexpr (!kLong) {
+        fetch(row, first + team);
+        sy = squares_of_y(row, first + team);
+        team_sums<kWaves>(sy, unused, box[1][team], wave, lane);
+    }
     const double per = 1.0 / a.D;
     for (int64_t t0 = first; t0 < end; t0 += kTeams) {  // every team as often: the barriers are the workgroup's
         const int64_t t = t0 + team;
         const bool live = t < end;
         Row next;
-        fetch(next, t + kTeams);
+        if constexpr (kLong) {
+            fetch(row, t);
+            sy = squares_of_y(row, t);
+            team_sums<kWaves>(sy, unused, box[kLong ? 2 : 0][team], wave, lane);
+        } else {
+            fetch(next, t + kTeams);
+        }
         const Inverse r1 = a.y && a.y_weight ? inverse_root(sy * per + (double)a.eps) : Inverse{1.0f, 1.0f};
-        f32x8_t n1[kChunks], x[kChunks], dx[kChunks];  // y's norm before its weight; h'; dz w2
+        f32x8_t normed[kChunks], x[kChunks], dx[kChunks];  // y's norm before its weight; h'; dz w2
+        const auto n1_of = [&](int c) {
+            f32x8_t v = row.y[c].values();
+            if (a.y_weight) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = r1.of(v[i]);
+            }
+            return v;
+        };
+        const auto n1 = [&](int c) { return kLong ? n1_of(c) : normed[c]; };
         double s = 0, m = 0;
         if (live) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
                 if (!here(c)) continue;
+                if constexpr (kLong) weights(c);
                 x[c] = row.h[c].values();
                 if (a.gate && !shared_gate) gate[c].load(a.gate, t * a.gate_stride + (c * kLanes + tid) * 8);
                 if (a.y) {
-                    n1[c] = row.y[c].values();
-                    if (a.y_weight) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) n1[c][i] = r1.of(n1[c][i]);
-                    }
-                    f32x8_t u = n1[c];
+                    f32x8_t u = n1_of(c);
+                    if constexpr (!kLong) normed[c] = u;
                     if (a.y_weight) u *= wy[c].values() + a.weight_add;
                     if (a.gate) u *= gate[c].values();
 #pragma unroll
@@ -370,21 +417,25 @@ __global__ __launch_bounds__((kWaves > 8 ? kWaves : 8) * kWave) void block_norm_
             for (int c = 0; c < kChunks; ++c) {
                 const int64_t d = (c * kLanes + tid) * 8;
                 if (!here(c)) continue;
+                if (kLong && a.y) {
+                    weights(c);
+                    if (a.gate && !shared_gate) gate[c].load(a.gate, t * a.gate_stride + d);
+                }
                 if (normed_z) {
-                    const f32x8_t v = row.dz[c].values();
+                    f32x8_t n2;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float n2 = r2.of(x[c][i]);
-                        sum_z[c][i] = fmaf(v[i], n2, sum_z[c][i]);
-                        dx[c][i] = r2.of(fmaf(-mean2, n2, dx[c][i]));
+                        n2[i] = r2.of(x[c][i]);
+                        dx[c][i] = r2.of(fmaf(-mean2, n2[i], dx[c][i]));
                     }
+                    grow(1, c, sum_z, row.dz[c].values(), n2);
                 }
                 if (g.dh_out) dx[c] += row.dho[c].values();
                 if (g.dh) store<kF32>(g.dh, t * g.dh_stride + d, a.y ? dx[c] * a.residual_scale : dx[c]);
                 if (!a.y) continue;
                 f32x8_t b = dx[c] * a.branch_scale;
                 if (a.gate) {
-                    f32x8_t u = n1[c];
+                    f32x8_t u = n1(c);
                     if (a.y_weight) u *= wy[c].values() + a.weight_add;
                     u *= b;
                     if (shared_gate) {
@@ -394,16 +445,16 @@ __global__ __launch_bounds__((kWaves > 8 ? kWaves : 8) * kWave) void block_norm_
                     }
                     b *= gate[c].values();
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum_y[c][i] = fmaf(b[i], n1[c][i], sum_y[c][i]);
+                grow(0, c, sum_y, b, n1(c));
                 if (a.y_weight) b *= wy[c].values() + a.weight_add;
                 dx[c] = b;
+                const f32x8_t n = n1(c);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m1 = fmaf(b[i], n1[c][i], m1);
+                for (int i = 0; i < 8; ++i) m1 = fmaf(b[i], n[i], m1);
             }
         }
         m = m1;
-        sy = squares_of_y(next, t + kTeams);
+        if constexpr (!kLong) sy = squares_of_y(next, t + kTeams);
         team_sums<kWaves>(m, sy, box[1][team], wave, lane);
         if (live && a.y && g.dy) {
             const float mean1 = (float)(m * per);
@@ -411,13 +462,23 @@ __global__ __launch_bounds__((kWaves > 8 ? kWaves : 8) * kWave) void block_norm_
             for (int c = 0; c < kChunks; ++c) {
                 if (!here(c)) continue;
                 if (a.y_weight) {
+                    const f32x8_t n = n1(c);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dx[c][i] = r1.of(fmaf(-mean1, n1[c][i], dx[c][i]));
+                    for (int i = 0; i < 8; ++i) dx[c][i] = r1.of(fmaf(-mean1, n[i], dx[c][i]));
                 }
                 store<false>(g.dy, t * g.dy_stride + (c * kLanes + tid) * 8, dx[c]);
             }
         }
-        row = next;
+        if constexpr (!kLong) row = next;
+    }
+    if constexpr (kLong) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                sum_y[c][i] = far_sums[0][2 * c + i / 4][tid][i % 4];
+                sum_z[c][i] = far_sums[1][2 * c + i / 4][tid][i % 4];
+            }
     }
 
     const auto put = [&](int which, f32x8_t* v) {
@@ -513,7 +574,7 @@ size_t block_norm_grad_workspace_bytes(int T, int D) { return (size_t)3 * runs_o
 hipError_t launch_block_norm_grad(const w4_norm_args& a, const w4_norm_grad_args& g, void* workspace, hipStream_t stream) {
     GradArgs k = {a, g, static_cast<float*>(workspace), runs_of(a.T)};
     if (a.T > 0) {
-        const dim3 grid((unsigned)k.runs), block(a.D <= 8192 ? 8 * kWave : 16 * kWave);
+        const dim3 grid((unsigned)k.runs), block(8 * kWave);
         const auto launch = [&](auto waves, auto chunks) {
             constexpr int kW = decltype(waves)::value, kC = decltype(chunks)::value;
             if (a.h_f32) {
@@ -525,12 +586,14 @@ hipError_t launch_block_norm_grad(const w4_norm_args& a, const w4_norm_grad_args
         };
         using std::integral_constant;
         constexpr integral_constant<int, 1> one{};
-        const hipError_t err = a.D <= 512    ? launch(one, one)
-                               : a.D <= 1024 ? launch(integral_constant<int, 2>{}, one)
-                               : a.D <= 2048 ? launch(integral_constant<int, 4>{}, one)
-                               : a.D <= 4096 ? launch(integral_constant<int, 8>{}, one)
-                               : a.D <= 8192 ? launch(integral_constant<int, 8>{}, integral_constant<int, 2>{})
-                                             : launch(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+        constexpr integral_constant<int, 8> eight{};
+        const hipError_t err = a.D <= 512     ? launch(one, one)
+                               : a.D <= 1024  ? launch(integral_constant<int, 2>{}, one)
+                               : a.D <= 2048  ? launch(integral_constant<int, 4>{}, one)
+                               : a.D <= 4096  ? launch(eight, one)
+                               : a.D <= 8192  ? launch(eight, integral_constant<int, 2>{})
+                               : a.D <= 12288 ? launch(eight, integral_constant<int, 3>{})
+                                              : launch(eight, integral_constant<int, 4>{});
         if (err != hipSuccess) return err;
     }
     if (!g.d_y_weight && !g.d_z_weight && !(g.d_gate && a.gate_stride == 0)) return hipSuccess;

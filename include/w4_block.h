@@ -31,8 +31,9 @@ extern "C" {
  *   u  = y / sqrt(mean(y^2) + eps) * (y_weight + weight_add)   (no y_weight: u = y)
  *   h' = residual_scale * h + branch_scale * gate * u          (no gate: 1; no y: h' = h)
  *   z  = h' / sqrt(mean(h'^2) + eps) * (z_weight + weight_add) (no z_weight: z = h')
- * Sums of squares are FP64, all else FP32; z is computed from h' before h' is
- * rounded to its type.  Each result is rounded once.
+ * A lane's share of a sum of squares is FP32, or FP64 where FP32 would not hold
+ * it; the sum over lanes is FP64, all else FP32.  z is computed from h' before h'
+ * is rounded to its type.  Each result is rounded once.
  *   h, h_out     device bf16, or float if h_f32 [T][D].  h_out may be exactly h
  *                (same pointer and stride), or NULL: not stored (then z is given)
  *   y            device bf16 [T][D], or NULL (then h_out must be NULL too)
