@@ -6,9 +6,10 @@
 // workgroup takes a few tokens, finds the rows of their choices and copies the
 // tokens there, reading each once.  What it needs of all other choices are two
 // numbers an expert, how many there are and how many come before; it counts
-// them itself in LDS where they are few, which takes one launch, else from a
-// table of counts per chunk of choices that a first launch makes.  The counts
-// are whole numbers, so LDS atomics do not decide any order.
+// them itself in LDS where they are few, which takes one launch.  Else a first
+// launch counts them per chunk of choices, and a workgroup sums that table, or where
+// it is large a second launch has summed it over the chunks.  The counts are whole
+// numbers, so LDS atomics do not decide any order.
 #include "block.hpp"
 #include "block_device.hpp"
 
@@ -19,7 +20,15 @@ constexpr int kThreads = 256;
 constexpr int kMaxE = W4_MOE_SORT_MAX_EXPERTS;
 constexpr int kOwn = 64;      // choices of a workgroup, at most
 constexpr int kAlone = 4096;  // choices that every workgroup counts itself
-constexpr int kTable = 16384; // counts of the table, at most
+// Counts of a table that every workgroup sums, at most, its chunks of kLongChunk choices;
+// larger ones are summed once, of kChunk choices or more.  us of both, the first
+// first: 683 tokens of 6 choices, 64 experts, rows of 4096 (320 counts) 11.9 and 13.6; 8191
+// (3072 counts) 87 either way; 4096 of 8, 256 experts, 2048 (8192) 43 and 33; 32768 of 8, 64
+// experts, 256 (16384) 191 and 50.
+constexpr int kTable = 4096;
+constexpr int kLongChunk = 1024, kChunk = 256;
+constexpr int kMaxChunks = 2048, kMaxCounts = 1 << 22;  // of a table summed once, at most
+constexpr int kScanExperts = 16;  // of a workgroup that sums over the chunks
 
 struct SortArgs {
     w4_moe_sort_args a;
@@ -27,7 +36,9 @@ struct SortArgs {
     int per;       // tokens of a workgroup
     int chunk;     // choices of a chunk; 0: no table
     int chunks;
-    int32_t* counts;  // [chunks][num_experts]
+    bool summed;      // moe_scan_kernel runs
+    int32_t* totals;  // [num_experts], if summed
+    int32_t* counts;  // [chunks][num_experts]: of a chunk; if summed, of all chunks before it
 };
 
 __global__ __launch_bounds__(kThreads) void moe_count_kernel(SortArgs k) {
@@ -44,6 +55,36 @@ __global__ __launch_bounds__(kThreads) void moe_count_kernel(SortArgs k) {
     for (int e = threadIdx.x; e < E; e += kThreads) k.counts[blockIdx.x * E + e] = hist[e];
 }
 
+// A column of the table a lane of sixteen, its chunks in sixteen runs.
+__global__ __launch_bounds__(kThreads) void moe_scan_kernel(SortArgs k) {
+    constexpr int kRuns = kThreads / kScanExperts, kAtOnce = 8;
+    __shared__ int sums[kRuns][kScanExperts];
+    const int E = k.a.num_experts, lane = threadIdx.x % kScanExperts, run = threadIdx.x / kScanExperts;
+    const int e = blockIdx.x * kScanExperts + lane, per = (k.chunks + kRuns - 1) / kRuns;
+    const int first = run * per, end = e < E ? min(first + per, k.chunks) : 0;
+    const auto over = [&](auto f) {
+        for (int c0 = first; c0 < end; c0 += kAtOnce) {
+            int x[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) x[i] = c0 + i < end ? k.counts[(c0 + i) * E + e] : 0;
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                if (c0 + i < end) f(c0 + i, x[i]);
+        }
+    };
+    int sum = 0;
+    over([&](int, int x) { sum += x; });
+    sums[run][lane] = sum;
+    __syncthreads();
+    sum = 0;
+    for (int r = 0; r < run; ++r) sum += sums[r][lane];
+    if (e < E && run == kRuns - 1) k.totals[e] = sum + sums[run][lane];
+    over([&](int c, int x) {
+        k.counts[c * E + e] = sum;
+        sum += x;
+    });
+}
+
 template <bool kApart>
 __global__ __launch_bounds__(kThreads) void moe_sort_kernel(SortArgs k) {
     __shared__ int total[kMaxE + 1], before[kMaxE], sums[kThreads / kWave], rows[kOwn];
@@ -51,20 +92,28 @@ __global__ __launch_bounds__(kThreads) void moe_sort_kernel(SortArgs k) {
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, E = a.num_experts;
     const int t0 = blockIdx.x * k.per, t1 = min(t0 + k.per, a.T);
     const int i0 = t0 * a.top, i1 = t1 * a.top;
-    for (int e = tid; e < E; e += kThreads) total[e] = before[e] = 0;
-    __syncthreads();
     int from = 0, to = k.n;  // the choices counted one by one
     if (k.chunk) {
         const int mine = i0 / k.chunk;
-        for (int i = tid; i < k.chunks * E; i += kThreads) {
-            const int c = k.counts[i], e = i % E;
-            if (c == 0) continue;
-            atomicAdd(&total[e], c);
-            if (i / E < mine) atomicAdd(&before[e], c);
-        }
         from = mine * k.chunk;
         to = i0;
+        for (int e = tid; e < E; e += kThreads) {
+            total[e] = k.summed ? k.totals[e] : 0;
+            before[e] = k.summed ? k.counts[mine * E + e] : 0;
+        }
+        if (!k.summed) {
+            __syncthreads();
+            for (int i = tid; i < k.chunks * E; i += kThreads) {
+                const int c = k.counts[i], e = i % E;
+                if (c == 0) continue;
+                atomicAdd(&total[e], c);
+                if (i / E < mine) atomicAdd(&before[e], c);
+            }
+        }
+    } else {
+        for (int e = tid; e < E; e += kThreads) total[e] = before[e] = 0;
     }
+    __syncthreads();
     for (int i = from + tid; i < to; i += kThreads) {
         const int e = a.experts[i];
         if ((unsigned)e >= (unsigned)E) continue;
@@ -145,10 +194,10 @@ SortArgs cut_of(int T, int top, int E) {
     // 16 choices a workgroup: 8191 tokens of 6 choices, rows of 4096: 74 us, of 64 80, of 6 74
     k.per = k.n <= kAlone || top > kOwn / 4 ? 1 : kOwn / 4 / top;
     if (k.n > kAlone) {
-        const int most = kTable / E;  // 16 chunks or more
-        k.chunk = (k.n + most - 1) / most;
-        if (k.chunk < 1024) k.chunk = 1024;
-        k.chunk = (k.chunk + k.per * top - 1) / (k.per * top) * (k.per * top);  // a workgroup's choices lie in one
+        const int most = kMaxCounts / E < kMaxChunks ? kMaxCounts / E : kMaxChunks;
+        k.summed = (int64_t)((k.n + kLongChunk - 1) / kLongChunk) * E > kTable;
+        k.chunk = k.summed ? (k.n + most - 1) / most : kLongChunk;
+        if (k.chunk < kChunk) k.chunk = kChunk;
         k.chunks = (k.n + k.chunk - 1) / k.chunk;
     }
     return k;
@@ -157,17 +206,25 @@ SortArgs cut_of(int T, int top, int E) {
 }  // namespace
 
 size_t moe_sort_workspace_bytes(int T, int top, int num_experts) {
-    return (size_t)cut_of(T, top, num_experts).chunks * num_experts * sizeof(int32_t);
+    const SortArgs k = cut_of(T, top, num_experts);
+    return (size_t)(k.chunks + k.summed) * num_experts * sizeof(int32_t);
 }
 
 hipError_t launch_moe_sort(const w4_moe_sort_args& a, void* workspace, hipStream_t stream) {
     SortArgs k = cut_of(a.T, a.top, a.num_experts);
     k.a = a;
-    k.counts = static_cast<int32_t*>(workspace);
     if (k.chunk) {
+        k.totals = static_cast<int32_t*>(workspace);
+        k.counts = k.totals + (k.summed ? a.num_experts : 0);
         moe_count_kernel<<<dim3((unsigned)k.chunks), dim3(kThreads), 0, stream>>>(k);
-        const hipError_t err = hipGetLastError();
+        hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
+        if (k.summed) {
+            moe_scan_kernel<<<dim3((unsigned)((a.num_experts + kScanExperts - 1) / kScanExperts)), dim3(kThreads), 0, stream>>>(k);
+            err = hipGetLastError();
+            if (err != hipSuccess) return err;
+        }
+        if (!a.x) k.per = kOwn / a.top;
     }
     const int groups = a.T > 0 ? (a.T + k.per - 1) / k.per : 1;
     if ((int64_t)k.n * a.D >= kRowsApart) {

@@ -140,8 +140,9 @@ def test_moe_sort_workspace():
     size = w4.w4_moe_sort_workspace_bytes
     assert size(0, 4, 64) == size(10, 0, 64) == size(10, 4, 0) == size(10, 65, 4) == size(1 << 23, 2, 4) == 0
     assert size(1, 6, 64) == 0  # a decode step's choices need no table
-    for T, top, E in ((8191, 6, 64), (1 << 23, 1, 1024), (1 << 17, 64, 1)):
-        assert 0 < size(T, top, E) <= 4 * 16384
+    assert size(8191, 6, 64) == 48 * 64 * 4  # counts of 48 chunks
+    for T, top, E in ((8191, 8, 256), (1 << 23, 1, 1024), (1 << 17, 64, 1)):
+        assert 0 < size(T, top, E) <= 4 * ((1 << 22) + 1024)  # of at most 2^22 and their sums
 
 
 def combine(**k):
