@@ -1876,7 +1876,7 @@ SharedCut shared_cut_of(const w4_attn_args& a, int prefix, const w4_kv4_cache& c
     // 5 rows of 8 heads, heads of 64, behind 4112: 54 and 38).
     // Long prompts, with rows enough of their own, are done request by request.
     const int64_t units = B * own_row_tiles * c.kv_heads * tiles, each = (rows + B - 1) / B;
-    if (a.T < 2 || own_rows > 64 || rows > (1 << 20) || units <= (each < 8 ? each : 8) * (c.head_dim == 64 ? 6144 : 2048)) return k;
+    if (a.T < 2 || own_rows > 64 || rows * c.kv_heads > (1 << 22) || units <= (each < 8 ? each : 8) * (c.head_dim == 64 ? 6144 : 2048)) return k;
     const int64_t own_groups = B * c.kv_heads * own_row_tiles, groups = c.kv_heads * ((rows + 63) / 64);
     if (own_groups > (1 << 20)) return k;
     k.tiles = (int)tiles;

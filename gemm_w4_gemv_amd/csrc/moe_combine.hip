@@ -149,7 +149,8 @@ hipError_t launch_moe_combine_grad(const w4_moe_combine_grad_args& a, hipStream_
         };
         if (a.N <= 512) return launch(std::integral_constant<int, 1>{});
         if (a.N <= 1024) return launch(std::integral_constant<int, 2>{});
-        if (a.N <= 2048) return launch(std::integral_constant<int, 4>{});
+        // (a launch counts its work-items in 32 bits)
+        if (a.N <= 2048 || a.T > 1 << 22) return launch(std::integral_constant<int, 4>{});
         return launch(std::integral_constant<int, 8>{});
     });
 }

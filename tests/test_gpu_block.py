@@ -584,3 +584,35 @@ def test_block_calls_repeat_their_bits_on_another_stream():
         if n == "drows" or n == "rows":  # rows behind the last are left: here every choice has one
             assert torch.equal(first[n], t)
         assert torch.equal(first[n], t), n
+
+
+def test_the_most_tokens_of_one_call():
+    """As many tokens as a call takes: a workgroup each must not pass what a launch counts."""
+    T, N = 1 << 23, 2056
+    dout = torch.empty(T, N, dtype=bf16, device=DEV)
+    some = [0, (1 << 22) + 1, T - 1]
+    values = tensor(60, (3, N))
+    dout[some] = values
+    y, row_of = tensor(61, (4, N)), torch.full((T, 1), -1, dtype=torch.int32, device=DEV)
+    row_of[some, 0] = ints([2, 0, 3])
+    dy, dw = torch.full_like(y, 7.0), torch.full((T, 1), 7.0, device=DEV)
+    w4.w4_moe_combine_grad(dout, y, row_of=row_of, dy=dy, dweights=dw)
+    torch.cuda.synchronize()
+    assert torch.equal(dy[[2, 0, 3]], values) and torch.all(dy[1] == 7.0)
+    want, size = (f64(values) * f64(y[[2, 0, 3]])).sum(1), np.abs(f64(values) * f64(y[[2, 0, 3]])).sum(1)
+    close(dw[some, 0], want, (8 * -(-N // 256) + 12) * 2.0 ** -24 * size, "dweights")
+    assert int((dw != 0).sum()) == 3
+    del dout
+    out = torch.full((T, 8), 7.0, dtype=bf16, device=DEV)
+    w4.w4_moe_combine(y[:, :8], out, row_of=row_of)
+    torch.cuda.synchronize()
+    assert torch.equal(out[some], y[[2, 0, 3], :8]) and int((out != 0).any(1).sum()) == 3
+    experts = torch.arange(T, dtype=torch.int32, device=DEV).remainder_(1000).view(T, 1)
+    start, rows = torch.zeros(1025, dtype=torch.int32, device=DEV), torch.zeros(T, 1, dtype=torch.int32, device=DEV)
+    work = torch.empty(w4.w4_moe_sort_workspace_bytes(T, 1, 1024), dtype=torch.uint8, device=DEV)
+    w4.w4_moe_sort(experts, 1024, start, rows, workspace=work)
+    torch.cuda.synchronize()
+    sizes = [T // 1000 + (e < T % 1000) for e in range(1000)] + [0] * 24
+    assert start.tolist() == [0, *np.cumsum(sizes).tolist()]
+    at = torch.arange(T, device=DEV)
+    assert torch.equal(rows[:, 0].long(), start[:1000].long()[at % 1000] + at // 1000)
