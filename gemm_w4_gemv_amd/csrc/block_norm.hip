@@ -171,11 +171,11 @@ __device__ __forceinline__ double squares(X x, F there) {
     return xx;
 }
 
-// A team of kWaves waves holds a row, kChunks times 8 values a lane; small
-// teams share a workgroup of four waves.
+// A team of kWaves waves holds a row, kChunks times 8 values a lane; teams of one
+// wave share a workgroup of four.
 template <int kWaves>
 constexpr int teams() {
-    return kWaves < 4 ? 4 / kWaves : 1;
+    return kWaves < 2 ? 4 : 1;
 }
 
 // ------------------------------------------------------------------ forward
@@ -539,16 +539,21 @@ __global__ __launch_bounds__(kRunWaves * kWave) void block_norm_runs_kernel(Grad
 
 int runs_of(int T) { return T < kRuns ? T : kRuns; }
 
-// f(waves, chunks) with the team that holds a row of D values.
+// f(waves, chunks) with the team that holds a row of D values: waves as few as keep
+// registers for many, for a row's barriers are theirs.  us of 2^25 values, a BF16 stream
+// then an FP32 one: 1152 (2, 2) 45 and 63, (4, 1) 60 and 64; 2048 40 and 65, 41 and 63; 4096
+// (4, 2) 39 and 65, (8, 1) 42 and 65; 8192 (8, 2) 41 and 66, (16, 1) 46 and 65; 12288 (8, 3) 42 and 66,
+// (16, 2) 58 and 73; 16384 (8, 4) 47 and 70, (16, 2) 54 and 71.
 template <typename F>
 hipError_t with_team(int D, F f) {
     using std::integral_constant;
     if (D <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
     if (D <= 1024) return f(integral_constant<int, 1>{}, integral_constant<int, 2>{});
-    if (D <= 2048) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+    if (D <= 2048) return f(integral_constant<int, 2>{}, integral_constant<int, 2>{});
     if (D <= 4096) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
     if (D <= 8192) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-    return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+    if (D <= 12288) return f(integral_constant<int, 8>{}, integral_constant<int, 3>{});
+    return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
 }
 
 }  // namespace
