@@ -256,7 +256,7 @@ __global__ __launch_bounds__(kWaves* teams<kWaves>() * kWave) void block_norm_ke
 }
 
 // ----------------------------------------------------------------- gradient
-// A workgroup of eight waves, in teams of as many as a row takes, goes over a run
+// A workgroup of eight waves (four: see two_groups), in teams of as many as a row takes, goes over a run
 // of rows.  The next row is on its way while one is worked on: a row is four
 // sums over it, two of which can wait for the others, so a row costs two
 // barriers; the sum of the next row's y^2 goes with the second.
@@ -264,8 +264,9 @@ __global__ __launch_bounds__(kWaves* teams<kWaves>() * kWave) void block_norm_ke
 //   first   sum h'^2 and sum g2 h'   (g2 = dz w2: mean(g2 n2) = r2 mean(g2 h'))
 //   second  sum g1 n1 of this row, sum y^2 of the next
 //
-// Measured, all gradients, an FP32 stream: 8192 rows of 4096 137 us, 4.4 TB/s; the
-// instructions of one workgroup a compute unit bound it, two waves a SIMD.
+// Measured, all gradients, an FP32 stream: 8192 rows of 4096 137 us, 4.4 TB/s, and no
+// less with a tenth of the instructions taken out or with two workgroups a compute
+// unit: memory bounds it, four arrays read and two written at once.
 // Rows past 8192 (kLong) would fill the registers: their sums over the rows lie in
 // LDS, weights are read row by row and no row is ahead (4 chunks of eight
 // waves: 2048 rows of 16384 275 us, 2 chunks of sixteen 328, with all in registers, most
@@ -274,7 +275,7 @@ __global__ __launch_bounds__(kWaves* teams<kWaves>() * kWave) void block_norm_ke
 // Sums over the rows are taken in three steps, none of whose order is left to
 // chance: a lane adds its columns row by row, the teams join in LDS, and a second
 // kernel adds the workgroups' sums in FP64.
-constexpr int kRuns = 256;
+constexpr int kMaxRuns = 512;
 constexpr int kRunWaves = 16;  // of block_norm_runs_kernel
 
 struct GradArgs {
@@ -284,14 +285,14 @@ struct GradArgs {
     int runs;
 };
 
-template <int kWaves, int kChunks, bool kF32>
-__global__ __launch_bounds__(8 * kWave) void block_norm_grad_kernel(GradArgs k) {
-    constexpr int kLanes = kWaves * kWave, kTeams = 8 / kWaves;
+template <int kWaves, int kChunks, bool kF32, int kGroup>
+__global__ __launch_bounds__(kGroup* kWave, 2) void block_norm_grad_kernel(GradArgs k) {
+    constexpr int kLanes = kWaves * kWave, kTeams = kGroup / kWaves;
     constexpr bool kLong = kChunks > 2;
     constexpr f32x8_t kZero = {0, 0, 0, 0, 0, 0, 0, 0};
     __shared__ double box[kLong ? 3 : 2][kTeams][kWaves][2];
     __shared__ f32x4_t far_sums[kLong ? 2 : 1][kLong ? 2 * kChunks : 1][kLong ? kLanes : 1];
-    __shared__ f32x8_t join[kTeams == 1 ? 1 : 4 * kWave][kChunks];
+    __shared__ f32x8_t join[kTeams == 1 ? 1 : kGroup / 2 * kWave][kChunks];
     const w4_norm_args& a = k.a;
     const w4_norm_grad_args& g = k.g;
     const int team = kTeams == 1 ? 0 : (int)sgpr(threadIdx.x / kLanes);
@@ -431,7 +432,7 @@ __global__ __launch_bounds__(8 * kWave) void block_norm_grad_kernel(GradArgs k) 
                     grow(1, c, sum_z, row.dz[c].values(), n2);
                 }
                 if (g.dh_out) dx[c] += row.dho[c].values();
-                if (g.dh) store<kF32>(g.dh, t * g.dh_stride + d, a.y ? dx[c] * a.residual_scale : dx[c]);
+                if (g.dh) store<kF32, !kF32>(g.dh, t * g.dh_stride + d, a.y ? dx[c] * a.residual_scale : dx[c]);
                 if (!a.y) continue;
                 f32x8_t b = dx[c] * a.branch_scale;
                 if (a.gate) {
@@ -441,7 +442,7 @@ __global__ __launch_bounds__(8 * kWave) void block_norm_grad_kernel(GradArgs k) 
                     if (shared_gate) {
                         sum_g[c] += u;
                     } else if (g.d_gate) {
-                        store<false>(g.d_gate, t * g.d_gate_stride + d, u);
+                        store<false, !kF32>(g.d_gate, t * g.d_gate_stride + d, u);
                     }
                     b *= gate[c].values();
                 }
@@ -466,7 +467,7 @@ __global__ __launch_bounds__(8 * kWave) void block_norm_grad_kernel(GradArgs k) 
 #pragma unroll
                     for (int i = 0; i < 8; ++i) dx[c][i] = r1.of(fmaf(-mean1, n[i], dx[c][i]));
                 }
-                store<false>(g.dy, t * g.dy_stride + (c * kLanes + tid) * 8, dx[c]);
+                store<false, !kF32>(g.dy, t * g.dy_stride + (c * kLanes + tid) * 8, dx[c]);
             }
         }
         if constexpr (!kLong) row = next;
@@ -508,8 +509,9 @@ __global__ __launch_bounds__(8 * kWave) void block_norm_grad_kernel(GradArgs k) 
     if (g.d_gate && shared_gate) put(2, sum_g);
 }
 
-// Adds the runs of one column of one of the three sums: sixteen lanes a column,
-// all their loads at once.
+// Adds the runs (kMost at most) of one column of one of the three sums: sixteen lanes a
+// column, all their loads at once.
+template <int kMost>
 __global__ __launch_bounds__(kRunWaves * kWave) void block_norm_runs_kernel(GradArgs k) {
     __shared__ double box[kRunWaves][kWave];
     float* out[3] = {k.g.d_y_weight, k.g.d_z_weight,
@@ -519,15 +521,15 @@ __global__ __launch_bounds__(kRunWaves * kWave) void block_norm_runs_kernel(Grad
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int d = blockIdx.x * kWave + lane;
     const float* from = k.part + (int64_t)blockIdx.y * k.runs * k.a.D + d;
-    float v[kRuns / kRunWaves];
+    float v[kMost / kRunWaves];
 #pragma unroll
-    for (int i = 0; i < kRuns / kRunWaves; ++i) {
+    for (int i = 0; i < kMost / kRunWaves; ++i) {
         const int r = wave + kRunWaves * i;
         v[i] = r < k.runs && d < k.a.D ? from[(int64_t)r * k.a.D] : 0.0f;
     }
     double s = 0;
 #pragma unroll
-    for (int i = 0; i < kRuns / kRunWaves; ++i) s += (double)v[i];
+    for (int i = 0; i < kMost / kRunWaves; ++i) s += (double)v[i];
     box[wave][lane] = s;
     __syncthreads();
     if (wave == 0 && d < k.a.D) {
@@ -537,7 +539,17 @@ __global__ __launch_bounds__(kRunWaves * kWave) void block_norm_runs_kernel(Grad
     }
 }
 
-int runs_of(int T) { return T < kRuns ? T : kRuns; }
+// Whether four waves take a row of 2049 to 4096 values and two workgroups share a compute
+// unit, each at its own row, in place of eight waves a row and one workgroup: a barrier
+// then stops half of the unit.  Twice the runs are twice the sums to join.  All
+// gradients, rows of 4096, two workgroups first: 8192 rows with a BF16 stream 102 us and
+// 118 (3.9 TB/s), with an FP32 one, more of it memory, 139 and 138; 512 rows of 2048 in
+// as many runs 24 and 17.
+bool two_groups(int T, int D, bool f32) { return !f32 && T >= 4096 && D > 2048 && D <= 4096; }
+int runs_of(int T, int D, bool f32) {
+    const int most = two_groups(T, D, f32) ? kMaxRuns : kMaxRuns / 2;
+    return T < most ? T : most;
+}
 
 // f(waves, chunks) with the team that holds a row of D values: waves as few as keep
 // registers for many, for a row's barriers are theirs.  us of 2^25 values, a BF16 stream
@@ -574,35 +586,43 @@ hipError_t launch_block_norm(const w4_norm_args& a, hipStream_t stream) {
     });
 }
 
-size_t block_norm_grad_workspace_bytes(int T, int D) { return (size_t)3 * runs_of(T) * D * sizeof(float); }
+size_t block_norm_grad_workspace_bytes(int T, int D) { return (size_t)3 * runs_of(T, D, false) * D * sizeof(float); }
 
 hipError_t launch_block_norm_grad(const w4_norm_args& a, const w4_norm_grad_args& g, void* workspace, hipStream_t stream) {
-    GradArgs k = {a, g, static_cast<float*>(workspace), runs_of(a.T)};
+    GradArgs k = {a, g, static_cast<float*>(workspace), runs_of(a.T, a.D, a.h_f32)};
     if (a.T > 0) {
-        const dim3 grid((unsigned)k.runs), block(8 * kWave);
-        const auto launch = [&](auto waves, auto chunks) {
-            constexpr int kW = decltype(waves)::value, kC = decltype(chunks)::value;
-            if (a.h_f32) {
-                block_norm_grad_kernel<kW, kC, true><<<grid, block, 0, stream>>>(k);
-            } else {
-                block_norm_grad_kernel<kW, kC, false><<<grid, block, 0, stream>>>(k);
+        const auto launch = [&](auto waves, auto chunks, auto group) {
+            constexpr int kW = decltype(waves)::value, kC = decltype(chunks)::value, kG = decltype(group)::value;
+            const dim3 grid((unsigned)k.runs), block(kG * kWave);
+            if (!a.h_f32) {
+                block_norm_grad_kernel<kW, kC, false, kG><<<grid, block, 0, stream>>>(k);
+            } else if constexpr (kG == 8) {
+                block_norm_grad_kernel<kW, kC, true, kG><<<grid, block, 0, stream>>>(k);
             }
             return hipGetLastError();
         };
         using std::integral_constant;
         constexpr integral_constant<int, 1> one{};
+        constexpr integral_constant<int, 2> two{};
+        constexpr integral_constant<int, 4> four{};
         constexpr integral_constant<int, 8> eight{};
-        const hipError_t err = a.D <= 512     ? launch(one, one)
-                               : a.D <= 1024  ? launch(integral_constant<int, 2>{}, one)
-                               : a.D <= 2048  ? launch(integral_constant<int, 4>{}, one)
-                               : a.D <= 4096  ? launch(eight, one)
-                               : a.D <= 8192  ? launch(eight, integral_constant<int, 2>{})
-                               : a.D <= 12288 ? launch(eight, integral_constant<int, 3>{})
-                                              : launch(eight, integral_constant<int, 4>{});
+        const hipError_t err = a.D <= 512     ? launch(one, one, eight)
+                               : a.D <= 1024  ? launch(two, one, eight)
+                               : a.D <= 2048  ? launch(four, one, eight)
+                               : two_groups(a.T, a.D, a.h_f32) ? launch(four, two, four)
+                               : a.D <= 4096  ? launch(eight, one, eight)
+                               : a.D <= 8192  ? launch(eight, two, eight)
+                               : a.D <= 12288 ? launch(eight, integral_constant<int, 3>{}, eight)
+                                              : launch(eight, four, eight);
         if (err != hipSuccess) return err;
     }
     if (!g.d_y_weight && !g.d_z_weight && !(g.d_gate && a.gate_stride == 0)) return hipSuccess;
-    block_norm_runs_kernel<<<dim3((unsigned)((a.D + kWave - 1) / kWave), 3), dim3(kRunWaves * kWave), 0, stream>>>(k);
+    const dim3 grid((unsigned)((a.D + kWave - 1) / kWave), 3), block(kRunWaves * kWave);
+    if (k.runs <= kMaxRuns / 2) {
+        block_norm_runs_kernel<kMaxRuns / 2><<<grid, block, 0, stream>>>(k);
+    } else {
+        block_norm_runs_kernel<kMaxRuns><<<grid, block, 0, stream>>>(k);
+    }
     return hipGetLastError();
 }
 

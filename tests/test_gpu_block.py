@@ -294,6 +294,14 @@ def test_block_norm_grad_parts(T, D, kind, post, pre, gate, dho, dz, leave):
     check_grad(run_grad(v, dho, dz, 0.9, 0.5, leave=leave), *grad_bounds(v, dho, dz, 0.9, 0.5, 1e-6, 0.0, kind))
 
 
+@pytest.mark.parametrize("T,kind,gate", [(4095, f32, "token"), (4096, bf16, "token"), (4099, f32, "channel"), (4099, bf16, None)])
+def test_block_norm_grad_of_many_rows(T, kind, gate):
+    """On both sides of where two workgroups share a compute unit."""
+    v = norm_case(24, T, 2064, kind, gate, True, True)
+    dho, dz = tensor(25, (T, 2064), 0.3, kind), tensor(26, (T, 2064))
+    check_grad(run_grad(v, dho, dz, 0.9, 0.5), *grad_bounds(v, dho, dz, 0.9, 0.5, 1e-6, 0.0, kind))
+
+
 @pytest.mark.parametrize("kind", [bf16, f32])
 def test_block_norm_grad_of_the_stream_alone_and_in_place(kind):
     v = dict(h=tensor(17, (20, 896), 3.0, kind), y=None, y_weight=None, z_weight=tensor(18, (896,), 0.2, mean=1.0), gate=None)
