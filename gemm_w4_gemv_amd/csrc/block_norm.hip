@@ -182,7 +182,7 @@ constexpr int teams() {
 // Measured: 4099 rows of 3840, a BF16 stream 21 us, 6.1 TB/s; one row 5.5 us, which is the
 // call's.
 // kApart: results go past the caches' ways of keeping them.  4099 rows of 3840: 28
-// us without, 21.5 with; a row later read by another norm, 256 rows 9.1 and 8.3, 64
+// us without, 21 with; a row later read by another norm, 256 rows 9.1 and 8.3, 64
 // rows 7.3 and 7.5.
 template <int kWaves, int kChunks, bool kF32, bool kApart>
 __global__ __launch_bounds__(kWaves* teams<kWaves>() * kWave) void block_norm_kernel(w4_norm_args a) {

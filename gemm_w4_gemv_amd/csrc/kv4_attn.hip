@@ -1537,7 +1537,7 @@ constexpr int kThreads = 256;
 // workgroup of each has both at work.
 // Measured with the join: 64 requests behind 16384 tokens, 32 and 8 heads of 128: 60 us,
 // 300 TFLOP/s of the prefix's two products; 32 behind 8192, 16 and 8 heads of 256: 33 us.
-// Of the first 52 are this kernel's, whose vector instructions (170 a wave's tile, beside 26
+// Of the first 52 are this kernel's, whose vector instructions (some 200 a wave's tile, beside 26
 // products and 20 reads of LDS) keep their unit busy 63 cycles of 100 and whose products
 // the matrix unit 29.  Three workgroups a compute unit (24 splits) take 67 us; the next
 // tile's scores beside this one's weights, which wants a third buffer and 210 registers, 80.

@@ -25,7 +25,7 @@ constexpr int kAlone = 4096;  // choices that every workgroup counts itself
 // Counts of a table that every workgroup sums, at most, its chunks of kLongChunk choices;
 // larger ones are summed once, of kChunk choices or more.  us of both, the first
 // first: 683 tokens of 6 choices, 64 experts, rows of 4096 (320 counts) 11.9 and 13.6; 8191
-// (3072 counts) 87 either way; 4096 of 8, 256 experts, 2048 (8192) 43 and 33; 32768 of 8, 64
+// (48 chunks) 87 either way; 4096 of 8, 256 experts, 2048 (8192) 43 and 33; 32768 of 8, 64
 // experts, 256 (16384) 191 and 50.
 constexpr int kTable = 4096;
 constexpr int kLongChunk = 1024, kChunk = 256;
