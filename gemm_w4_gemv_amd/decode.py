@@ -300,6 +300,8 @@ class DecodeStep:
         ends, last = {}, -1
         for lin in self.linears:
             name, layer = lin["name"], lin["layer"]
+            if name != "logits" and name not in turn:
+                raise ValueError(f"no linear of a decoder layer is named '{name}'")
             at = 4 * self.norms.layers if name == "logits" else 4 * layer + turn[name]
             if name != "logits" and not 0 <= layer < self.norms.layers:
                 raise ValueError(f"layer {layer}: the norms have {self.norms.layers} layers")

@@ -42,7 +42,7 @@ def test_norms_refuse_an_order_that_could_not_work():
 
     check(good)
     for bad in (good[:3] + good[4:], good[:6] + good[7:], [good[3]] + good[:3] + good[4:], good[:4] + [good[6]] + good[4:6] + good[7:],
-                [("logits", 1)] + good[:-1], [("q", 1)] + good[1:], good[:4] + good[3:]):
+                [("logits", 1)] + good[:-1], [("q", 1)] + good[1:], good[:4] + good[3:], [("w", 0)] + good):
         with pytest.raises(ValueError):
             check(bad)
     with pytest.raises(ValueError):
