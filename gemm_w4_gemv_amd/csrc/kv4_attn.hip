@@ -1881,7 +1881,8 @@ SharedCut shared_cut_of(const w4_attn_args& a, int prefix, const w4_kv4_cache& c
     // 34; heads of 64, 4096 (64, 2048, 64 and 8 heads) 18.6 and 20.9, 16384 (64, 8192) 61 and 41.  A
     // request of more than 8 rows has products of its own full enough (24 requests of up to
     // 5 rows of 8 heads, heads of 64, behind 4112: 54 and 38).
-    // Long prompts, with rows enough of their own, are done request by request.
+    // Long prompts, with rows enough of their own, are done request by request, and more
+    // rows than the join's launch could count.
     const int64_t units = B * own_row_tiles * c.kv_heads * tiles, each = (rows + B - 1) / B;
     if (a.T < 2 || own_rows > 64 || rows * c.kv_heads > (1 << 22) || units <= (each < 8 ? each : 8) * (c.head_dim == 64 ? 6144 : 2048)) return k;
     const int64_t own_groups = B * c.kv_heads * own_row_tiles, groups = c.kv_heads * ((rows + 63) / 64);

@@ -624,3 +624,59 @@ def test_the_most_tokens_of_one_call():
     assert start.tolist() == [0, *np.cumsum(sizes).tolist()]
     at = torch.arange(T, device=DEV)
     assert torch.equal(rows[:, 0].long(), start[:1000].long()[at % 1000] + at // 1000)
+
+
+def test_graphs_that_share_a_workspace():
+    """Calls of several launches: three graphs over one workspace, replayed in turn with eager calls between."""
+    v = norm_case(70, 4096, 2056, bf16, "channel", True, True)
+    dz = tensor(71, (4096, 2056))
+    grads = {n: torch.zeros(2056, device=DEV) for n in ("d_y_weight", "d_z_weight", "d_gate")}
+    grads["dy"] = torch.zeros_like(v["y"])
+    few, many = ints(routed(72, 3000, 6, 16, 0.1)), ints(routed(73, 3000, 8, 256, 0.1))
+    x = tensor(74, (3000, 64))
+    out = [(torch.zeros(E + 1, dtype=torch.int32, device=DEV), torch.zeros_like(ids), torch.zeros(ids.numel(), 64, dtype=bf16, device=DEV))
+           for E, ids in ((16, few), (256, many))]
+    sizes = [w4.w4_block_norm_grad_workspace_bytes(4096, 2056), w4.w4_moe_sort_workspace_bytes(3000, 6, 16),
+             w4.w4_moe_sort_workspace_bytes(3000, 8, 256)]
+    assert all(sizes)
+    work = torch.full((max(sizes),), 0xAB, dtype=torch.uint8, device=DEV)
+    calls = [lambda s: w4.w4_block_norm_grad(**v, dz=dz, workspace=work, stream=s, **grads)]
+    for (start, row_of, rows), E, ids in ((out[0], 16, few), (out[1], 256, many)):
+        calls.append(lambda s, start=start, row_of=row_of, rows=rows, E=E, ids=ids:
+                     w4.w4_moe_sort(ids, E, start, row_of, x=x, rows=rows, capacity=500, workspace=work, stream=s))
+    results = [list(grads.values()), list(out[0]), list(out[1])]
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graphs = []
+    for call in calls:
+        w4.w4_graph_begin(stream)
+        try:
+            call(stream)
+        finally:
+            graphs.append(w4.w4_graph_end(stream))
+    for k in range(3):
+        v["y"].copy_(tensor(75 + k, tuple(v["y"].shape)))
+        few.copy_(ints(routed(75 + k, 3000, 6, 16, 0.1)))
+        many.copy_(ints(routed(78 + k, 3000, 8, 256, 0.1)))
+        got = []
+        for graph, tensors in zip(graphs, results):
+            for t in tensors:
+                t.fill_(3)
+            torch.cuda.synchronize()
+            graph.replay(stream)
+        torch.cuda.synchronize()
+        got = [[t.clone() for t in tensors] for tensors in results]
+        work.fill_(0xCD)
+        for call, tensors in zip(calls, results):
+            for t in tensors:
+                t.fill_(3)
+            torch.cuda.synchronize()
+            call(stream)
+        torch.cuda.synchronize()
+        for first, tensors in zip(got, results):
+            for a, b in zip(first, tensors):
+                assert torch.equal(a, b)
+        want = ref.moe_sort(many.cpu().numpy(), 256, 500)
+        assert out[1][0].tolist() == list(want[0]) and np.array_equal(out[1][1].cpu().numpy(), want[1])
+    for graph in graphs:
+        graph.destroy()
