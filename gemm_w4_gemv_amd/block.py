@@ -227,9 +227,9 @@ def _choices(row_of, weights, T, R, device):
     """(choices a token, row_of's address, weights' address)."""
     given = row_of if row_of is not None else weights
     if given is None:
-        if T == 0 or R % T:
+        if R % T if T else R:
             raise ValueError(f"without row_of and weights, {R} rows must be as many for each of {T} tokens")
-        top = R // T
+        top = R // T if T else 1
     else:
         if not isinstance(given, torch.Tensor) or given.dim() != 2 or given.shape[0] != T:
             raise ValueError(f"row_of and weights must be [{T}, top]")

@@ -496,6 +496,26 @@ def test_moe_combine_grad(T, top, R, N, weighted):
     assert torch.equal(over[moved], dy[moved]) and torch.equal(over[~moved], y[~moved])
 
 
+def test_empty_calls():
+    """No tokens, or rows of which none are asked for: nothing is written, nothing is wrong."""
+    none, some = torch.zeros(0, 64, dtype=bf16, device=DEV), tensor(50, (6, 64))
+    ids = torch.zeros(0, 3, dtype=torch.int32, device=DEV)
+    assert w4.w4_moe_combine(none, none) is none
+    w4.w4_moe_combine(some, none, row_of=ids)
+    w4.w4_moe_combine_grad(none, none, dy=none)
+    left = some.clone()
+    w4.w4_moe_combine_grad(none, some, row_of=ids, dy=some, dweights=ids.float())
+    w4.w4_block_norm(none, none, h_out=none, z=none)
+    start, row_of, *_ = run_sort(np.zeros((0, 3), dtype=np.int32), 4)
+    assert start.tolist() == [0] * 5
+    torch.cuda.synchronize()
+    assert torch.equal(some, left)
+    with pytest.raises(ValueError):
+        w4.w4_moe_combine(some, none)
+    with pytest.raises(ValueError):
+        w4.w4_moe_combine(some, some[:4])
+
+
 def test_gradient_of_sorting_and_back_against_the_formula():
     """x -> rows -> (rows as they are) -> out: the gradients of the pair against those of the same sums in 64 bits."""
     T, top, E, N = 29, 4, 12, 136
