@@ -1991,7 +1991,7 @@ hipError_t launch_kv4_attn_shared(const w4_attn_args& a, const int32_t* prefix_t
     own.part_o = base + space.own_o;
     own.part_ml = base + space.own_ml;
     shared.table = prefix_table;
-    shared.width = (prefix + c.block_size - 1) / c.block_size;
+    shared.width = (int)(((int64_t)prefix + c.block_size - 1) / c.block_size);  // prefix may be 2^31 - 1
     shared.B = 1;
     shared.row_tiles = cut.row_tiles;
     shared.splits = cut.splits;

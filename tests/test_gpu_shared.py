@@ -240,3 +240,22 @@ def test_attn_shared_repeats_its_bits_on_another_stream():
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     assert np.array_equal(run(dev, q, table, lens, q_start, shared, 1024, stream=side), want)
+
+
+@pytest.mark.parametrize("prefix", [2 ** 31 - 1, 2 ** 31 - 255])
+def test_attn_shared_prefix_within_a_page_of_2_31(prefix):
+    """A prefix far longer than any request, its last page's end past 2^31 - 1: what the requests hold of it is read."""
+    lens, B, hq, hkv, dim, block = [700, 1, 900, 256, 0, 257], 48, 8, 8, 64, 256
+    lens = lens * (B // len(lens))
+    assert apart(prefix, lens, [1] * B, hq, hkv, dim, block)
+    cache, q = random_cache(9, 6, block, hkv, dim), si.bf16_normal(9, (96,), (B, hq, dim))
+    pages = si.rng(9, 97).permutation(6)
+    far = ints(np.resize(pages, -(-prefix // block)))
+    table, out = ints(np.tile(pages[:4], (B, 1))), torch.full((B, hq, dim), 7.0, dtype=bf16, device=DEV)
+    dev = to_device(cache)
+    size = w4.w4_kv4_attn_shared_workspace_bytes(dev, B, B, hq, 1, 900, prefix)
+    work = torch.full((size // 4,), float("nan"), dtype=torch.float32, device=DEV)
+    w4.w4_kv4_attn_shared(q=host.bf16_tensor(q), cache=dev, block_table=table, kv_lens=ints(lens), out=out, prefix_table=far,
+                          prefix=prefix, max_kv=900, workspace=work)
+    torch.cuda.synchronize()
+    check_attn(host.bf16_values(out), *expect(cache, q, np.tile(pages[:4], (B, 1)), lens, range(B + 1), dim))
