@@ -457,6 +457,17 @@ __global__ __launch_bounds__(kGroup* kWave, 2) void block_norm_grad_kernel(GradA
             }
         }
         m = m1;
+        // in FP64, as in products, where the lane's sum leaves FP32
+        if (live && a.y && a.y_weight && __any(!(m1 < INFINITY && m1 > -INFINITY))) {
+            m = 0;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                if (!here(c)) continue;
+                const f32x8_t n = n1(c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = fma((double)dx[c][i], (double)n[i], m);
+            }
+        }
         if constexpr (!kLong) sy = squares_of_y(next, t + kTeams);
         team_sums<kWaves>(m, sy, box[1][team], wave, lane);
         if (live && a.y && g.dy) {

@@ -303,6 +303,16 @@ def test_block_norm_grad_of_many_rows(T, kind, gate):
 
 
 @pytest.mark.parametrize("kind", [bf16, f32])
+@pytest.mark.parametrize("D", [512, 1024, 2048, 4096, 8192, 16384])
+def test_block_norm_grad_of_far_gradients(D, kind):
+    """Gradients whose products with y's norm, eight or more of one sign in a lane, pass FP32 where the result does not."""
+    v = norm_case(27, 3, D, kind, None, True, True)
+    dho = (0.7e38 * torch.sign(v["y"].float()) * torch.tensor([[1.0], [-1.0], [2.0 ** -120]], device=DEV)).to(kind)
+    rest = (1.0, 1.0, 1e-6, 0.0)
+    check_grad(run_grad(v, dho, None, *rest, leave=("d_y_weight", "d_z_weight")), *grad_bounds(v, dho, None, *rest, kind))
+
+
+@pytest.mark.parametrize("kind", [bf16, f32])
 def test_block_norm_grad_of_the_stream_alone_and_in_place(kind):
     v = dict(h=tensor(17, (20, 896), 3.0, kind), y=None, y_weight=None, z_weight=tensor(18, (896,), 0.2, mean=1.0), gate=None)
     dho, dz = tensor(19, (20, 896), 0.3, kind), tensor(20, (20, 896))
