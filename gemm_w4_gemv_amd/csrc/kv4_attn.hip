@@ -368,18 +368,21 @@ struct Rows {
         }
     }
 
-    // The rows' positions, of tokens ``first`` on, and the first and last of them (they are in no order).
+    // The rows' positions, of tokens ``first`` on (they are in no order): the lowest and the
+    // highest of them, -1 where a row sees nothing, and the lowest of those that see any.
     __device__ __forceinline__ void place(const AttnArgs& a, const int* of, int first, int r0, int rows, int lane, int* low,
-                                          int* high) {
+                                          int* seeing, int* high) {
 #pragma unroll
         for (int n = 0; n < kNB; ++n) {
             const int mine = r0 + 16 * n + (lane & 15), at = of[min(mine, rows - 1) / a.g - first];
             pos[n] = mine < rows ? at : -1;
         }
-        int lo = pos[0], hi = pos[0];
+        int lo = 0x7FFFFFFF, hi = -1;
+        bool all = true;
 #pragma unroll
-        for (int n = 1; n < kNB; ++n) {
-            lo = min(lo, pos[n]);
+        for (int n = 0; n < kNB; ++n) {
+            all &= pos[n] >= 0;
+            lo = min(lo, pos[n] < 0 ? 0x7FFFFFFF : pos[n]);
             hi = max(hi, pos[n]);
         }
 #pragma unroll
@@ -387,7 +390,8 @@ struct Rows {
             lo = min(lo, __shfl_xor(lo, x));
             hi = max(hi, __shfl_xor(hi, x));
         }
-        *low = (int)sgpr((uint32_t)lo);
+        *seeing = (int)sgpr((uint32_t)lo);
+        *low = __all(all) ? *seeing : -1;
         *high = (int)sgpr((uint32_t)hi);
     }
 
@@ -1344,6 +1348,7 @@ __device__ __forceinline__ void many_rows(const AttnArgs& a, int id, ManyLds<D, 
     // this wave's rows; past the last there may be none
     const int r0 = min(base + wave * kCols, rows);
     int my_low = first_pos + min(r0, rows - 1) / a.g, my_high = first_pos + (min(r0 + kCols, rows) - 1) / a.g;
+    int my_seeing = max(my_low, 0);
     R rw;
     // A shared prefix: the positions of the workgroup's rows.  Only with a window do the
     // tiles depend on them; without one the first tiles are sent for before they are known.
@@ -1363,9 +1368,9 @@ __device__ __forceinline__ void many_rows(const AttnArgs& a, int id, ManyLds<D, 
         if (a.window != 0) {
             set_positions();
             __syncthreads();
-            rw.place(a, pos, base / a.g, r0, rows, lane, &my_low, &my_high);
+            rw.place(a, pos, base / a.g, r0, rows, lane, &my_low, &my_seeing, &my_high);
             if (lane == 0) {
-                reach[wave][0] = r0 < rows ? my_low : 0x7FFFFFFF;
+                reach[wave][0] = my_seeing;
                 reach[wave][1] = my_high;
             }
             __syncthreads();
@@ -1470,7 +1475,7 @@ __device__ __forceinline__ void many_rows(const AttnArgs& a, int id, ManyLds<D, 
     rw.start();
     if (kShared && a.window == 0) set_positions();
     lds_barrier();
-    if (kShared && a.window == 0) rw.place(a, pos, base / a.g, r0, rows, lane, &my_low, &my_high);
+    if (kShared && a.window == 0) rw.place(a, pos, base / a.g, r0, rows, lane, &my_low, &my_seeing, &my_high);
 
     const float slack = fminf(8.0f / a.scale2, 3e38f);
     const u32x4_t ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
@@ -1491,7 +1496,7 @@ __device__ __forceinline__ void many_rows(const AttnArgs& a, int id, ManyLds<D, 
         // Rows of a wave that lie before the tile, or before whose window it ends, pass
         // it over.  (Positions below 0 see nothing; less a window they could pass 32 bits.)
         const bool sees = r0 < rows && t0 <= my_high &&
-                          (a.window == 0 || t0 + kTile - 1 > max(my_low, 0) - a.window || t0 < a.sinks);
+                          (a.window == 0 || t0 + kTile - 1 > my_seeing - a.window || t0 < a.sinks);
         if (sees) {
             const bool whole = t0 + kTile - 1 <= my_low && (a.window == 0 || t0 > my_high - a.window || t0 + kTile <= a.sinks) &&
                                page[0][0] >= 0 && page[0][1] >= 0 && r0 + kCols <= rows;

@@ -259,3 +259,45 @@ def test_attn_shared_prefix_within_a_page_of_2_31(prefix):
                           prefix=prefix, max_kv=900, workspace=work)
     torch.cuda.synchronize()
     check_attn(host.bf16_values(out), *expect(cache, q, np.tile(pages[:4], (B, 1)), lens, range(B + 1), dim))
+
+
+def test_attn_shared_window_with_rows_that_see_nothing():
+    """A window over a part of the prefix, requests with more rows than tokens and empty ones among the rest."""
+    prefix, lens, news = 2048, [5, 2100, 0, 2049] * 8, [9, 1, 0, 2] * 8
+    assert apart(prefix, lens, news, 8, 8, 128, 64, 1500)
+    cache, shared, table, q_start, q = case(10, prefix, lens, news, 8, 8, 128, 64)
+    dev = to_device(cache)
+    for window, sinks in ((1500, 0), (1500, 40), (1900, 0)):
+        got = run(dev, q, table, lens, q_start, shared, prefix, window=window, sinks=sinks, tail=3)
+        assert np.all(got[-3:] == 7.0)
+        check_attn(got[:-3], *expect(cache, q, table, lens, q_start, 128, window, sinks), f"window {window}, {sinks} first tokens")
+
+
+def test_attn_shared_window_is_not_passed_by_for_a_row_that_is_not_there():
+    """40 rows, of which the last block of 16 is half empty, and rows of no request take a window's tiles, not all of the
+    prefix's: 512 tiles of 32768, where 48 rows take as many.  (Three times is far from both: 64 times the tiles.)"""
+    prefix, block, hq, hkv, dim, window = 1 << 20, 256, 16, 8, 128, 1 << 14
+    dev = to_device(random_cache(11, 6, block, hkv, dim))
+    far = ints(np.resize(np.arange(6), prefix // block))
+    times = {}
+    for rows, tail in ((24, 0), (20, 0), (22, 2)):
+        lens = [prefix + 1 + i for i in range(rows)]
+        assert apart(prefix, lens, [1] * rows, hq, hkv, dim, block, window)
+        T = rows + tail
+        q, q_start = host.bf16_tensor(si.bf16_normal(11, (98, rows), (T, hq, dim))), ints(range(rows + 1))
+        table, out = torch.cat((far, ints([0]))).repeat(rows, 1), torch.zeros(T, hq, dim, dtype=bf16, device=DEV)
+        size = w4.w4_kv4_attn_shared_workspace_bytes(dev, T, rows, hq, 1, max(lens), prefix, window)
+        work = torch.empty(size, dtype=torch.uint8, device=DEV)
+        args = (q, dev, table, ints(lens), out, far, prefix)
+        kw = dict(q_start=q_start, max_kv=max(lens), window=window, workspace=work)
+        took = []
+        for _ in range(8):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(4):
+                w4.w4_kv4_attn_shared(*args, **kw)
+            b.record()
+            torch.cuda.synchronize()
+            took.append(a.elapsed_time(b))
+        times[T, tail] = min(took)
+    assert max(times.values()) < 3 * times[24, 0], times
