@@ -1880,16 +1880,41 @@ SharedCut shared_cut_of(const w4_attn_args& a, int prefix, const w4_kv4_cache& c
     // units of a tile against 16 rows.  Together they cost by the rows, and the parts'
     // way through memory and a join.  us request by request, then together, by units
     // over rows a request: heads of 128, 2048 (4 requests behind 8192 tokens, 32 and 8 heads)
-    // 15.9 and 17.7, 2048 (64, 8192, 8 and 1 heads) 22.8 and 24.2, 4096 (16, 4096) 23.4 and
-    // 15.9, 4096 (64, 1024) 17.0 and 16.5, 65536 (64, 16384) 150 and 60; heads of 256, 2048
-    // (4, 4096, 16 and 8 heads) 17.7 and 18.4, 4096 (16, 2048) 22.0 and 16.2, 32768 (32, 8192) 99 and
-    // 34; heads of 64, 4096 (64, 2048, 64 and 8 heads) 18.6 and 20.9, 16384 (64, 8192) 61 and 41.  A
-    // request of more than 8 rows has products of its own full enough (24 requests of up to
-    // 5 rows of 8 heads, heads of 64, behind 4112: 54 and 38).
+    // 15.9 and 17.7, 2048 (64, 8192, 8 and 1 heads) 22.8 and 24.2, 2304 (36, 1024, 8 and 4 heads)
+    // 11.2 and 14.0, 4608 (36, 2048) 16.2 and 14.7, 4096 (16, 4096) 23.4 and 15.9, 4096 (64,
+    // 1024) 17.0 and 16.5, 65536 (64, 16384) 150 and 60; heads of 256, 2048 (4, 4096, 16 and 8
+    // heads) 17.7 and 18.4, 4096 (16, 2048) 22.0 and 16.2, 32768 (32, 8192) 99 and 34; heads of 64,
+    // 4096 (64, 2048, 64 and 8 heads) 18.6 and 20.9, 16384 (64, 8192) 61 and 41.  A request of more
+    // than 8 rows has products of its own full enough (24 requests of up to 5 rows of 8 heads,
+    // heads of 64, behind 4112: 54 and 38).
     // Long prompts, with rows enough of their own, are done request by request, and more
     // rows than the join's launch could count.
-    const int64_t units = B * own_row_tiles * c.kv_heads * tiles, each = (rows + B - 1) / B;
-    if (a.T < 2 || own_rows > 64 || rows * c.kv_heads > (1 << 22) || units <= (each < 8 ? each : 8) * (c.head_dim == 64 ? 6144 : 2048)) return k;
+    // With a window a request sees ``far`` tokens at most, its own before the prefix's
+    // (max_kv says how many those are), and all requests together the tiles that the
+    // shortest one does; what a window leaves has to be more than without one, for its
+    // tiles differ from row to row.  us request by request, then together, heads of 128, by the
+    // same units: 1536 (64 requests behind 16384 tokens, 32 and 8 heads, window 500) 11.8 and 15.9,
+    // 2088 (36, 8 and 4 heads, 1024) 10.9 and 14.5, 3440 (20, 16 and 8 heads, 1500) 13.0 and 15.7,
+    // 3780 (63, 9 and 3 heads, 2048) 16.6 and 17.4, 4392 (36, 2048) 16.2 and 15.0, 15872 (64, 4096) 41.5
+    // and 25.9; heads of 256, 1536 (32, 16 and 8 heads, 500) 13.1 and 17.4, 3712 (1024) 17.7 and 17.5, 7808
+    // (2048) 26.4 and 18.1; heads of 64, 3840 (64, 64 and 8 heads, 2048) 18.2 and 23.3, 7936 (4096) 31.8
+    // and 28.6.  Up to 32 tiles are few enough to be cut as without a window (36 requests
+    // behind 1024 tokens, 8 and 4 heads of 128: window 300 7.9 and 12.2, 2048 11.0 and 14.2).
+    int64_t own_tokens = (int64_t)a.max_kv - tiles * kTile, seen = tiles, reach = tiles;
+    int64_t least = c.head_dim == 64 ? 6144 : 2048;
+    if (a.window > 0) {
+        const int64_t far = (int64_t)a.window + a.sinks + a.max_q;
+        if (tiles > 32) {
+            const int64_t left = far - a.sinks - (own_tokens > 0 ? own_tokens : 0);
+            const auto some = [&](int64_t tokens) { return tokens / kTile < tiles ? tokens / kTile : tiles; };
+            seen = some(a.sinks + (left > 0 ? left : 0));
+            reach = some(far + kTile);
+            if (c.head_dim != 64) least = 3584;
+        }
+        own_tokens = own_tokens < far ? own_tokens : far;
+    }
+    const int64_t units = B * own_row_tiles * c.kv_heads * seen, each = (rows + B - 1) / B;
+    if (a.T < 2 || own_rows > 64 || rows * c.kv_heads > (1 << 22) || units <= (each < 8 ? each : 8) * least) return k;
     const int64_t own_groups = B * c.kv_heads * own_row_tiles, groups = c.kv_heads * ((rows + 63) / 64);
     if (own_groups > (1 << 20)) return k;
     k.tiles = (int)tiles;
@@ -1901,7 +1926,6 @@ SharedCut shared_cut_of(const w4_attn_args& a, int prefix, const w4_kv4_cache& c
         x = x < most ? x : most;
         return (int)(x < 1 ? 1 : x < kMaxSplits ? x : kMaxSplits);
     };
-    const int64_t own_tokens = (int64_t)a.max_kv - tiles * kTile;
     k.own_splits = bounded(own_tokens / (32 * kTile), 1024 / own_groups);
     // The prefix: two workgroups a compute unit (four with heads of 64, of half the
     // registers), each with eight tiles or more; short prefixes up to 16 of four.  A
@@ -1909,8 +1933,8 @@ SharedCut shared_cut_of(const w4_attn_args& a, int prefix, const w4_kv4_cache& c
     // 8 heads of 256: 16 splits 38.5 us, 24 33.2, 32 34.4, 48 46; 64 behind 16384, 32 and 8
     // heads of 128: 12 70 us, 16 60, 20 64; 64 of 1024, 16 and 8 heads of 256: 4 23.8, 8 22.1, 16
     // 26.8; 64 of 8192, 64 and 8 heads of 64: 8 48, 12 43.4, 16 40.6, 20 46.
-    const int64_t few = tiles / 4 < 16 ? tiles / 4 : 16;
-    k.splits = bounded((c.head_dim == 64 ? 1024 : 512) / groups, few > tiles / 8 ? few : tiles / 8);
+    const int64_t few = reach / 4 < 16 ? reach / 4 : 16;
+    k.splits = bounded((c.head_dim == 64 ? 1024 : 512) / groups, few > reach / 8 ? few : reach / 8);
     return k;
 }
 

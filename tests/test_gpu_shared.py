@@ -301,3 +301,15 @@ def test_attn_shared_window_is_not_passed_by_for_a_row_that_is_not_there():
             took.append(a.elapsed_time(b))
         times[T, tail] = min(took)
     assert max(times.values()) < 3 * times[24, 0], times
+
+
+@pytest.mark.parametrize("prefix,lens,news,hq,hkv,dim,block,window,sinks", [
+    (2048, [2100, 2060, 2300] * 14, [1] * 42, 8, 4, 128, 64, 2000, 0), (1504, [1600, 1510] * 25, [1] * 50, 8, 4, 128, 16, 1400, 6),
+    (2560, [2600, 2561, 2570] * 8, [1, 3, 2] * 8, 16, 8, 256, 64, 2500, 0), (3200, [3300, 3201, 3350] * 11, [1] * 33, 8, 8, 64, 32, 3000, 700),
+    (4096, [4150, 30, 4100] * 8, [1, 2, 1] * 8, 8, 8, 128, 128, 2048, 0),
+])
+def test_attn_shared_window_over_a_part_of_a_long_prefix(prefix, lens, news, hq, hkv, dim, block, window, sinks):
+    assert apart(prefix, lens, news, hq, hkv, dim, block, window, sinks)
+    cache, shared, table, q_start, q = case(12, prefix, lens, news, hq, hkv, dim, block)
+    got = run(to_device(cache), q, table, lens, q_start, shared, prefix, window=window, sinks=sinks)
+    check_attn(got, *expect(cache, q, table, lens, q_start, dim, window, sinks))

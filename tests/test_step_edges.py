@@ -164,3 +164,21 @@ def test_attn_far_negative_sizes_are_negative(name):
     assert size(**{name: FAR}) == size(**{name: 2 ** 31 - 1})
 
 
+# ------------------------------------------------- a shared prefix and a window
+@pytest.mark.parametrize("B,hq,hkv,dim,block,window,together", [
+    (64, 32, 8, 128, 128, 0, True), (64, 32, 8, 128, 128, 500, False), (64, 32, 8, 128, 128, 4096, True),
+    (32, 16, 8, 256, 64, 0, True), (32, 16, 8, 256, 64, 500, False), (32, 16, 8, 256, 64, 2048, True),
+    (64, 64, 8, 64, 64, 0, True), (64, 64, 8, 64, 64, 1024, False), (64, 64, 8, 64, 64, 8192, True),
+])
+def test_attn_shared_is_cut_by_what_a_window_leaves(B, hq, hkv, dim, block, window, together):
+    """Behind 16384 tokens: requests that see few of them go the attention's way, and parts are for the tiles that are seen."""
+    import ctypes
+    from gemm_w4_gemv_amd import step
+    cache = types.SimpleNamespace(ref=ctypes.byref(step._CacheStruct(1, 1, 1, 1, 100000, block, hkv, dim)))
+    size = lambda window, own=100: w4.w4_kv4_attn_shared_workspace_bytes(cache, B, B, hq, 1, 16384 + own, 16384, window)  # noqa: E731
+    alone = w4.w4_kv4_attn_workspace_bytes(cache, B, B, hq, 1, 16484, window)
+    assert (size(window) != alone) == together
+    if window and together:
+        assert size(window) <= size(0)
+        # whose own tokens fill the window see nothing of the prefix
+        assert size(window, window + 5) == w4.w4_kv4_attn_workspace_bytes(cache, B, B, hq, 1, 16384 + window + 5, window)
