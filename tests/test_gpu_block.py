@@ -710,3 +710,46 @@ def test_graphs_that_share_a_workspace():
         assert out[1][0].tolist() == list(want[0]) and np.array_equal(out[1][1].cpu().numpy(), want[1])
     for graph in graphs:
         graph.destroy()
+
+
+# ------------------------------------------------- rows past the caches' keeping
+# From 2^22 values of all choices on (block.hpp) rows go past the caches: kernels of their own.
+@pytest.mark.parametrize("T,top,E,capacity,D,R,bad", [
+    (1100, 6, 64, 0, 1024, None, 0.0), (1100, 6, 64, 90, 1024, 5000, 0.1), (600, 6, 16, 0, 1200, None, 0.05),  # by every workgroup
+    (200, 64, 256, 0, 336, 12000, 0.0), (9000, 8, 512, 130, 64, None, 0.02),  # a table summed once
+])
+def test_moe_sort_of_many_values(T, top, E, capacity, D, R, bad):
+    assert T * top * D >= 1 << 22
+    check_sort(routed(81, T, top, E, bad), E, capacity, D, R, pad=8)
+
+
+MANY_VALUES = [(1100, 8, 8900, 512), (950, 9, 8600, 504), (700, 6, 4200, 1024), (350, 6, 2200, 2048), (100, 12, 1300, 4104), (30, 64, 1920, 2304)]
+
+
+@pytest.mark.parametrize("T,top,R,N", MANY_VALUES)
+@pytest.mark.parametrize("weighted,added", [(True, True), (False, False)])
+def test_moe_combine_of_many_values(T, top, R, N, weighted, added):
+    assert T * top * N >= 1 << 22
+    test_moe_combine(T, top, R, N, weighted, added)
+
+
+@pytest.mark.parametrize("T,top,R,N", MANY_VALUES)
+def test_moe_combine_grad_of_many_values(T, top, R, N):
+    assert T * top * N >= 1 << 22
+    test_moe_combine_grad(T, top, R, N, True)
+
+
+@pytest.mark.parametrize("kind", [bf16, f32])
+@pytest.mark.parametrize("D", [64, 512, 520, 1024, 1032, 2048, 2056, 4096, 4104, 8192, 8200, 12288, 12296, 16384])
+def test_block_norm_of_many_values(D, kind):
+    """From 2^19 values on both outputs go past the caches; over their inputs too."""
+    T = (1 << 19) // D + 3
+    v = norm_case(82, T, D, kind, "token" if D % 16 else "channel", True, True)
+    x, z, ex, ez = norm_bounds(v, 0.75, 0.22, 1e-6, 1.0)
+    ho, zo = run_norm(v, 0.75, 0.22, add=1.0)
+    close(ho, x, ex + ROUND[kind] * np.abs(x), "h_out")
+    close(zo, z, ez, "z")
+    w4.w4_block_norm(v["h"], v["y"], h_out=v["h"], z=v["y"], y_weight=v["y_weight"], z_weight=v["z_weight"], gate=v["gate"],
+                     residual_scale=0.75, branch_scale=0.22, weight_add=1.0)
+    torch.cuda.synchronize()
+    assert torch.equal(v["h"], ho) and torch.equal(v["y"], zo)
