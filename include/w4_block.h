@@ -70,6 +70,10 @@ W4_API w4_status w4_block_norm(const w4_norm_args* args, void* stream);
  *   d_gate     = branch_scale * dH * u, summed over t if the gate is shared
  * h' is computed again from h and y, which must hold what they held before the
  * call of w4_block_norm.
+ * Means over a row as in w4_block_norm.  A sum over t is FP32 over a run of rows,
+ * one after the other, FP64 over the runs: at most ceil(T / 256) rows, so up to
+ * 8192 where T is 2^21 (a half, a quarter and an eighth of that for D up to 2048, 1024
+ * and 512, whose runs are shared by teams).
  *   args          as for w4_block_norm; h_out and z are not used
  *   dh_out        device, h's type [T][D], or NULL for 0
  *   dz            device bf16 [T][D], or NULL for 0; one of the two is given

@@ -753,3 +753,24 @@ def test_block_norm_of_many_values(D, kind):
                      residual_scale=0.75, branch_scale=0.22, weight_add=1.0)
     torch.cuda.synchronize()
     assert torch.equal(v["h"], ho) and torch.equal(v["y"], zo)
+
+
+@pytest.mark.parametrize("T,D,kind,teams", [(1 << 21, 8, bf16, 8), (150000, 136, f32, 8), (30000, 520, bf16, 4), (20000, 1032, f32, 2),
+                                            (10000, 2056, f32, 1), (10000, 2056, bf16, 1)])
+def test_block_norm_grad_sums_over_long_runs(T, D, kind, teams):
+    """Sums over t of many rows.  A run is at most ceil(T / 256) of them, in turn over its teams: a lane's FP32 sum
+    takes that part of them one after the other, each off by 2^-24 of the magnitudes so far, the teams' join three more
+    roundings, which K has room for; FP64 joins the runs.  The terms are off as in ``grad_bounds``."""
+    v = norm_case(83, T, D, kind, None, True, True)
+    dho, dz = tensor(84, (T, D), 0.3, kind), tensor(85, (T, D))
+    got = run_grad(v, dho, dz, 0.9, 0.5)
+    want, bound = grad_bounds(v, dho, dz, 0.9, 0.5, 1e-6, 0.0, kind)
+    h, y, wz = (f64(v[n]) for n in ("h", "y", "z_weight"))
+    x, _ = ref.block_norm(h, y, f64(v["y_weight"]), wz, None, 0.9, 0.5, 1e-6, 0.0)
+    r, n1 = ref.rms(x, 1e-6), y / ref.rms(y, 1e-6)
+    n2, g = x / r, f64(dz) * wz
+    dx = f64(dho) + (g - n2 * (g * n2).mean(-1, keepdims=True)) / r
+    more = -(-(-(-T // 256)) // teams) * 2.0 ** -24
+    bound["d_z_weight"] = bound["d_z_weight"] + more * np.abs(f64(dz) * n2).sum(0)
+    bound["d_y_weight"] = bound["d_y_weight"] + more * np.abs(0.5 * dx * n1).sum(0)
+    check_grad(got, want, bound)
