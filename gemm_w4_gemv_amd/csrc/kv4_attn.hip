@@ -1573,7 +1573,7 @@ template <int D>
 __global__ __launch_bounds__(kThreads) void kv4_attn_shared_join_kernel(AttnArgs a, const float* own_o, const float* own_ml,
                                                                         int own_splits) {
     constexpr int kWaves = kThreads / kWave, kFirst = 8, kJ = D == 64 ? 4 : 8, kPieces = Rows<D, 1>::kPieces;
-    __shared__ float sm[2 * kMaxSplits][16], sl[2 * kMaxSplits][16], sums[kWaves][16];
+    __shared__ float sm[kMaxSplits][16], sl[kMaxSplits][16], sums[kWaves][16];  // sm, sl: the prefix's
     __shared__ f32x4_t part[kWaves][kWave];
     __shared__ int row_in[16];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = (int)sgpr(tid / kWave);
