@@ -29,7 +29,7 @@ constexpr int kAlone = 4096;  // choices that every workgroup counts itself
 // experts, 256 (16384) 191 and 50.
 constexpr int kTable = 4096;
 constexpr int kLongChunk = 1024, kChunk = 256;
-constexpr int kMaxChunks = 2048, kMaxCounts = 1 << 22;  // of a table summed once, at most
+constexpr int kMaxChunks = 2048;  // of a table summed once, at most (2^21 counts)
 constexpr int kScanExperts = 16;  // of a workgroup that sums over the chunks
 
 struct SortArgs {
@@ -196,9 +196,8 @@ SortArgs cut_of(int T, int top, int E) {
     // 16 choices a workgroup: 8191 tokens of 6 choices, rows of 4096: 74 us, of 64 80, of 6 74
     k.per = k.n <= kAlone || top > kOwn / 4 ? 1 : kOwn / 4 / top;
     if (k.n > kAlone) {
-        const int most = kMaxCounts / E < kMaxChunks ? kMaxCounts / E : kMaxChunks;
         k.summed = (int64_t)((k.n + kLongChunk - 1) / kLongChunk) * E > kTable;
-        k.chunk = k.summed ? (k.n + most - 1) / most : kLongChunk;
+        k.chunk = k.summed ? (k.n + kMaxChunks - 1) / kMaxChunks : kLongChunk;
         if (k.chunk < kChunk) k.chunk = kChunk;
         k.chunks = (k.n + k.chunk - 1) / k.chunk;
     }
