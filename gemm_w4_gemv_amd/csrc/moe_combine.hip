@@ -113,10 +113,6 @@ __global__ __launch_bounds__(kWaves* kWave) void moe_combine_grad_kernel(w4_moe_
     }
 }
 
-}  // namespace
-
-namespace {
-
 // f(apart): whether the choices' rows, of N values, go past the caches.
 template <typename F>
 hipError_t with_apart(int64_t choices, int N, F f) {
