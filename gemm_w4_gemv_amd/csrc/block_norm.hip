@@ -266,13 +266,16 @@ __global__ __launch_bounds__(kWaves* teams<kWaves>() * kWave) void block_norm_ke
 //   first   sum h'^2 and sum g2 h'   (g2 = dz w2: mean(g2 n2) = r2 mean(g2 h'))
 //   second  sum g1 n1 of this row, sum y^2 of the next
 //
-// Measured, all gradients, an FP32 stream: 8192 rows of 4096 137 us, 4.4 TB/s, and no
+// Measured, all gradients, an FP32 stream: 8192 rows of 4096 138 us, 4.4 TB/s, and no
 // less with a tenth of the instructions taken out or with two workgroups a compute
 // unit: memory bounds it, four arrays read and two written at once.
 // Rows past 8192 (kLong) would fill the registers: their sums over the rows lie in
 // LDS, weights are read row by row and no row is ahead (4 chunks of eight
-// waves: 2048 rows of 16384 275 us, 2 chunks of sixteen 328, with all in registers, most
-// of which the compiler then moves to memory, 1250; 2730 of 12288 183, 329 and 1217).
+// waves, some 100 of whose registers the compiler moves to memory: 2048 rows of 16384 270 us,
+// 2 chunks of sixteen 328, with all in registers, most of which it then moves, 1250; 2730 of
+// 12288, none moved, 184, 329 and 1217).
+// Few rows are two launches' latency: 512 rows of 2048, 16 us, 9 of them this kernel's (first
+// loads, two rows and their barriers, the teams' sums) and 7 the runs'.
 //
 // Sums over the rows are taken in three steps, none of whose order is left to
 // chance: a lane adds its columns row by row, the teams join in LDS, and a second
@@ -555,12 +558,17 @@ __global__ __launch_bounds__(kRunWaves * kWave) void block_norm_runs_kernel(Grad
 // Whether four waves take a row of 2049 to 4096 values and two workgroups share a compute
 // unit, each at its own row, in place of eight waves a row and one workgroup: a barrier
 // then stops half of the unit.  Twice the runs are twice the sums to join.  All
-// gradients, rows of 4096, two workgroups first: 8192 rows with a BF16 stream 102 us and
-// 118 (3.9 TB/s), with an FP32 one, more of it memory, 139 and 138; 512 rows of 2048 in
-// as many runs 24 and 17.
+// gradients, a BF16 stream, us with two workgroups and with one: rows of 4096, 2048 of
+// them 39 and 36, 4096 54 and 54, 6000 70 and 73, 8192 97 and 110; rows of 2056, 2048 33 and
+// 31, 4096 45 and 48, 8192 69 and 82.  Rows of up to 2048 have teams of four waves in a
+// workgroup of eight: of 2048, 4096 40 and 35, 16384 113 and 112.  An FP32 stream, more
+// of it memory, 8192 rows of 4096 139 and 138.
 bool two_groups(int T, int D, bool f32) { return !f32 && T >= 4096 && D > 2048 && D <= 4096; }
 // Each team has a row at least, a sum more to join costs more than a second row: 256 rows
 // of 1024, four teams a workgroup, 64 runs 10.7 us, 128 11.4, 256 14.4; 512 rows 12.6, 12.0, 14.3.
+// Then as many as workgroups are on the chip: 128, 256 and 512 runs of 2048 rows of 4096 48,
+// 36 and 44 us, of 32768 of 1024 175, 107 and 117, of 8192 of 512 27, 22 and 30, of 2048 of
+// 16384 316, 221 and 256; with two workgroups a unit 256 and 512 of 8192 rows of 4096 131 and 98.
 int runs_of(int T, int D, bool f32) {
     const int most = two_groups(T, D, f32) ? kMaxRuns : kMaxRuns / 2;
     const int teams = D <= 512 ? 8 : D <= 1024 ? 4 : D <= 2048 ? 2 : 1;

@@ -1541,11 +1541,12 @@ constexpr int kThreads = 256;
 // bound by arithmetic, the second by memory, and a compute unit that holds a
 // workgroup of each has both at work.
 // Measured with the join: 64 requests behind 16384 tokens, 32 and 8 heads of 128: 60 us,
-// 300 TFLOP/s of the prefix's two products; 32 behind 8192, 16 and 8 heads of 256: 33 us.
-// Of the first 52 are this kernel's, whose vector instructions (some 200 a wave's tile, beside 26
-// products and 20 reads of LDS) keep their unit busy 63 cycles of 100 and whose products
-// the matrix unit 29.  Three workgroups a compute unit (24 splits) take 67 us; the next
-// tile's scores beside this one's weights, which wants a third buffer and 210 registers, 80.
+// 300 TFLOP/s of the prefix's two products; 32 behind 8192, 16 and 8 heads of 256: 34 us.
+// Without the join's launch 53 and 26: this kernel, whose vector instructions (some 200 a
+// wave's tile, beside 26 products and 20 reads of LDS) keep their unit busy 63 cycles of 100
+// in the first and whose products the matrix unit 29.  Three workgroups a compute unit
+// (24 splits) take 67 us; the next tile's scores beside this one's weights, which wants a
+// third buffer and 210 registers, 80.
 template <int D, bool kWide, int kSets>
 __global__ __launch_bounds__(kThreads, 2) void kv4_attn_shared_kernel(AttnArgs shared, AttnArgs own, int shared_units) {
     typedef ManyLds<D, 1, true> Many;
@@ -1730,18 +1731,18 @@ Cut cut_of(const w4_attn_args& a, const w4_kv4_cache& c) {
     // share them: it pays where nearly every compute unit has two workgroups (heads
     // of 64, whose tiles are the least work, four), for then the shortest can go with
     // the longest.  us of both kernels, shared tiles first, prompts with nothing
-    // before them unless said: heads of 256, 256 workgroups 104 and 78 (1024 tokens
-    // after 1024), 448 198 and 198 (1792 after 2048), 512 204 and 225 (2048 after
-    // 2048) and 22 and 42 (eight prompts of 250), 1024 155 and 185 (two of 2048); heads
-    // of 128, 384 196 and 152 (1536 after 2048), 464 53 and 55 (two of 912), 576 26
-    // and 47 (nine of 250), 1008 156 and 171 (two of 2000); heads of 64, 512 49 and
-    // 40 (1024 tokens), 1024 59 and 77 (four of 1000), 2048 106 and 142 (eight).
-    // One prompt of heads of 128, whose workgroups differ most: 456 96 and 78 (1824),
-    // 576 303 and 248 (2304 after 2048), 1024 302 and 295 (4096), 531 and 538 (4096
+    // before them unless said: heads of 256, 256 workgroups 99 and 70 (1024 tokens
+    // after 1024), 448 194 and 186 (1792 after 2048), 512 205 and 220 (2048 after
+    // 2048) and 24 and 42 (eight prompts of 250), 1024 151 and 181 (two of 2048); heads
+    // of 128, 384 180 and 144 (1536 after 2048), 464 50 and 55 (two of 912), 576 26
+    // and 47 (nine of 250), 1008 144 and 162 (two of 2000); heads of 64, 512 45 and
+    // 40 (1024 tokens), 1024 58 and 74 (four of 1000), 2048 94 and 136 (eight).
+    // One prompt of heads of 128, whose workgroups differ most: 456 92 and 76 (1824),
+    // 576 308 and 234 (2304 after 2048), 1024 281 and 277 (4096), 502 and 505 (4096
     // after 2048).  A few workgroups past 512 run on their own when the first end,
-    // which counts where each has far to go: 576 180 and 164 (two of 1152 after 1000,
-    // heads of 256), 323 and 260 (2304 after 2048), 128 and 108 at 640 (16 of 144 after
-    // 1000, heads of 128), but 72 and 85 (two of 1152), and 768 155 and 176 (four of
+    // which counts where each has far to go: 576 167 and 144 (two of 1152 after 1000,
+    // heads of 256), 316 and 254 (2304 after 2048), 119 and 100 at 640 (16 of 144 after
+    // 1000, heads of 128), but 64 and 74 (two of 1152), and 768 168 and 172 (four of
     // 768 after 1000).
     const int64_t many_rows = 64 * many_blocks(c.head_dim);
     const int64_t shared = (int64_t)a.B * c.kv_heads * ((rows + many_rows - 1) / many_rows);

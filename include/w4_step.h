@@ -223,8 +223,10 @@ W4_API w4_status w4_kv4_attn(const w4_attn_args* args, const w4_kv4_cache* cache
  *   workspace     at least w4_kv4_attn_shared_workspace_bytes() bytes for the
  *                 same arguments, else as for w4_kv4_attn
  * It pays where the rows of a key/value head, over all requests, far outnumber
- * those of one; few requests or a short prefix go w4_kv4_attn's way.  Requests
- * behind different prefixes are calls of their own.
+ * those of one.  Few requests, a short prefix, a window that leaves little of it (by
+ * max_kv, which says how far the longest request goes on behind it), and all of a call
+ * where max_q makes more than 64 rows of a key/value head go w4_kv4_attn's way: a
+ * prompt's chunk is a call of its own.  Requests behind different prefixes too.
  * Errors: as w4_kv4_attn; W4_ERR_SHAPE for a negative prefix.
  */
 W4_API size_t w4_kv4_attn_shared_workspace_bytes(const w4_attn_args* args, int prefix, const w4_kv4_cache* cache);
