@@ -1916,18 +1916,13 @@ SharedCut shared_cut_of(const w4_attn_args& a, int prefix, const w4_kv4_cache& c
     }
     const int64_t units = B * own_row_tiles * c.kv_heads * seen, each = (rows + B - 1) / B;
     if (a.T < 2 || own_rows > 64 || rows * c.kv_heads > (1 << 22) || units <= (each < 8 ? each : 8) * least) return k;
-    const int64_t own_groups = B * c.kv_heads * own_row_tiles, groups = c.kv_heads * ((rows + 63) / 64);
+    const int64_t row_tiles = (rows + 63) / 64;
+    const int64_t own_groups = B * c.kv_heads * own_row_tiles, groups = c.kv_heads * row_tiles;
     if (own_groups > (1 << 20)) return k;
-    k.tiles = (int)tiles;
-    k.row_tiles = (int)((rows + 63) / 64);
-    k.blocks = (int)((rows + 15) / 16);
-    k.sets = own_rows > 8 ? 1 : own_rows > 4 || c.head_dim == 256 ? 2 : 4;
-    k.own_row_tiles = (int)own_row_tiles;
     const auto bounded = [](int64_t x, int64_t most) {
         x = x < most ? x : most;
         return (int)(x < 1 ? 1 : x < kMaxSplits ? x : kMaxSplits);
     };
-    k.own_splits = bounded(own_tokens / (32 * kTile), 1024 / own_groups);
     // The prefix: two workgroups a compute unit (four with heads of 64, of half the
     // registers), each with eight tiles or more; short prefixes up to 16 of four.  A
     // part more is a write and a read of its rows.  32 requests behind 8192 tokens, 16 and
@@ -1935,7 +1930,30 @@ SharedCut shared_cut_of(const w4_attn_args& a, int prefix, const w4_kv4_cache& c
     // heads of 128: 12 70 us, 16 60, 20 64; 64 of 1024, 16 and 8 heads of 256: 4 23.8, 8 22.1, 16
     // 26.8; 64 of 8192, 64 and 8 heads of 64: 8 48, 12 43.4, 16 40.6, 20 46.
     const int64_t few = reach / 4 < 16 ? reach / 4 : 16;
-    k.splits = bounded((c.head_dim == 64 ? 1024 : 512) / groups, few > reach / 8 ? few : reach / 8);
+    const int splits = bounded((c.head_dim == 64 ? 1024 : 512) / groups, few > reach / 8 ? few : reach / 8);
+    // And the chip's waves have to get fewer tiles by it.  Request by request 2048 of them
+    // share the units; together each passes over its split's tiles, 64 rows at a time
+    // however few there are.  (Four workgroups a compute unit take twice as long for it, with
+    // heads of 64; with heads of 256 half of a tile is unpacking, which a workgroup does
+    // once.)  us request by request, then together, by the one over the other: heads of
+    // 128, 0.25 (a request of 3 rows behind 131072 tokens, 32 and 8 heads) 40 and 103, 0.75 (3 of one
+    // row) 74 and 104, 1 (4, 8 and 8 heads) 93 and 104, 1 (8 of 4 rows, 64 and 4 heads) 307 and 341, 1.5 (6,
+    // 8 and 8 heads) 120 and 103; heads of 256, 0.25 (one of 3 rows, 16 and 8 heads) 58 and 134, 0.5 (2) 108
+    // and 134, 0.75 (3) 145 and 134, behind 16384 27 and 37, 1 (4) 185 and 134, 37 and 37; heads of 64,
+    // 1.5 (3, 64 and 8 heads) 50 and 71, 2 (4) 62 and 63, 3 (6) 83 and 70.  Up to 130 tiles the first
+    // loads of a workgroup count for more than its tiles; there the requests' row tiles decide,
+    // where the prefix is split: 8 requests of one row behind 4096 tokens, 8 and 8 heads of 128, 14.6
+    // and 18.7, 12 17.7 and 18.7, 16 22.3 and 16.4; 48 of 8 rows behind 1024, 32 and 8 heads, in two splits 23
+    // and 44.
+    const int64_t fair = c.head_dim == 64 ? 4096 : c.head_dim == 128 ? 2048 : 1600, own_tiles = B * own_row_tiles;
+    if (units * splits <= fair * reach && (tiles > 130 || splits < 4 || own_tiles < 9 || own_tiles < 4 * row_tiles)) return k;
+    k.splits = splits;
+    k.tiles = (int)tiles;
+    k.row_tiles = (int)row_tiles;
+    k.blocks = (int)((rows + 15) / 16);
+    k.sets = own_rows > 8 ? 1 : own_rows > 4 || c.head_dim == 256 ? 2 : 4;
+    k.own_row_tiles = (int)own_row_tiles;
+    k.own_splits = bounded(own_tokens / (32 * kTile), 1024 / own_groups);
     return k;
 }
 

@@ -182,3 +182,19 @@ def test_attn_shared_is_cut_by_what_a_window_leaves(B, hq, hkv, dim, block, wind
         assert size(window) <= size(0)
         # whose own tokens fill the window see nothing of the prefix
         assert size(window, window + 5) == w4.w4_kv4_attn_workspace_bytes(cache, B, B, hq, 1, 16384 + window + 5, window)
+
+
+@pytest.mark.parametrize("B,new,hq,hkv,dim,prefix,together", [
+    (1, 2, 32, 8, 128, 131072, False), (1, 8, 8, 8, 128, 131072, False), (2, 1, 32, 8, 128, 131072, False), (3, 1, 8, 8, 128, 32768, False),
+    (8, 4, 64, 4, 128, 131072, False), (8, 1, 8, 1, 128, 131072, False), (6, 1, 8, 8, 128, 131072, True), (8, 1, 32, 8, 128, 32768, True),
+    (1, 3, 16, 8, 256, 131072, False), (2, 1, 16, 8, 256, 65536, False), (4, 1, 16, 8, 256, 131072, True), (8, 1, 16, 8, 256, 16384, True),
+    (1, 8, 64, 8, 64, 131072, False), (3, 1, 64, 8, 64, 131072, False), (8, 2, 64, 8, 64, 131072, False), (8, 1, 64, 8, 64, 131072, True),
+    (8, 1, 8, 8, 128, 4096, False), (16, 1, 8, 8, 128, 4096, True), (48, 8, 32, 8, 128, 1024, False),
+])
+def test_attn_shared_is_together_where_that_takes_tiles_off_the_waves(B, new, hq, hkv, dim, prefix, together):
+    """One request behind a long prefix, or few, share nothing that pays; nor do rows that fill their tiles already."""
+    import ctypes
+    from gemm_w4_gemv_amd import step
+    cache = types.SimpleNamespace(ref=ctypes.byref(step._CacheStruct(1, 1, 1, 1, 100000, 128, hkv, dim)))
+    args = (cache, B * new, B, hq, new, prefix + 100)
+    assert (w4.w4_kv4_attn_shared_workspace_bytes(*args, prefix) != w4.w4_kv4_attn_workspace_bytes(*args)) == together
