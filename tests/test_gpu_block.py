@@ -774,3 +774,57 @@ def test_block_norm_grad_sums_over_long_runs(T, D, kind, teams):
     bound["d_z_weight"] = bound["d_z_weight"] + more * np.abs(f64(dz) * n2).sum(0)
     bound["d_y_weight"] = bound["d_y_weight"] + more * np.abs(0.5 * dx * n1).sum(0)
     check_grad(got, want, bound)
+
+
+# ------------------------------------------------------------ rows far apart
+def far_rows(t):
+    """The same rows 2^31 + 8 values apart: offsets past 32 bits from the third on, bytes from the second."""
+    step = (1 << 31) + 8
+    space = torch.empty((len(t) - 1) * step + t.shape[1], dtype=t.dtype, device=DEV)
+    out = torch.as_strided(space, t.shape, (step, 1))
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("kind", [bf16, f32])
+def test_rows_far_apart(kind):
+    """Each operator on rows whose offsets pass 32 bits: the bits of rows that lie together."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 160 << 30:
+        pytest.skip("less than 160 GiB of memory is free")
+    T, D = 3, 520
+    v = norm_case(86, T, D, kind, "token", True, True)
+    want = run_norm(v)
+    f = {n: far_rows(t) if t.dim() == 2 else t for n, t in v.items()}
+    ho, z = far_rows(torch.full_like(v["h"], 7.0)), far_rows(torch.full_like(v["y"], 7.0))
+    w4.w4_block_norm(f["h"], f["y"], h_out=ho, z=z, y_weight=v["y_weight"], z_weight=v["z_weight"], gate=f["gate"])
+    assert torch.equal(ho, want[0]) and torch.equal(z, want[1])
+    dho, dz = tensor(87, (T, D), 0.3, kind), tensor(88, (T, D))
+    want = run_grad(v, dho, dz)
+    ho.copy_(dho)
+    z.copy_(dz)
+    dgate = far_rows(torch.full_like(v["gate"], 7.0))
+    w4.w4_block_norm_grad(f["h"], f["y"], dh_out=ho, dz=z, dh=ho, dy=z, y_weight=v["y_weight"], z_weight=v["z_weight"],
+                          gate=f["gate"], d_gate=dgate)
+    assert torch.equal(ho, want["dh"]) and torch.equal(z, want["dy"]) and torch.equal(dgate, want["d_gate"])
+    del f, ho, dgate
+    if kind is f32:
+        return
+    ids = ints([[1, 0], [1, 1], [0, 2]])
+    start, row_of = torch.zeros(4, dtype=torch.int32, device=DEV), torch.zeros(T, 2, dtype=torch.int32, device=DEV)
+    x = tensor(89, (T, D))
+    z.copy_(x)
+    rows = far_rows(torch.full((6, D), 7.0, dtype=bf16, device=DEV))
+    w4.w4_moe_sort(ids, 3, start, row_of, x=z, rows=rows)
+    assert row_of.tolist() == [[2, 0], [3, 4], [1, 5]]
+    assert torch.equal(rows, x[[0, 2, 0, 1, 1, 2]])
+    w, out = torch.rand(T, 2, device=DEV), torch.zeros(T, D, dtype=bf16, device=DEV)
+    w4.w4_moe_combine(x[[0, 2, 0, 1, 1, 2]], out, row_of=row_of, weights=w, add=x)
+    w4.w4_moe_combine(rows, z, row_of=row_of, weights=w, add=z)
+    assert torch.equal(z, out)
+    dy, dw = torch.zeros(6, D, dtype=bf16, device=DEV), torch.zeros_like(w)
+    w4.w4_moe_combine_grad(out, x[[0, 2, 0, 1, 1, 2]], row_of=row_of, weights=w, dy=dy, dweights=dw)
+    far_w = torch.zeros_like(w)
+    w4.w4_moe_combine_grad(z, rows, row_of=row_of, weights=w, dy=rows, dweights=far_w)
+    torch.cuda.synchronize()
+    assert torch.equal(rows, dy) and torch.equal(far_w, dw)

@@ -313,3 +313,32 @@ def test_attn_shared_window_over_a_part_of_a_long_prefix(prefix, lens, news, hq,
     cache, shared, table, q_start, q = case(12, prefix, lens, news, hq, hkv, dim, block)
     got = run(to_device(cache), q, table, lens, q_start, shared, prefix, window=window, sinks=sinks)
     check_attn(got, *expect(cache, q, table, lens, q_start, dim, window, sinks))
+
+
+def test_attn_shared_cache_and_rows_past_32_bit_offsets():
+    """Shared and own pages whose bytes lie past 2^32, queries and outputs 2^31 values apart."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 120 << 30:
+        pytest.skip("less than 120 GiB of memory is free")
+    hq, hkv, dim, block, prefix = 8, 8, 128, 256, 4096
+    shared = prefix // block
+    lens = [prefix + 1 + 7 * i for i in range(12)]
+    assert apart(prefix, lens, [1] * 12, hq, hkv, dim, block)
+    small = random_cache(13, shared + 12, block, hkv, dim)
+    blocks = (5 << 30) // (hkv * block * dim // 2)
+    far = w4.Kv4Cache.empty(blocks, block, hkv, dim)
+    pages = blocks - 1 - si.rng(13, 99).permutation(shared + 12)
+    for name in ("k_codes", "k_meta", "v_codes", "v_meta"):
+        getattr(far, name)[torch.from_numpy(pages).to(DEV)] = torch.from_numpy(getattr(small, name)).to(DEV)
+    q = si.bf16_normal(13, (100,), (12, hq, dim))
+    step = (1 << 31) + 8
+    space = [torch.empty(11 * step + hq * dim, dtype=bf16, device=DEV) for _ in range(2)]
+    far_q, out = (torch.as_strided(s, (12, hq, dim), (step, dim, 1)) for s in space)
+    far_q.copy_(host.bf16_tensor(q))
+    own = np.concatenate((np.tile(np.arange(shared), (12, 1)), np.arange(shared, shared + 12)[:, None]), axis=1)
+    size = w4.w4_kv4_attn_shared_workspace_bytes(far, 12, 12, hq, 1, max(lens), prefix)
+    work = torch.full((size // 4,), float("nan"), dtype=torch.float32, device=DEV)
+    w4.w4_kv4_attn_shared(far_q, far, ints(pages[own]), ints(lens), out, ints(pages[:shared]), prefix, max_kv=max(lens),
+                          workspace=work)
+    torch.cuda.synchronize()
+    check_attn(host.bf16_values(out.contiguous()), *expect(small, q, own, lens, range(13), dim))
